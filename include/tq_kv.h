@@ -81,7 +81,8 @@ enum {
     TQ_ERR_MISALIGNED = -5        /* a device pointer is not 16-byte aligned */
 };
 
-enum { TQ_DTYPE_F32 = 0, TQ_DTYPE_BF16 = 1 };
+/* TQ_DTYPE_F16: the 8-bit cache and prompt attention calls only. */
+enum { TQ_DTYPE_F32 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F16 = 2 };
 /*
  * Decode output flag, OR-ed into out_dtype: with MSE-quantised values, return
  * the attention output in the rotated space, R out = sum_t p_t n16_t c_v[idx_t],
@@ -400,6 +401,114 @@ tq_status tq_decode_attention_noalloc(const tq_cache* cache, const void* q, int 
                                       const int32_t* block_table, const int32_t* seq_lens, const void* tail_k,
                                       const void* tail_v, const int32_t* tail_lens, float scale, int batch,
                                       void* out, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache: for the layers (or models) whose keys and values are kept
+ * at 8 bits instead of TurboQuant's 2 to 4.  The pages have no counterpart.
+ *
+ * Same paging as the compressed cache: [num_blocks][num_kv_heads][page_bytes],
+ * a page holding 16 tokens of one KV head:
+ *   K codes   16 x d   e4m3
+ *   V codes   16 x d   e4m3
+ *   K scales  16 x u8  exponent byte E: the vector's scale is 2^(E - 127)
+ *   V scales  16 x u8  (E = 255: the vector is NaN)
+ * page_bytes = 32 d + 32.  A stored element stands for code * 2^(E - 127).
+ * The scale is a power of two, so that scaling is exact and a stored element
+ * carries one rounding, that to e4m3 (4 significant bits, ties to even).
+ * ------------------------------------------------------------------------ */
+typedef struct tq_f8_config {
+    int32_t head_dim;           /* d, 128 or 256 */
+    int32_t num_kv_heads;       /* H_kv >= 1 */
+    int32_t num_q_heads;        /* H_q = G * H_kv, any G >= 1; q head h reads KV head h / G */
+    int32_t block_size;         /* tokens per cache block; must be 16 */
+    int64_t num_blocks;         /* blocks in the cache pool */
+    int32_t max_batch;          /* sequences per load or decode call */
+    int32_t max_blocks_per_seq; /* columns of the block table */
+} tq_f8_config;
+
+typedef struct tq_f8_cache tq_f8_cache;
+
+/* Sizes, in bytes, of the caller-owned device buffers; any pointer may be NULL. */
+tq_status tq_f8_cache_sizes(const tq_f8_config* cfg, size_t* page_bytes, size_t* cache_bytes,
+                            size_t* workspace_bytes);
+
+/*
+ * Make a handle that records workspace_dev (>= workspace_bytes, 16-byte
+ * aligned; split partials, their counters and the device error word).  Zeroes
+ * the counters and the error word and synchronises `stream` once (set-up
+ * only).  As with tq_cache_create, one handle = one workspace: calls (and
+ * captured graphs) of one handle must not overlap on the GPU.
+ */
+tq_status tq_f8_cache_create(const tq_f8_config* cfg, void* workspace_dev, void* stream, tq_f8_cache** out);
+tq_status tq_f8_cache_destroy(tq_f8_cache* cache);
+
+/*
+ * Quantise new vectors into the 8-bit cache.  For every token t with
+ * slot_mapping[t] >= 0, every KV head and both k and v:
+ *   a = max_i |x_i|;  e = the smallest integer with a <= 448 * 2^e, at least
+ *   -126;  codes = e4m3(x * 2^-e);  E = e + 127.
+ * A vector with an infinity or a NaN is stored as E = 255 with zero codes.
+ *   k, v          device [num_tokens][num_kv_heads][d], in_dtype (F32, BF16 or
+ *                 F16), token t starting k_stride (v_stride) elements after
+ *                 token t - 1: H_kv * d if packed, more for rows of a fused
+ *                 projection.  Base and stride: multiples of 16 bytes
+ *                 (else TQ_ERR_MISALIGNED).
+ *   slot_mapping  device int64 [num_tokens]: block * 16 + row; -1 skips the
+ *                 token; any other slot outside [0, 16 * num_blocks) also skips
+ *                 it and sets TQ_DEVERR_SLOT.  The slots of one call must
+ *                 differ: of two vectors sent to one slot, which bytes stay is
+ *                 unspecified.
+ * num_tokens == 0 is a no-op.  Slots no token names are left as they were.
+ */
+tq_status tq_f8_store(const tq_f8_cache* cache, const void* k, const void* v, int in_dtype, int64_t k_stride,
+                      int64_t v_stride, int64_t num_tokens, const int64_t* slot_mapping, void* cache_buf,
+                      void* stream);
+
+/*
+ * Read sequences of the 8-bit cache back into packed rows, for attention over
+ * a stored prefix (tq_prompt_attention) or a conversion to another cache:
+ *   k_out[cu_out[b] + t], v_out[cu_out[b] + t] = the stored vectors of token t
+ *   of sequence b, t < seq_lens[b], rounded once to out_dtype (e4m3 times a
+ *   power of two: exact unless it leaves out_dtype's range).
+ *   block_table  device int32 [batch][max_blocks_per_seq]
+ *   seq_lens     device int32 [batch], 0..16*max_blocks_per_seq (otherwise
+ *                clamped, TQ_DEVERR_SEQLEN)
+ *   cu_out       device int32 [batch] (or more), first row of each sequence;
+ *                rows outside [0, n_rows) are not written and set
+ *                TQ_DEVERR_CHUNK
+ *   k_out/v_out  device [n_rows][num_kv_heads][d], out_dtype, 16-byte aligned
+ * Rows no sequence names, and the rows of a block id outside [0, num_blocks)
+ * (TQ_DEVERR_BLOCK), are left as they were.
+ */
+tq_status tq_f8_load(const tq_f8_cache* cache, const void* cache_buf, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* cu_out, int batch, int64_t n_rows, void* k_out,
+                     void* v_out, int out_dtype, void* stream);
+
+/*
+ * Decode attention over the 8-bit cache: one new query per sequence.
+ *   out[b][h] = sum_t softmax_t(scale <q, k_t>) v_t, t < seq_lens[b], with
+ *   k_t, v_t the stored vectors; 0 where the sequence has no token.
+ *   q        device [batch][H_q][d], q_dtype (F32, BF16, F16); row b starts
+ *            q_stride elements after row b - 1; base and stride multiples of
+ *            16 bytes
+ *   out      device [batch][H_q][d], out_dtype (F32, BF16, F16)
+ *   block_table, seq_lens as for tq_f8_load; a block id outside
+ *            [0, num_blocks) is skipped (TQ_DEVERR_BLOCK)
+ *   scale    softmax scale; <= 0 means 1/sqrt(d)
+ * The products run on 16-bit operands that hold the codes exactly.  With
+ * 16-bit q and out the probabilities are rounded to fp16 once; where q or out
+ * is F32 both q and the probabilities go in as two fp16 parts (~22 bits).
+ * A query with an infinity or a NaN gets NaN.  1 <= batch <= max_batch.  One
+ * launch of a fixed grid: the caches' pages are dealt out evenly whatever the
+ * lengths, and the last block to finish a (sequence, KV head) joins its parts
+ * in a fixed order, so results do not change from run to run.
+ */
+tq_status tq_f8_decode_attention(const tq_f8_cache* cache, const void* q, int q_dtype, int64_t q_stride,
+                                 const void* cache_buf, const int32_t* block_table, const int32_t* seq_lens,
+                                 float scale, int batch, void* out, int out_dtype, void* stream);
+
+/* Read and clear the handle's device error word, like tq_get_device_error. */
+tq_status tq_f8_get_device_error(const tq_f8_cache* cache, uint32_t* flags, void* stream);
 
 #ifdef __cplusplus
 }

@@ -23,9 +23,11 @@ __all__ = [
     "tq_store", "tq_decode_attention", "tq_decode_attention_noalloc", "tq_set_profile_events",
     "tq_get_device_error", "tq_set_store_small_max", "tq_extend_attention", "TQ_DEVERR_CHUNK", "TQCache",
     "TQ_PROF_STORE", "TQ_PROF_DECODE_SPLIT", "tq_check_wait_timeout", "tq_store_decode_attention",
+    "TQ_DTYPE_F16", "tq_f8_config", "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store",
+    "tq_f8_load", "tq_f8_decode_attention", "tq_f8_get_device_error", "TQF8Cache",
 ]
 
-TQ_DTYPE_F32, TQ_DTYPE_BF16 = 0, 1
+TQ_DTYPE_F32, TQ_DTYPE_BF16, TQ_DTYPE_F16 = 0, 1, 2
 TQ_OUT_ROTATED = 0x100
 TQ_V_MSE, TQ_V_G32 = 0, 1
 TQ_CODEBOOK_LLOYD, TQ_CODEBOOK_UNIFORM = 0, 1
@@ -39,6 +41,8 @@ EXPORTED = [
     "tq_set_profile_events", "tq_get_device_error", "tq_decode_attention_noalloc", "tq_last_cuda_error",
     "tq_set_store_small_max", "tq_make_uniform_codebook", "tq_extend_attention", "tq_check_wait_timeout",
     "tq_store_decode_attention",
+    "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store", "tq_f8_load",
+    "tq_f8_decode_attention", "tq_f8_get_device_error",
 ]
 TQ_PROF_STORE, TQ_PROF_DECODE_SPLIT = 0, 1
 
@@ -77,6 +81,21 @@ class tq_cache_config(ctypes.Structure):
         defaults = dict(block_size=16, k_qjl=1, seed_rot=2, seed_qjl=1, max_batch=1, split_blocks=32, tail_cap=0)
         defaults.update(kw)
         super().__init__(**defaults)
+
+
+class tq_f8_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int64),
+        ("max_batch", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32),
+    ]
+
+    def __init__(self, **kw):
+        super().__init__(**{**dict(block_size=16, max_batch=1), **kw})
 
 
 _LIB = None
@@ -122,6 +141,17 @@ def load_library():
             "tq_store_decode_attention": (
                 i32, [_P, _P, _P, i32, i64, _P, _P, i32, _P, _P, _P, _P, _P, _P, ctypes.c_float, i32, _P, i32, _P]),
         }
+        f8p = ctypes.POINTER(tq_f8_config)
+        sig.update({
+            "tq_f8_cache_sizes": (i32, [f8p, sz, sz, sz]),
+            "tq_f8_cache_create": (i32, [f8p, _P, _P, ctypes.POINTER(_P)]),
+            "tq_f8_cache_destroy": (i32, [_P]),
+            "tq_f8_store": (i32, [_P, _P, _P, i32, i64, i64, i64, _P, _P, _P]),
+            "tq_f8_load": (i32, [_P, _P, _P, _P, _P, i32, i64, _P, _P, i32, _P]),
+            "tq_f8_decode_attention": (
+                i32, [_P, _P, i32, i64, _P, _P, _P, ctypes.c_float, i32, _P, i32, _P]),
+            "tq_f8_get_device_error": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
+        })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
@@ -418,6 +448,214 @@ class TQCache:
     def close(self):
         if self.handle:
             tq_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------------- 8-bit cache
+_DTYPE_CODES = None
+
+
+def _code(t, name):
+    """dtype code of a tensor of the 8-bit cache and prompt calls."""
+    global _DTYPE_CODES
+    if _DTYPE_CODES is None:
+        import torch
+
+        _DTYPE_CODES = {torch.float32: TQ_DTYPE_F32, torch.bfloat16: TQ_DTYPE_BF16, torch.float16: TQ_DTYPE_F16}
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}: float32, bfloat16 or float16")
+    return code
+
+
+def _rows(t, name, heads, d):
+    """Pointer and row stride of a CUDA tensor [rows, heads, d] whose rows are
+    contiguous (the rows themselves may lie apart, as in a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(t.shape)}")
+    row, head, el = t.stride()
+    if el != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name}: the [{heads}, {d}] part of a row must be contiguous")
+    if t.shape[0] <= 1:
+        row = heads * d
+    elif row < heads * d:
+        raise ValueError(f"{name}: rows overlap (row stride {row})")
+    return t.data_ptr(), row
+
+
+def _out_rows(t, name, rows, heads, d):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads}, {d}], got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _index(t, name, dtype, least):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() < least:
+        raise ValueError(f"{name} must have at least {least} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _table(t, batch, columns):
+    import torch
+
+    if t.dim() != 2 or t.shape[0] < batch or t.shape[1] != columns:
+        raise ValueError(f"block_table must be [>= {batch}, {columns}], got {tuple(t.shape)}")
+    return _index(t, "block_table", torch.int32, 0)
+
+
+def _same_device(device, **tensors):
+    """Every tensor on the handle's device, which must be the current one (the
+    calls launch on the current device)."""
+    import torch
+
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the handle's buffers on {device}")
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the current device is cuda:{torch.cuda.current_device()}, the handle's buffers are on {device}")
+
+
+def tq_f8_cache_sizes(cfg):
+    vals = [ctypes.c_size_t() for _ in range(3)]
+    _check(load_library().tq_f8_cache_sizes(ctypes.byref(cfg), *[ctypes.byref(v) for v in vals]), "tq_f8_cache_sizes")
+    return dict(zip(["page_bytes", "cache_bytes", "workspace_bytes"], [v.value for v in vals]))
+
+
+def tq_f8_cache_create(cfg, workspace, stream=None):
+    h = _P()
+    _check(load_library().tq_f8_cache_create(ctypes.byref(cfg), _P(workspace.data_ptr()), _stream_ptr(stream),
+                                             ctypes.byref(h)), "tq_f8_cache_create")
+    return h
+
+
+def tq_f8_cache_destroy(handle):
+    _check(load_library().tq_f8_cache_destroy(handle), "tq_f8_cache_destroy")
+
+
+def tq_f8_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
+    """k, v [T, H_kv, d] (f32, bf16 or f16, same dtype; rows may lie apart);
+    slot_mapping int64 [T]."""
+    import torch
+
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and dtype")
+    kp, ks = _rows(k, "k", cfg.num_kv_heads, cfg.head_dim)
+    vp, vs = _rows(v, "v", cfg.num_kv_heads, cfg.head_dim)
+    n = k.shape[0]
+    _check(load_library().tq_f8_store(handle, kp, vp, _code(k, "k"), ks, vs, n,
+                                      _index(slot_mapping, "slot_mapping", torch.int64, n), _dev(cache, "cache"),
+                                      _stream_ptr(stream)), "tq_f8_store")
+
+
+def tq_f8_load(handle, cfg, cache, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
+    """block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]; cu_out
+    int32 [B] (or more): first row of each sequence in k_out, v_out [rows,
+    H_kv, d] (f32, bf16 or f16)."""
+    import torch
+
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have the same shape and dtype")
+    b, n = seq_lens.shape[0], k_out.shape[0]
+    _check(load_library().tq_f8_load(
+        handle, _dev(cache, "cache"),
+        _table(block_table, b, cfg.max_blocks_per_seq),
+        _index(seq_lens, "seq_lens", torch.int32, b), _index(cu_out, "cu_out", torch.int32, b), b, n,
+        _out_rows(k_out, "k_out", None, cfg.num_kv_heads, cfg.head_dim),
+        _out_rows(v_out, "v_out", n, cfg.num_kv_heads, cfg.head_dim), _code(k_out, "k_out"), _stream_ptr(stream)),
+        "tq_f8_load")
+
+
+def tq_f8_decode_attention(handle, cfg, q, cache, block_table, seq_lens, out, scale=0.0, stream=None):
+    """q, out [B, H_q, d] (f32, bf16 or f16 each; q's rows may lie apart);
+    block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]."""
+    import torch
+
+    qp, qs = _rows(q, "q", cfg.num_q_heads, cfg.head_dim)
+    b = q.shape[0]
+    _check(load_library().tq_f8_decode_attention(
+        handle, qp, _code(q, "q"), qs, _dev(cache, "cache"),
+        _table(block_table, b, cfg.max_blocks_per_seq),
+        _index(seq_lens, "seq_lens", torch.int32, b), float(scale), b,
+        _out_rows(out, "out", b, cfg.num_q_heads, cfg.head_dim), _code(out, "out"), _stream_ptr(stream)),
+        "tq_f8_decode_attention")
+
+
+def tq_f8_get_device_error(handle, stream=None):
+    flags = ctypes.c_uint32()
+    _check(load_library().tq_f8_get_device_error(handle, ctypes.byref(flags), _stream_ptr(stream)),
+           "tq_f8_get_device_error")
+    return flags.value
+
+
+class TQF8Cache:
+    """Owns (or adopts) the pages of an 8-bit cache, its workspace and the
+    library handle.  ``cache``: an existing uint8 tensor of cache_bytes."""
+
+    def __init__(self, device="cuda", cache=None, **cfg_kwargs):
+        import torch
+
+        self.handle = None
+        self.cfg = tq_f8_config(**cfg_kwargs)
+        self.sizes = tq_f8_cache_sizes(self.cfg)
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        if cache is None:
+            cache = torch.zeros(self.sizes["cache_bytes"], dtype=torch.uint8, device=self.device)
+        elif (cache.dtype != torch.uint8 or cache.numel() != self.sizes["cache_bytes"] or not cache.is_contiguous()
+              or cache.device != self.device):
+            raise ValueError(f"cache must be {self.sizes['cache_bytes']} contiguous uint8 bytes on {self.device}")
+        self.cache = cache
+        self.workspace = torch.empty(self.sizes["workspace_bytes"], dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            self.handle = tq_f8_cache_create(self.cfg, self.workspace)
+
+    @property
+    def page_bytes(self):
+        return self.sizes["page_bytes"]
+
+    def pages(self):
+        """The cache as [num_blocks, H_kv, page_bytes]."""
+        return self.cache.view(self.cfg.num_blocks, self.cfg.num_kv_heads, self.page_bytes)
+
+    def store(self, k, v, slot_mapping, stream=None):
+        _same_device(self.device, k=k, v=v, slot_mapping=slot_mapping)
+        tq_f8_store(self.handle, self.cfg, k, v, slot_mapping, self.cache, stream)
+
+    def load(self, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
+        _same_device(self.device, block_table=block_table, seq_lens=seq_lens, cu_out=cu_out, k_out=k_out, v_out=v_out)
+        tq_f8_load(self.handle, self.cfg, self.cache, block_table, seq_lens, cu_out, k_out, v_out, stream)
+        return k_out, v_out
+
+    def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
+        import torch
+
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        _same_device(self.device, q=q, block_table=block_table, seq_lens=seq_lens, out=out)
+        tq_f8_decode_attention(self.handle, self.cfg, q, self.cache, block_table, seq_lens, out, scale, stream)
+        return out
+
+    def device_error(self, stream=None):
+        return tq_f8_get_device_error(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            tq_f8_cache_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
