@@ -423,7 +423,8 @@ typedef struct tq_f8_config {
     int32_t block_size;         /* tokens per cache block; must be 16 */
     int64_t num_blocks;         /* blocks in the cache pool */
     int32_t max_batch;          /* sequences per load or decode call */
-    int32_t max_blocks_per_seq; /* columns of the block table */
+    int32_t max_blocks_per_seq; /* columns of the block table;
+                                   max_batch * max_blocks_per_seq * H_kv * ceil(G / 16) < 2^31 */
 } tq_f8_config;
 
 typedef struct tq_f8_cache tq_f8_cache;

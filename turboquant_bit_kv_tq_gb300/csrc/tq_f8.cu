@@ -226,8 +226,11 @@ static tq_status f8_check(const tq_f8_config& c) {
     if (c.num_blocks < 1 || c.num_blocks > 0x7FFFFFFF || c.max_batch < 1 || c.max_blocks_per_seq < 1 ||
         c.max_blocks_per_seq > 0x7FFFFFFF / kBlock)
         return TQ_ERR_INVALID_ARG;
-    // counters of every (sequence, KV head, head group), and the q rows, within int32
-    if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF) return TQ_ERR_INVALID_ARG;
+    // q rows and the pages of all block-table entries, KV heads and head groups within int32
+    const F8Geom g = f8_geom(c);
+    if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF ||
+        (double)c.max_batch * c.max_blocks_per_seq * c.num_kv_heads * g.nhg > 2147483647.0)
+        return TQ_ERR_INVALID_ARG;
     return TQ_OK;
 }
 
@@ -263,10 +266,11 @@ tq_status tq_f8_cache_create(const tq_f8_config* cfg, void* workspace_dev, void*
     h->geom = f8_geom(*cfg);
     h->err = reinterpret_cast<uint32_t*>(ws + w.err);
     h->cnt = reinterpret_cast<uint32_t*>(ws + w.cnt);
-    h->part = reinterpret_cast<float*>(ws + w.part);
-    h->meta = reinterpret_cast<float*>(ws + w.meta);
+    h->gcnt = reinterpret_cast<uint32_t*>(ws + w.gcnt);
+    h->part = reinterpret_cast<float4*>(ws + w.part);
+    h->meta = reinterpret_cast<float4*>(ws + w.meta);
     cudaStream_t s = (cudaStream_t)stream;
-    tq_status cs = cuda_status(cudaMemsetAsync(ws, 0, w.cnt + w.cnt_bytes, s));
+    tq_status cs = cuda_status(cudaMemsetAsync(ws, 0, w.zeroed, s));
     if (cs == TQ_OK) cs = cuda_status(cudaStreamSynchronize(s));
     if (cs != TQ_OK) {
         delete h;

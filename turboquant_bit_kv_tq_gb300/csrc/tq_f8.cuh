@@ -5,9 +5,10 @@
 
 namespace tq {
 
-// Resident blocks a decode grid may have; the workspace holds two split
-// partials for each.
-constexpr int kF8MaxCtas = 512;
+// Decode grids: kF8Warps warps per block, at most kF8Ctas blocks per SM and
+// kF8MaxSms SMs; the workspace holds two partial sums for each of their warps.
+constexpr int kF8Warps = 4, kF8Ctas = 3, kF8MaxSms = 160;
+constexpr int kF8Slots = 2 * kF8Warps * kF8Ctas * kF8MaxSms;
 
 // Query heads of one KV head that one work unit serves (nhg units per KV head
 // share its pages through L2 when G > 16), in n-tiles of 8 heads.
@@ -25,20 +26,22 @@ inline F8Geom f8_geom(const tq_f8_config& c) {
 
 struct F8Workspace {
     // err: the error word; cnt: one counter per (sequence, KV head, head group);
-    // part: [2 * kF8MaxCtas][8 nt][d] fp32; meta: [2 * kF8MaxCtas][8 nt][4] fp32
-    size_t err, cnt, cnt_bytes, part, meta, total;
+    // gcnt: one per slot; part: [kF8Slots][d/16][nt][32][4] fp32 sums in
+    // fragment order; meta: [kF8Slots][8 nt] {r, r', l, -}
+    size_t err, cnt, gcnt, zeroed, part, meta, total;
 };
 inline F8Workspace f8_workspace(const tq_f8_config& c) {
     const F8Geom g = f8_geom(c);
     F8Workspace w;
     w.err = 0;
     w.cnt = 16;
-    w.cnt_bytes = (size_t)c.max_batch * c.num_kv_heads * g.nhg * 4;
-    size_t off = (w.cnt + w.cnt_bytes + 255) & ~(size_t)255;
+    w.gcnt = w.cnt + (size_t)c.max_batch * c.num_kv_heads * g.nhg * 4;
+    w.zeroed = w.gcnt + (size_t)kF8Slots * 4;
+    size_t off = (w.zeroed + 255) & ~(size_t)255;
     w.part = off;
-    off += (size_t)2 * kF8MaxCtas * 8 * g.nt * c.head_dim * 4;
+    off += (size_t)kF8Slots * 8 * g.nt * c.head_dim * 4;
     w.meta = off;
-    off += (size_t)2 * kF8MaxCtas * 8 * g.nt * 16;
+    off += (size_t)kF8Slots * 8 * g.nt * 16;
     w.total = off;
     return w;
 }
@@ -79,6 +82,21 @@ __device__ __forceinline__ void f8_store2(void* row, int64_t i, float x, float y
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + i) = f8_pack16(x, y, dtype);
 }
 
+// 16 consecutive elements to row + i (16-byte aligned)
+__device__ __forceinline__ void f8_store16(void* row, int64_t i, const float (&v)[16], int dtype) {
+    if (dtype == TQ_DTYPE_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    } else {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + i);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            p[k] = make_uint4(f8_pack16(v[8 * k], v[8 * k + 1], dtype), f8_pack16(v[8 * k + 2], v[8 * k + 3], dtype),
+                              f8_pack16(v[8 * k + 4], v[8 * k + 5], dtype), f8_pack16(v[8 * k + 6], v[8 * k + 7], dtype));
+    }
+}
+
 // the power of two an exponent byte stands for (0: 2^-127, a subnormal; 255: NaN)
 __device__ __forceinline__ float f8_scale(uint32_t e) {
     return __uint_as_float(e == 255u ? 0x7FC00000u : e == 0u ? 0x00400000u : e << 23);
@@ -104,7 +122,6 @@ struct tq_f8_cache {
     tq_f8_config cfg;
     tq::F8Geom geom;
     uint32_t* err;
-    uint32_t* cnt;
-    float* part;
-    float* meta;
+    uint32_t *cnt, *gcnt;
+    float4 *part, *meta;
 };

@@ -9,21 +9,23 @@
 // own, so no weight over- or underflows whatever the scales are.
 //
 // Bound by memory (2 d + 2 bytes per token and KV head).  All pages of all
-// sequences, in the order (sequence, KV head, page), are dealt out evenly to a
-// fixed grid of resident blocks; a block's run is cut into segments of one
-// (sequence, KV head) each.  The warps of a block take steps of 256/d pages of a
-// segment in turn; each warp keeps a ring of steps in flight with cp.async,
-// which puts the rows where the tensor-core operands read them without bank
-// conflicts, and prefetches across segments.  Products per 16 tokens:
+// sequences, in the order (sequence, KV head, page), are dealt out evenly in
+// runs to a fixed grid of resident blocks: one run per block, whose warps share
+// its segments (the pages of one (sequence, KV head) each) step by step and add
+// up in shared memory at a segment's end; or, with many short sequences, one run
+// per warp, and no warp waits for another.  A step is 256/d pages.  Each warp
+// keeps a ring of steps in flight with cp.async, across segments; the copies put
+// the rows where the tensor-core operands read them without bank conflicts.  Products per 16 tokens:
 //   S^T[tokens x heads] = K Q^T     mma.m16n8k16, A = codes as fp16 (exact)
 //   O^T[d x heads] += V^T P^T       A = pairs of value codes, B = the weights
 // so a KV head's query heads (8 or 16 columns) share every page, and tokens and
 // coordinates fill the 16 rows: a group of 8 heads wastes nothing.  (tcgen05
 // would want 128 rows of operands in shared memory, written back after the
-// conversion; mma.sync takes the converted codes from registers and runs at
-// about a third of its rate here.)
-// A segment that is a whole (sequence, KV head) is written out; the others go
-// to the workspace, and the last block to arrive joins them in block order.
+// conversion; mma.sync takes the converted codes from registers.)
+// A segment that is a whole (sequence, KV head) is written out at once.  The
+// sums of the others go to the workspace and are joined in run order: those of
+// one block when its warps are through, then those of 16 blocks by the last of
+// them to arrive, then the groups' by the last group.
 
 #include <algorithm>
 
@@ -37,19 +39,20 @@ struct F8DecodeArgs {
     const uint8_t* cache;
     const int32_t *table, *lens;
     void* out;
-    uint32_t *err, *cnt;
-    float *part, *meta;
+    uint32_t *err, *cnt, *gcnt;
+    float4 *part, *meta;
     int64_t num_blocks;
     float scale_log2e;
     int q_dtype, out_dtype;
     int batch, heads, q_heads, group, nhg, hp, max_blocks;
 };
 
-constexpr int kF8Warps = 4;
 constexpr int kF8Threads = 32 * kF8Warps;
-// weights are kept below 2^kF8Slack and the reference is set so that the
-// largest is 2^kF8Head: small weights stay normal fp16 numbers further down
-constexpr float kF8Slack = 12.f, kF8Head = 4.f;
+// weights are kept below kF8Most and the reference is set so that the largest
+// is 2^kF8Head: small weights stay normal fp16 numbers further down
+constexpr float kF8Most = 4096.f, kF8Head = 4.f;
+// the reference of an empty sum; any score is far above it
+constexpr float kF8None = -1e30f;
 
 __device__ __forceinline__ float f8_exp2(float x) {
     float r;
@@ -86,549 +89,714 @@ struct F8Cfg {
     static constexpr int PP = 256 / D;                 // pages per step
     static constexpr int PAGE = f8_page_bytes(D);
     static constexpr int STEP = PP * PAGE;             // bytes of a ring stage
-    static constexpr int STAGES = 3;
     static constexpr int HEADS = 8 * NT;
-    static constexpr int QF = (D / 16) * NT * 32 * 8 * (PREC ? 2 : 1);
-    static constexpr int BUF_LD = D + 8;               // head stride of the merge buffer, in floats
+    static constexpr int QF = (D / 16) * NT * 32 * 8 * (PREC ? 2 : 1);  // query operands of a warp
+    // blocks per SM (three where two pages per warp and the registers allow it, else two), and as
+    // deep a ring as fits then, of at most four stages
+    static constexpr int per_cta(int n) { return 233472 / n - 1024 - 1280; }
+    static constexpr int fit(int n) { return (per_cta(n) / kF8Warps - QF - 64) / STEP; }
+    static constexpr int CTAS = fit(3) >= 2 && NT == 1 && D == 128 ? 3 : fit(2) >= 2 ? 2 : 1;
+    static constexpr int STAGES = fit(CTAS) < 6 ? fit(CTAS) : 6;
+    static_assert(STAGES >= 2, "ring");
     static constexpr int off_q = kF8Warps * STAGES * STEP;
-    // the merge buffer takes the query operands' place: it is written once
-    // every warp is through with the segment's scores
-    static constexpr int off_buf = off_q;
-    static constexpr int BUF = HEADS * BUF_LD * 4;
-    static constexpr int off_cq = off_q + (QF > BUF ? QF : BUF);
-    static constexpr int off_ref = off_cq + HEADS * 4;             // [warps][HEADS][3] r, r', l
-    static constexpr int off_info = off_ref + kF8Warps * HEADS * 3 * 4;  // [warps][STAGES][PP] valid tokens
+    static constexpr int off_info = off_q + kF8Warps * QF;         // [warps][STAGES][PP] valid tokens
     static constexpr int total = off_info + kF8Warps * STAGES * PP * 4;
-    static constexpr int CTAS = total + 1024 <= 233472 / 2 ? 2 : 1;  // per SM
+    static constexpr int ITEMS = D / 16 * NT * 32;     // float4 per partial sum
+    // two sums fit the four warps' query operands, whose place they take at a segment's end
+    static_assert(2 * ITEMS * 16 <= kF8Warps * QF, "merge buffers");
 };
+static_assert(kF8Ctas >= F8Cfg<128, 1, false>::CTAS, "workspace slots");
 
-__device__ __forceinline__ int f8_seq_pages(const F8DecodeArgs& a, int b) {
-    const int len = __ldg(a.lens + b), cap = a.max_blocks * 16;
-    return (max(0, min(len, cap)) + 15) >> 4;
-}
+__device__ __forceinline__ int f8_clamp(const F8DecodeArgs& a, int len) { return max(0, min(len, a.max_blocks * 16)); }
+__device__ __forceinline__ int f8_pages(const F8DecodeArgs& a, int len) { return (f8_clamp(a, len) + 15) >> 4; }
 
 // A position in the order (sequence, KV head and head group, page) and the
-// pages left of a block's run.
+// pages left of a warp's run.
 struct F8Walk {
-    int b, j, p, np;
-    int64_t left;
+    int b, j, p, len, left;
 };
 struct F8Seg {
-    int b, j, p0, p1, np;
+    int b, j, p0, p1, len;
+    __device__ __forceinline__ int np() const { return (len + 15) >> 4; }
 };
 __device__ __forceinline__ F8Seg f8_next(const F8DecodeArgs& a, F8Walk& w, int nj) {
     F8Seg s;
     s.b = w.b;
     s.j = w.j;
     s.p0 = w.p;
-    s.np = w.np;
-    const int n = (int)min((int64_t)(w.np - w.p), w.left);
+    s.len = w.len;
+    const int n = min(s.np() - w.p, w.left);
     s.p1 = w.p + n;
     w.left -= n;
     w.p = 0;
     if (++w.j == nj) {
         w.j = 0;
-        w.np = 0;
-        while (w.left > 0 && w.np == 0 && ++w.b < a.batch) w.np = f8_seq_pages(a, w.b);
+        w.len = 0;
+        while (w.left > 0 && w.len == 0 && ++w.b < a.batch) w.len = f8_clamp(a, __ldg(a.lens + w.b));
     }
     return s;
 }
 
+// Even runs: run i < n takes units [start(i), start(i + 1)) of `total` >= n.
+struct F8Runs {
+    uint32_t q, r, n;
+    __device__ __forceinline__ uint32_t start(uint32_t i) const { return i * q + min(i, r); }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+        const uint32_t big = r * (q + 1);
+        return u < big ? u / (q + 1) : r + (u - big) / q;
+    }
+};
+
+// 2^(r' - r) / l of a head's sums; no token: 0
+__device__ __forceinline__ float f8_norm(float R, float Rv, float L) { return L == 0.f ? 0.f : exp2f(Rv - R) / L; }
+
+constexpr int kF8SoloPages = 32;  // pages per unit on average below which warps go alone
+constexpr int kF8Join = 16;  // blocks a group joins; at most kF8MaxSms * kF8Ctas / kF8Join + 1 groups
+struct F8JoinSmem {
+    float fac[32][16];
+    float4 tot[16];
+};
+static_assert(kF8MaxSms * kF8Ctas / kF8Join + 1 <= 32, "groups of a join");
+
 template <int D, int NT, bool PREC>
-__global__ void __launch_bounds__(kF8Threads, 2) f8_decode_kernel(F8DecodeArgs a) {
+__global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decode_kernel(F8DecodeArgs a) {
     using C = F8Cfg<D, NT, PREC>;
     constexpr int S = C::STAGES, PP = C::PP, W = kF8Warps, HEADS = C::HEADS;
+    static_assert(sizeof(F8JoinSmem) <= C::total, "the join reuses the rings");
     extern __shared__ __align__(16) uint8_t smem[];
-    uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q);
-    float* buf = reinterpret_cast<float*>(smem + C::off_buf);
-    float* cq = reinterpret_cast<float*>(smem + C::off_cq);
-    float* ref = reinterpret_cast<float*>(smem + C::off_ref);
-    __shared__ long long s_scan[kF8Threads / 32 + 1], s_units[kF8Threads / 32];
-    __shared__ long long s_base;
-    __shared__ int s_b, s_last;
+    __shared__ int s_last;
+    __shared__ float4 s_ref[W][HEADS];
+    __shared__ F8Seg s_part[W][2];  // segments whose sums are in the workspace (b < 0: none)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int nj = a.heads * a.nhg;
     uint8_t* ring = smem + warp * (S * C::STEP);
+    uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q + warp * C::QF);
     int* info = reinterpret_cast<int*>(smem + C::off_info) + warp * S * PP;
 
-    // ---- the run of this block: totals, and the sequence its run starts in
-    const int per = (a.batch + kF8Threads - 1) / kF8Threads;
-    const int bt0 = min(a.batch, tid * per), bt1 = min(a.batch, bt0 + per);
-    long long mine = 0, some = 0;
+    if (lane < 2) s_part[warp][lane].b = -1;
+    pdl_wait();
+    // ---- totals: lane i of every warp counts the sequences [i per, (i + 1) per)
+    const int per = (a.batch + 31) >> 5;
+    const int bt0 = min(a.batch, lane * per), bt1 = min(a.batch, bt0 + per);
+    int mine = 0, some = 0;
+#pragma unroll 4
     for (int b = bt0; b < bt1; ++b) {
         const int len = __ldg(a.lens + b);
         if (len < 0 || len > a.max_blocks * 16) set_error(a.err, TQ_DEVERR_SEQLEN);
-        const int np = f8_seq_pages(a, b);
+        const int np = f8_pages(a, len);
         mine += np;
         some += np > 0;
     }
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
-        some += __shfl_xor_sync(0xffffffffu, some, o);
     }
-    if (lane == 31) s_scan[warp] = incl;
-    if (lane == 0) s_units[warp] = some;
-    if (tid == 0) s_b = -1;
-    __syncthreads();
-    long long before = incl - mine, total = 0, units = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        before += w < warp ? s_scan[w] : 0;
-        total += s_scan[w];
-        units += s_units[w];
-    }
-    before *= nj;
-    total *= nj;
-    units *= nj;
-    // blocks that get a run: every one, unless it would be shorter than a
-    // step of each warp (then as many as there are (sequence, KV head)s, at least)
-    const long long N =
-        max(1ll, min((long long)gridDim.x, max(units, (total + W * PP - 1) / (W * PP))));
-    const long long u0 = min(total, (long long)blockIdx.x * total / N);
-    const long long u1 = blockIdx.x < N ? ((long long)blockIdx.x + 1) * total / N : u0;
-    if (u0 < u1 && before <= u0 && u0 < before + mine * nj) {
-        long long at = before;
-        for (int b = bt0; b < bt1; ++b) {
-            const long long n = (long long)f8_seq_pages(a, b) * nj;
-            if (u0 < at + n) {
-                s_b = b;
-                s_base = at;
-                break;
-            }
-            at += n;
-        }
-    }
+    const int before = (incl - mine) * nj;
+    const int total = __shfl_sync(0xffffffffu, incl, 31) * nj;
+    const int units = (int)__reduce_add_sync(0xffffffffu, (unsigned)some) * nj;
     // sequences without a token: their rows are zero
-    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-        if (f8_seq_pages(a, b) > 0) continue;
-        for (int i = tid; i < a.q_heads * D / 2; i += kF8Threads)
-            f8_store2(a.out, (int64_t)b * a.q_heads * D + 2 * i, 0.f, 0.f, a.out_dtype);
-    }
-    __syncthreads();
-    if (u0 >= u1) return;
-
-    F8Walk cons;
-    cons.b = s_b;
-    cons.np = f8_seq_pages(a, s_b);
+    if (units < a.batch * nj)
+        for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+            if (f8_pages(a, __ldg(a.lens + b)) > 0) continue;
+            for (int i = tid; i < a.q_heads * D / 2; i += kF8Threads)
+                f8_store2(a.out, (int64_t)b * a.q_heads * D + 2 * i, 0.f, 0.f, a.out_dtype);
+        }
+    if (total == 0) return;
+    // One run per block, of at least 16 pages on average (two steps for each
+    // warp), or, with more units than blocks and those short, one per warp, of at
+    // least 8 pages.
+    const bool solo = units > (int)gridDim.x && (long long)total < (long long)kF8SoloPages * units;
+    const int rpb = solo ? W : 1;  // runs per block
+    F8Runs runs;
     {
-        const long long rel = u0 - s_base;
-        cons.j = (int)(rel / cons.np);
-        cons.p = (int)(rel - (long long)cons.j * cons.np);
+        const int per_run = solo ? 8 : 16;
+        const long long want = (long long)units * max(1, total / units / per_run);
+        runs.n = (uint32_t)min((long long)gridDim.x * rpb, want);
+        runs.q = (uint32_t)total / runs.n;
+        runs.r = (uint32_t)total - runs.q * runs.n;
     }
-    cons.left = u1 - u0;
-    F8Walk prod = cons;
+    const uint32_t run0 = blockIdx.x * rpb, run = solo ? run0 + warp : run0;
+    if (run0 >= runs.n) return;
 
-    // ---- producer: this warp's steps, segment after segment
-    F8Seg ps = f8_next(a, prod, nj);
-    int pst = warp, plen = min(__ldg(a.lens + ps.b), a.max_blocks * 16);
-    int ids = -1, ids_at = -1;  // block ids of 32 / PP steps from step ids_at (stride W) on
-    auto produce = [&](int stage) {
-        // move on to a segment that has a step for this warp
-        while (pst * PP >= ps.p1 - ps.p0) {
-            if (prod.left <= 0) return;
-            ps = f8_next(a, prod, nj);
-            pst = warp;
-            plen = min(__ldg(a.lens + ps.b), a.max_blocks * 16);
-            ids_at = -1;
+    if (run < runs.n) {
+        const int u0 = (int)runs.start(run), u1 = (int)runs.start(run + 1);
+        const int sw = solo ? 0 : warp, sn = solo ? 1 : W;  // this warp takes the steps sw, sw + sn, ... of a segment
+        F8Walk cons;
+        {
+            // the sequence u0 lies in: one lane has it among its own
+            int at = before, b = bt0, len = 0;
+            const bool here = u0 >= before && u0 < before + mine * nj;
+            if (here)
+                for (;; ++b) {
+                    len = __ldg(a.lens + b);
+                    const int n = f8_pages(a, len) * nj;
+                    if (u0 < at + n) break;
+                    at += n;
+                }
+            const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            cons.b = __shfl_sync(0xffffffffu, b, src);
+            cons.len = f8_clamp(a, __shfl_sync(0xffffffffu, len, src));
+            const int rel = u0 - __shfl_sync(0xffffffffu, at, src), np = (cons.len + 15) >> 4;
+            cons.j = rel / np;
+            cons.p = rel - cons.j * np;
         }
-        if (ids_at < 0 || pst >= ids_at + W * (32 / PP)) {
-            ids_at = pst;
-            const int p = ps.p0 + (pst + W * (lane / PP)) * PP + lane % PP;
-            ids = p < ps.p1 ? __ldg(a.table + (int64_t)ps.b * a.max_blocks + p) : -1;
-            if (p < ps.p1 && (ids < 0 || ids >= a.num_blocks)) {
-                set_error(a.err, TQ_DEVERR_BLOCK);
-                ids = -1;
+        cons.left = u1 - u0;
+        F8Walk prod = cons;
+
+        // ---- producer: this warp's steps, segment after segment
+        F8Seg ps = f8_next(a, prod, nj);
+        int pst = sw;
+        int ids = -1, ids_at = 0, ids_n = 0;  // block ids of ids_n pages: this warp's steps from ids_at on
+        auto produce = [&](int stage) {
+            while (ps.p0 + pst * PP >= ps.p1) {
+                if (prod.left <= 0) return;
+                ps = f8_next(a, prod, nj);
+                pst = sw;
+                ids_n = 0;
             }
-        }
-        const int h = ps.j / a.nhg;
+            if (ids_at >= ids_n) {
+                ids_at = 0;
+                ids_n = 32;
+                const int p = ps.p0 + (pst + sn * (lane / PP)) * PP + lane % PP;
+                ids = p < ps.p1 ? __ldg(a.table + (int64_t)ps.b * a.max_blocks + p) : -1;
+                if (p < ps.p1 && (ids < 0 || ids >= a.num_blocks)) {
+                    set_error(a.err, TQ_DEVERR_BLOCK);
+                    ids = -1;
+                }
+            }
+            const int h = a.nhg == 1 ? ps.j : ps.j / a.nhg;
 #pragma unroll
-        for (int pp = 0; pp < PP; ++pp) {
-            const int blk = __shfl_sync(0xffffffffu, ids, (pst - ids_at) / W * PP + pp);
-            const int p = ps.p0 + pst * PP + pp;
-            if (lane == 0) info[stage * PP + pp] = blk < 0 ? 0 : min(16, plen - 16 * p);
-            if (blk < 0) continue;
-            const uint8_t* src = a.cache + ((int64_t)blk * a.heads + h) * C::PAGE;
-            const uint32_t dst = smem_u32(ring + stage * C::STEP + pp * C::PAGE);
-            constexpr int CPR = D / 16;
-#pragma unroll
-            for (int i = 0; i < CPR; ++i) {
+            for (int pp = 0; pp < PP; ++pp) {
+                const int blk = __shfl_sync(0xffffffffu, ids, ids_at + pp);
+                const int p = ps.p0 + pst * PP + pp;
+                // (a page behind the segment's last has block id -1 too)
+                if (lane == 0) info[stage * PP + pp] = blk < 0 ? 0 : min(16, ps.len - 16 * p);
+                if (blk < 0) continue;
+                const uint8_t* src = a.cache + ((int64_t)blk * a.heads + h) * C::PAGE;
+                const uint32_t dst = smem_u32(ring + stage * C::STEP + pp * C::PAGE);
                 // 32 rows (16 keys, 16 values) of CPR 16-byte chunks; chunk ch of
                 // row r goes to ch ^ 4 (r & 1) for keys and ch ^ (r & 6) for values,
                 // which the operand reads below hit without bank conflicts
-                const int idx = lane + 32 * i, r = idx / CPR, ch = idx % CPR;
-                const int x = r < 16 ? (r & 1) << 2 : r & 6;
-                cp_async16(dst + r * D + ((ch ^ x) << 4), src + idx * 16);
-            }
-            if (lane < 2) cp_async16(dst + 32 * D + 16 * lane, src + 32 * D + 16 * lane);
-        }
-        pst += W;
-    };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+                constexpr int CPR = D / 16, RPI = 32 / CPR;  // rows per warp-wide copy
+                const int r0 = lane / CPR, ch = lane % CPR;
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        produce(s);
-        commit();
-    }
-    int stage = 0;
-
-    while (cons.left > 0) {
-        const F8Seg sg = f8_next(a, cons, nj);
-        const int kvh = sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
-        const int nh = min(a.hp, a.group - hg * a.hp);      // heads of this unit
-        const int qh0 = kvh * a.group + hg * a.hp;
-
-        // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9)
-        // (exact for bf16 and fp16 inputs), in fragment order
-        for (int h = warp; h < HEADS; h += W) {
-            float4 x[D / 128];
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (h < nh) {
-                    const int64_t off = (int64_t)sg.b * a.q_stride + (int64_t)(qh0 + h) * D + 128 * i + 4 * lane;
-                    x[i] = f8_load4(static_cast<const uint8_t*>(a.q) + off * (a.q_dtype == TQ_DTYPE_F32 ? 4 : 2),
-                                    a.q_dtype);
+                for (int i = 0; i < CPR; ++i) {
+                    const int x = i < CPR / 2 ? (r0 & 1) << 2 : (r0 & 6 & (RPI - 1)) ^ (RPI * i & 6);
+                    cp_async16(dst + r0 * D + ((ch ^ x) << 4) + 512 * i, src + 16 * lane + 512 * i);
                 }
-                top = max(max(top, max(__float_as_uint(x[i].x) & 0x7FFFFFFFu, __float_as_uint(x[i].y) & 0x7FFFFFFFu)),
-                          max(__float_as_uint(x[i].z) & 0x7FFFFFFFu, __float_as_uint(x[i].w) & 0x7FFFFFFFu));
+                if (lane < 2) cp_async16(dst + 32 * D + 16 * lane, src + 32 * D + 16 * lane);
             }
+            pst += sn;
+            ids_at += PP;
+        };
+        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const bool bad = top >= 0x7F800000u;
-            const uint32_t e = max(top >> 23, 16u);
-            const float mul = bad ? 0.f : __uint_as_float((262u - min(e, 254u)) << 23);
-            if (lane == 0) cq[h] = bad ? __uint_as_float(0x7FC00000u) : a.scale_log2e * __uint_as_float((e - 8u) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                if (bad) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                x[i].x *= mul, x[i].y *= mul, x[i].z *= mul, x[i].w *= mul;
-                // elements 128 i + 4 lane ..: 64-element half, 16-element lane part, K step
-                const int el = 128 * i + 4 * lane, ks = (el >> 6) * 4 + ((el >> 2) & 3), cc = (el >> 4) & 3;
-                uint2 f = make_uint2(f8_pack_f16(x[i].x, x[i].y), f8_pack_f16(x[i].z, x[i].w));
-                const int at = (ks * NT + (h >> 3)) * 32 + (h & 7) * 4 + cc;
-                qf[at] = f;
-                if constexpr (PREC)
-                    qf[(D / 16) * NT * 32 + at] =
-                        make_uint2(f8_pack_rest(x[i].x, x[i].y, f.x), f8_pack_rest(x[i].z, x[i].w, f.y));
-            }
-        }
-        __syncthreads();
-        float cqr[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) cqr[n][0] = cq[8 * n + 2 * c], cqr[n][1] = cq[8 * n + 2 * c + 1];
-
-        float o[D / 16][NT][4];
-        float r[NT][2], rv[NT][2], l[NT][2];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) r[n][e] = rv[n][e] = -INFINITY, l[n][e] = 0.f;
-
-        const int nst = (sg.p1 - sg.p0 + PP - 1) / PP;
-        for (int st = warp; st < nst; st += W) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-            __syncwarp();
-            produce(stage == 0 ? S - 1 : stage - 1);
+        for (int s = 0; s < S - 1; ++s) {
+            produce(s);
             commit();
-            const uint8_t* sp = ring + stage * C::STEP;
+        }
+        int stage = 0;
 
-            // ---- scores
-            float s[PP][NT][4];
+        while (cons.left > 0) {
+            const F8Seg sg = f8_next(a, cons, nj);
+            const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
+            const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
+            const int qh0 = kvh * a.group + hg * a.hp;
+
+            // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9)
+            // (exact for bf16 and fp16 inputs), in fragment order
+            float cqr[NT][2];
+            constexpr int QB = HEADS * D <= 8 * 128 ? 8 : 4;  // heads loaded at once
+            const int64_t qoff = (int64_t)sg.b * a.q_stride + (int64_t)qh0 * D + 4 * lane;
 #pragma unroll
-            for (int pp = 0; pp < PP; ++pp)
+            for (int h8 = 0; h8 < HEADS; h8 += QB) {
+                float4 x[QB][D / 128];
+                if (PREC && a.q_dtype == TQ_DTYPE_F32) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[pp][n][0] = s[pp][n][1] = s[pp][n][2] = s[pp][n][3] = 0.f;
+                    for (int hh = 0; hh < QB; ++hh)
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                uint4 ka[PP][2];
+                        for (int i = 0; i < D / 128; ++i)
+                            x[hh][i] = h8 + hh < nh ? __ldg(reinterpret_cast<const float4*>(
+                                                          static_cast<const float*>(a.q) + qoff + (h8 + hh) * D + 128 * i))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                } else {
+                    uint2 y[QB][D / 128];
 #pragma unroll
-                for (int pp = 0; pp < PP; ++pp)
+                    for (int hh = 0; hh < QB; ++hh)
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        ka[pp][u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + (g + 8 * u) * D +
-                                                                    (((4 * h + c) ^ ((g & 1) << 2)) << 4));
+                        for (int i = 0; i < D / 128; ++i)
+                            y[hh][i] = h8 + hh < nh ? __ldg(reinterpret_cast<const uint2*>(
+                                                          static_cast<const uint16_t*>(a.q) + qoff + (h8 + hh) * D + 128 * i))
+                                                    : make_uint2(0u, 0u);
+                    const bool bf = a.q_dtype == TQ_DTYPE_BF16;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                    for (int hh = 0; hh < QB; ++hh)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int at = ((4 * h + k) * NT + n) * 32 + lane;
-                        const uint2 b = qf[at];
-                        uint2 bl = make_uint2(0u, 0u);
-                        if constexpr (PREC) bl = qf[(D / 16) * NT * 32 + at];
-#pragma unroll
-                        for (int pp = 0; pp < PP; ++pp) {
-                            const uint32_t w0 = k == 0 ? ka[pp][0].x : k == 1 ? ka[pp][0].y : k == 2 ? ka[pp][0].z : ka[pp][0].w;
-                            const uint32_t w1 = k == 0 ? ka[pp][1].x : k == 1 ? ka[pp][1].y : k == 2 ? ka[pp][1].z : ka[pp][1].w;
-                            const uint32_t a0 = f8_to_f16x2(w0), a1 = f8_to_f16x2(w1), a2 = f8_to_f16x2_hi(w0),
-                                           a3 = f8_to_f16x2_hi(w1);
-                            f8_mma(s[pp][n], a0, a1, a2, a3, b);
-                            if constexpr (PREC) f8_mma(s[pp][n], a0, a1, a2, a3, bl);
+                        for (int i = 0; i < D / 128; ++i) {
+                            const float2 u = bf ? F8Elem::from_bf16x2(y[hh][i].x) : F8Elem::from_f16x2(y[hh][i].x);
+                            const float2 w = bf ? F8Elem::from_bf16x2(y[hh][i].y) : F8Elem::from_f16x2(y[hh][i].y);
+                            x[hh][i] = make_float4(u.x, u.y, w.x, w.y);
                         }
+                }
+#pragma unroll
+                for (int hh = 0; hh < QB; ++hh) {
+                    const int h = h8 + hh;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i)
+                        top = max(max(top, max(__float_as_uint(x[hh][i].x) & 0x7FFFFFFFu,
+                                               __float_as_uint(x[hh][i].y) & 0x7FFFFFFFu)),
+                                  max(__float_as_uint(x[hh][i].z) & 0x7FFFFFFFu,
+                                      __float_as_uint(x[hh][i].w) & 0x7FFFFFFFu));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    const bool bad = top >= 0x7F800000u;
+                    const uint32_t e = max(top >> 23, 16u);
+                    const float mul = bad ? 0.f : __uint_as_float((262u - min(e, 254u)) << 23);
+                    const float cq =
+                        bad ? __uint_as_float(0x7FC00000u) : a.scale_log2e * __uint_as_float((e - 8u) << 23);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            if (8 * n + 2 * c + u == h) cqr[n][u] = cq;
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        float4 y = x[hh][i];
+                        if (bad) y = make_float4(0.f, 0.f, 0.f, 0.f);
+                        y.x *= mul, y.y *= mul, y.z *= mul, y.w *= mul;
+                        // elements 128 i + 4 lane ..: 64-element half, K step, 16-element lane part
+                        const int el = 128 * i + 4 * lane, ks = (el >> 6) * 4 + ((el >> 2) & 3), cc = (el >> 4) & 3;
+                        const uint2 f = make_uint2(f8_pack_f16(y.x, y.y), f8_pack_f16(y.z, y.w));
+                        const int at = (ks * NT + (h >> 3)) * 32 + (h & 7) * 4 + cc;
+                        qf[at] = f;
+                        if constexpr (PREC)
+                            qf[(D / 16) * NT * 32 + at] =
+                                make_uint2(f8_pack_rest(y.x, y.y, f.x), f8_pack_rest(y.z, y.w, f.y));
                     }
                 }
             }
 
-            // ---- scaled scores, references
-            float ev[PP][2];
-            bool ok[PP][2];
-            int nv[PP];
-            bool moved = false;
+            float o[D / 16][NT][4];
+            float r[NT][2], rv[NT][2], l[NT][2];
 #pragma unroll
-            for (int pp = 0; pp < PP; ++pp) {
-                nv[pp] = st * PP + pp < sg.p1 - sg.p0 ? info[stage * PP + pp] : 0;
-                const uint8_t* ex = sp + pp * C::PAGE + 32 * D;
+            for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float ks = f8_scale(ex[g + 8 * u]);
-                    const uint32_t eb = ex[16 + g + 8 * u];
-                    ev[pp][u] = eb == 255u ? __uint_as_float(0x7FC00000u) : (float)((int)eb - 127);
-                    ok[pp][u] = g + 8 * u < nv[pp];
+                for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) r[n][e] = rv[n][e] = kF8None, l[n][e] = 0.f;
+
+            for (int p = sg.p0 + sw * PP; p < sg.p1; p += sn * PP) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+                __syncwarp();  // the step has landed for every lane; the last step's stage (and qf) is settled
+                produce(stage == 0 ? S - 1 : stage - 1);
+                commit();
+                const uint8_t* sp = ring + stage * C::STEP;
+                // ---- scores
+                float s[PP][NT][4];
+#pragma unroll
+                for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[pp][n][0] = s[pp][n][1] = s[pp][n][2] = s[pp][n][3] = 0.f;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint4 ka[PP][2];
+#pragma unroll
+                    for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            ka[pp][u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + (g + 8 * u) * D +
+                                                                        (((4 * h + c) ^ ((g & 1) << 2)) << 4));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const int at = ((4 * h + k) * NT + n) * 32 + lane;
+                            const uint2 b = qf[at];
+                            uint2 bl = make_uint2(0u, 0u);
+                            if constexpr (PREC) bl = qf[(D / 16) * NT * 32 + at];
+#pragma unroll
+                            for (int pp = 0; pp < PP; ++pp) {
+                                const uint32_t w0 = k == 0 ? ka[pp][0].x : k == 1 ? ka[pp][0].y : k == 2 ? ka[pp][0].z : ka[pp][0].w;
+                                const uint32_t w1 = k == 0 ? ka[pp][1].x : k == 1 ? ka[pp][1].y : k == 2 ? ka[pp][1].z : ka[pp][1].w;
+                                const uint32_t a0 = f8_to_f16x2(w0), a1 = f8_to_f16x2(w1), a2 = f8_to_f16x2_hi(w0),
+                                               a3 = f8_to_f16x2_hi(w1);
+                                f8_mma(s[pp][n], a0, a1, a2, a3, b);
+                                if constexpr (PREC) f8_mma(s[pp][n], a0, a1, a2, a3, bl);
+                            }
+                        }
+                    }
+                }
+
+                // ---- weights.  p = 2^(x - r), w = 2^(x + ev - r') with x = score * ck
+                float ck[PP][2], ev[PP][2], pw[PP][NT][4], w[PP][NT][4], top = 0.f;
+                int nv[PP];
+                bool full = true;
+#pragma unroll
+                for (int pp = 0; pp < PP; ++pp) {
+                    nv[pp] = info[stage * PP + pp];
+                    full &= nv[pp] == 16;
+                    const uint8_t* ex = sp + pp * C::PAGE + 32 * D;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        // a vector stored as NaN has zero codes and E = 255: 0 * inf here
+                        ck[pp][u] = __uint_as_float((uint32_t)ex[g + 8 * u] << 23);
+                        const uint32_t eb = ex[16 + g + 8 * u];
+                        ev[pp][u] = eb == 255u ? __uint_as_float(0x7FC00000u)
+                                               : __uint_as_float(0x4B000000u | eb) - (8388608.f + 127.f);
+                    }
+                }
+                auto weights = [&]() {
+#pragma unroll
+                    for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float x = s[pp][n][2 * u + e], f = ck[pp][u] * cqr[n][e];
+                                    pw[pp][n][2 * u + e] = f8_exp2(fmaf(x, f, -r[n][e]));
+                                    w[pp][n][2 * u + e] = f8_exp2(fmaf(x, f, ev[pp][u] - rv[n][e]));
+                                }
+                    if (!full) {
+#pragma unroll
+                        for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (g + 8 * (i >> 1) >= nv[pp]) pw[pp][n][i] = w[pp][n][i] = 0.f;
+                    }
+                };
+                weights();
+#pragma unroll
+                for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(pw[pp][n][i], w[pp][n][i]));
+                if (__any_sync(0xffffffffu, top > kF8Most)) {
+                    // a weight has outgrown its reference: move the references
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float& x = s[pp][n][2 * u + e];
-                            x = ok[pp][u] ? x * cqr[n][e] * ks : -INFINITY;
-                            moved |= x > r[n][e] + kF8Slack || x + ev[pp][u] > rv[n][e] + kF8Slack;
+                            float m = r[n][e], mv = rv[n][e] + kF8Head;
+#pragma unroll
+                            for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+                                    if (g + 8 * u < nv[pp]) {
+                                        const float x = s[pp][n][2 * u + e] * (ck[pp][u] * cqr[n][e]);
+                                        m = fmaxf(m, x);
+                                        mv = fmaxf(mv, x + ev[pp][u]);
+                                    }
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 16)) - kF8Head;
+                            const float fv = f8_exp2(rv[n][e] - mv);
+                            l[n][e] *= f8_exp2(r[n][e] - m);
+                            r[n][e] = m;
+                            rv[n][e] = mv;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) o[i][n][e] *= fv, o[i][n][2 + e] *= fv;
                         }
+                    weights();
                 }
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                uint2 pb[PP][NT], pl[PP][NT];  // as the B operand (tokens x heads)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int pp = 0; pp < PP; ++pp)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float m = -INFINITY, mv = -INFINITY;
-#pragma unroll
-                        for (int pp = 0; pp < PP; ++pp)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                m = fmaxf(m, s[pp][n][2 * u + e]);
-                                mv = fmaxf(mv, ok[pp][u] ? s[pp][n][2 * u + e] + ev[pp][u] : -INFINITY);
-                            }
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) {
-                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, x));
-                        }
-                        m = fmaxf(r[n][e], m);
-                        mv = fmaxf(rv[n][e], mv - kF8Head);
-                        const float f = r[n][e] == -INFINITY ? 0.f : f8_exp2(r[n][e] - m);
-                        const float fv = rv[n][e] == -INFINITY ? 0.f : f8_exp2(rv[n][e] - mv);
-                        r[n][e] = m;
-                        rv[n][e] = mv;
-                        l[n][e] *= f;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) o[i][n][e] *= fv, o[i][n][2 + e] *= fv;
+                    for (int n = 0; n < NT; ++n) {
+                        l[n][0] += pw[pp][n][0] + pw[pp][n][2];
+                        l[n][1] += pw[pp][n][1] + pw[pp][n][3];
+                        const float* x = w[pp][n];
+                        const uint32_t h0 = f8_pack_f16(x[0], x[1]), h1 = f8_pack_f16(x[2], x[3]);
+                        pb[pp][n] = make_uint2(f8_transpose(h0), f8_transpose(h1));
+                        if constexpr (PREC)
+                            pl[pp][n] = make_uint2(f8_transpose(f8_pack_rest(x[0], x[1], h0)),
+                                                   f8_transpose(f8_pack_rest(x[2], x[3], h1)));
                     }
-            }
 
-            // ---- weights, as the B operand (tokens x heads)
-            uint2 pb[PP][NT], pl[PP][NT];
-#pragma unroll
-            for (int pp = 0; pp < PP; ++pp)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float w[4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = s[pp][n][2 * u + e];
-                            l[n][e] += ok[pp][u] ? f8_exp2(x - r[n][e]) : 0.f;
-                            w[2 * u + e] = ok[pp][u] ? f8_exp2(x + ev[pp][u] - rv[n][e]) : 0.f;
-                        }
-                    const uint32_t h0 = f8_pack_f16(w[0], w[1]), h1 = f8_pack_f16(w[2], w[3]);
-                    pb[pp][n] = make_uint2(f8_transpose(h0), f8_transpose(h1));
-                    if constexpr (PREC)
-                        pl[pp][n] = make_uint2(f8_transpose(f8_pack_rest(w[0], w[1], h0)),
-                                               f8_transpose(f8_pack_rest(w[2], w[3], h1)));
+                // ---- values: token pairs (2c, 2c + 1) and (2c + 8, 2c + 9) of 16 coordinates
+                if (!full) {
+                    // rows behind the last token may hold anything, NaN codes too
+#pragma unroll 1
+                    for (int idx = lane; idx < PP * 16 * (D / 16); idx += 32) {
+                        const int pp = idx / D, t = idx / (D / 16) % 16;
+                        if (t >= info[stage * PP + pp])
+                            *reinterpret_cast<uint4*>(ring + stage * C::STEP + pp * C::PAGE + 16 * D + (idx % D) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
                 }
-
-            // ---- values: token pairs (2c, 2c + 1) and (2c + 8, 2c + 9) of 16 coordinates
 #pragma unroll
-            for (int pp = 0; pp < PP; ++pp) {
-                if (nv[pp] == 0) continue;
+                for (int pp = 0; pp < PP; ++pp) {
+                    if (nv[pp] == 0) continue;
 #pragma unroll
-                for (int h = 0; h < D / 128; ++h) {
-                    uint4 v[4];
+                    for (int h = 0; h < D / 128; ++h) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int t = 2 * c + (u & 1) + 8 * (u >> 1);
-                        v[u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + 16 * D + t * D +
-                                                               (((8 * h + g) ^ (t & 6)) << 4));
-                        // rows behind the last token may hold anything
-                        if (nv[pp] < 16 && t >= nv[pp]) v[u] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                        for (int u = 0; u < 4; ++u) {
+                            const int t = 2 * c + (u & 1) + 8 * (u >> 1);
+                            v[u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + 16 * D + t * D +
+                                                                   (((8 * h + g) ^ (t & 6)) << 4));
+                        }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t t0 = k == 0 ? v[0].x : k == 1 ? v[0].y : k == 2 ? v[0].z : v[0].w;
-                        const uint32_t t1 = k == 0 ? v[1].x : k == 1 ? v[1].y : k == 2 ? v[1].z : v[1].w;
-                        const uint32_t t2 = k == 0 ? v[2].x : k == 1 ? v[2].y : k == 2 ? v[2].z : v[2].w;
-                        const uint32_t t3 = k == 0 ? v[3].x : k == 1 ? v[3].y : k == 2 ? v[3].z : v[3].w;
-                        const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
-                        const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t t0 = k == 0 ? v[0].x : k == 1 ? v[0].y : k == 2 ? v[0].z : v[0].w;
+                            const uint32_t t1 = k == 0 ? v[1].x : k == 1 ? v[1].y : k == 2 ? v[1].z : v[1].w;
+                            const uint32_t t2 = k == 0 ? v[2].x : k == 1 ? v[2].y : k == 2 ? v[2].z : v[2].w;
+                            const uint32_t t3 = k == 0 ? v[3].x : k == 1 ? v[3].y : k == 2 ? v[3].z : v[3].w;
+                            const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
+                            const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint32_t x = m ? x1 : x0, y = m ? y1 : y0;
-                            const uint32_t a0 = f8_to_f16x2(x), a1 = f8_to_f16x2_hi(x), a2 = f8_to_f16x2(y),
-                                           a3 = f8_to_f16x2_hi(y);
-                            const int i = 8 * h + 2 * k + m;
+                            for (int m = 0; m < 2; ++m) {
+                                const uint32_t x = m ? x1 : x0, y = m ? y1 : y0;
+                                const uint32_t a0 = f8_to_f16x2(x), a1 = f8_to_f16x2_hi(x), a2 = f8_to_f16x2(y),
+                                               a3 = f8_to_f16x2_hi(y);
+                                const int i = 8 * h + 2 * k + m;
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                f8_mma(o[i][n], a0, a1, a2, a3, pb[pp][n]);
-                                if constexpr (PREC) f8_mma(o[i][n], a0, a1, a2, a3, pl[pp][n]);
+                                for (int n = 0; n < NT; ++n) {
+                                    f8_mma(o[i][n], a0, a1, a2, a3, pb[pp][n]);
+                                    if constexpr (PREC) f8_mma(o[i][n], a0, a1, a2, a3, pl[pp][n]);
+                                }
                             }
                         }
                     }
                 }
+                stage = stage == S - 1 ? 0 : stage + 1;
             }
-            stage = stage == S - 1 ? 0 : stage + 1;
-        }
 
-        // ---- the warps' sums become the block's, in warp order
+            // ---- the segment's sums
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
-                if (g == 0) {
-                    float* p = ref + (warp * HEADS + 8 * n + 2 * c + e) * 3;
-                    p[0] = r[n][e];
-                    p[1] = rv[n][e];
-                    p[2] = l[n][e];
-                }
-            }
-        __syncthreads();
+                    for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+            if (!solo) {
+                // the warps' sums, (0 + 2) + (1 + 3), in warp 0's registers
+                float4* buf = reinterpret_cast<float4*>(smem + C::off_q);
+                if (g == 0)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float m = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < W; ++w) m = fmaxf(m, ref[(w * HEADS + 8 * n + 2 * c + e) * 3 + 1]);
-                const float f = rv[n][e] == -INFINITY ? (l[n][e] == 0.f ? 0.f : 1.f) : f8_exp2(rv[n][e] - m);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) o[i][n][e] *= f, o[i][n][2 + e] *= f;
-            }
-        for (int w = 0; w < W; ++w) {
-            if (warp == w) {
+                        for (int e = 0; e < 2; ++e)
+                            s_ref[warp][8 * n + 2 * c + e] = make_float4(r[n][e], rv[n][e], l[n][e], 0.f);
+                __syncthreads();
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float* p = buf + (8 * n + 2 * c + e) * C::BUF_LD + 2 * g;
+                        float R = kF8None, Rv = kF8None, L = 0.f;
+                        float4 m[W];
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            float2 x = make_float2(o[i][n][e], o[i][n][2 + e]);
-                            float2* at = reinterpret_cast<float2*>(p + 16 * i);
-                            if (w > 0) x.x += at->x, x.y += at->y;
-                            *at = x;
+                        for (int w = 0; w < W; ++w) {
+                            m[w] = s_ref[w][8 * n + 2 * c + e];
+                            R = fmaxf(R, m[w].x);
+                            Rv = fmaxf(Rv, m[w].y);
                         }
-                    }
-            }
-            __syncthreads();
-        }
-        // buffer position of coordinate x of a 128-wide half: 16 (x / 2 % 8) + 2 (x / 16) + x % 2
-        auto pos = [](int x) { return (x & ~127) + ((x >> 1) & 7) * 16 + ((x >> 4) & 7) * 2 + (x & 1); };
-        auto head_sum = [&](int h, float& R, float& Rv, float& L) {
-            R = Rv = -INFINITY;
-            L = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                R = fmaxf(R, ref[(w * HEADS + h) * 3]);
-                Rv = fmaxf(Rv, ref[(w * HEADS + h) * 3 + 1]);
-            }
+                        for (int w = 0; w < W; ++w) L += m[w].z * f8_exp2(m[w].x - R);
+                        const float f = f8_exp2(rv[n][e] - Rv);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float* p = ref + (w * HEADS + h) * 3;
-                L += p[0] == -INFINITY ? p[2] : p[2] * f8_exp2(p[0] - R);
-            }
-        };
-        // 2^(r' - r) / l; no token: 0.  (A NaN sum keeps r at -inf: NaN.)
-        auto norm = [](float R, float Rv, float L) {
-            return L == 0.f ? 0.f : (R == -INFINITY || Rv == -INFINITY ? 1.f : exp2f(Rv - R)) / L;
-        };
-        const bool whole = sg.p0 == 0 && sg.p1 == sg.np;
-        if (whole) {
-            for (int i = tid; i < nh * (D / 2); i += kF8Threads) {
-                const int h = i / (D / 2), x = 2 * (i - h * (D / 2));
-                float R, Rv, L;
-                head_sum(h, R, Rv, L);
-                const float f = norm(R, Rv, L);
-                const float2 v = *reinterpret_cast<const float2*>(buf + h * C::BUF_LD + pos(x));
-                f8_store2(a.out, ((int64_t)sg.b * a.q_heads + qh0 + h) * D + x, L == 0.f ? 0.f : v.x * f,
-                          L == 0.f ? 0.f : v.y * f, a.out_dtype);
-            }
-        } else {
-            // ---- a part: to the workspace; the last block of the unit joins
-            // the unit [v0, v1) of pages this segment belongs to, in run order
-            const long long here = u1 - u0 - cons.left - (sg.p1 - sg.p0);  // pages of this run before the segment
-            const long long v0 = u0 + here - sg.p0, v1 = v0 + sg.np;
-            const long long i0 = ((v0 + 1) * N - 1) / total, i1 = (v1 * N - 1) / total;
-            const int slot = blockIdx.x * 2 + (u0 >= v0 ? 0 : 1);
-            float* part = a.part + (int64_t)slot * HEADS * D;
-            float* meta = a.meta + (int64_t)slot * HEADS * 4;
-            for (int i = tid; i < nh * D; i += kF8Threads) {
-                const int h = i / D, x = i - h * D;
-                part[i] = buf[h * C::BUF_LD + x];  // buffer order
-            }
-            if (tid < nh) {
-                float R, Rv, L;
-                head_sum(tid, R, Rv, L);
-                meta[4 * tid] = R;
-                meta[4 * tid + 1] = Rv;
-                meta[4 * tid + 2] = L;
-            }
-            __threadfence();
-            __syncthreads();
-            uint32_t* cnt = a.cnt + (int64_t)sg.b * nj + sg.j;
-            if (tid == 0) {
-                const uint32_t old = atomicAdd(cnt, 1u);
-                s_last = old == (uint32_t)(i1 - i0);
-                if (s_last) *cnt = 0;  // ready for the next call
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                auto slot_of = [&](long long i) { return (int)i * 2 + (i * total / N >= v0 ? 0 : 1); };
-                for (int i = tid; i < nh * (D / 2); i += kF8Threads) {
-                    const int h = i / (D / 2), x = 2 * (i - h * (D / 2));
-                    float R = -INFINITY, Rv = -INFINITY;
-                    for (long long k = i0; k <= i1; ++k) {
-                        const float* m = a.meta + ((int64_t)slot_of(k) * HEADS + h) * 4;
-                        R = fmaxf(R, __ldcg(m));
-                        Rv = fmaxf(Rv, __ldcg(m + 1));
+                        for (int i = 0; i < D / 16; ++i) o[i][n][e] *= f, o[i][n][2 + e] *= f;
+                        r[n][e] = R;
+                        rv[n][e] = Rv;
+                        l[n][e] = L;
                     }
-                    float L = 0.f, v0f = 0.f, v1f = 0.f;
-                    for (long long k = i0; k <= i1; ++k) {
-                        const int64_t sl = slot_of(k);
-                        const float* m = a.meta + (sl * HEADS + h) * 4;
-                        const float mr = __ldcg(m), mv = __ldcg(m + 1), ml = __ldcg(m + 2);
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + (sl * HEADS + h) * D + pos(x)));
-                        L += mr == -INFINITY ? ml : ml * f8_exp2(mr - R);
-                        const float f = mv == -INFINITY ? 1.f : f8_exp2(mv - Rv);
-                        v0f += v.x * f;
-                        v1f += v.y * f;
-                    }
-                    const float f = norm(R, Rv, L);
-                    f8_store2(a.out, ((int64_t)sg.b * a.q_heads + qh0 + h) * D + x, L == 0.f ? 0.f : v0f * f,
-                              L == 0.f ? 0.f : v1f * f, a.out_dtype);
-                }
+                auto put = [&](int at) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            buf[at * C::ITEMS + (i * NT + n) * 32 + lane] =
+                                make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+                };
+                auto add = [&](int at) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float4 x = buf[at * C::ITEMS + (i * NT + n) * 32 + lane];
+                            o[i][n][0] += x.x, o[i][n][1] += x.y, o[i][n][2] += x.z, o[i][n][3] += x.w;
+                        }
+                };
+                if (warp >= 2) put(warp - 2);
+                __syncthreads();
+                if (warp < 2) add(warp);
+                if (warp == 1) put(1);
+                __syncthreads();
+                if (warp == 0) add(1);
+                __syncthreads();  // the query operands' place is free
             }
+            if (!solo && warp != 0) {
+                // warp 0 has the sums
+            } else if (sg.p0 == 0 && sg.p1 == sg.np()) {
+                // lane (g, c): coordinates 16 g .. 16 g + 15 of each 128, heads 2c and 2c + 1
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int h = 8 * n + 2 * c + e;
+                        const float f = f8_norm(r[n][e], rv[n][e], l[n][e]);
+                        if (h < nh)
+#pragma unroll
+                            for (int i0 = 0; i0 < D / 16; i0 += 8) {
+                                float v[16];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    v[2 * i] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][e] * f;
+                                    v[2 * i + 1] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][2 + e] * f;
+                                }
+                                f8_store16(a.out, ((int64_t)sg.b * a.q_heads + qh0 + h) * D + 16 * i0 + 16 * g, v,
+                                           a.out_dtype);
+                            }
+                    }
+            } else {
+                const int which = u0 >= u1 - cons.left - sg.p1 ? 0 : 1;  // 0: the run starts in this unit
+                const int slot = 2 * (int)run + which;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        a.part[(int64_t)slot * C::ITEMS + (i * NT + n) * 32 + lane] =
+                            make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+                if (g == 0)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            a.meta[slot * HEADS + 8 * n + 2 * c + e] = make_float4(r[n][e], rv[n][e], l[n][e], 0.f);
+                if (lane == 0) s_part[warp][which] = sg;
+            }
+            __syncwarp();  // qf is free
         }
-        __syncthreads();  // query operands, buffer and references are free
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // ---- joins
+    __threadfence();
+    __syncthreads();  // the rings are free, the block's partial sums visible
+    F8JoinSmem& js = *reinterpret_cast<F8JoinSmem*>(smem);
+    // the sums of `count` <= 32 slots (s0, then s1 + st, s1 + 2 st, ...) into slot s0, or out
+    auto join = [&](int count, int s0, int s1, int st, bool fin, const F8Seg& sg) {
+        auto slot = [&](int k) { return (int64_t)(k == 0 ? s0 : s1 + k * st); };
+        // lane k: slot k
+        for (int h = warp; h < HEADS; h += W) {
+            float4 m = make_float4(kF8None, kF8None, 0.f, 0.f);
+            if (lane < count) m = __ldcg(a.meta + slot(lane) * HEADS + h);
+            const float R = warp_max(m.x), Rv = warp_max(m.y);
+            const float L = warp_sum(m.z * f8_exp2(m.x - R));
+            js.fac[lane][h] = f8_exp2(m.y - Rv);
+            if (lane == 0) js.tot[h] = make_float4(R, Rv, L, f8_norm(R, Rv, L));
+        }
+        const int kvh = sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
+        const int nh = min(a.hp, a.group - hg * a.hp), qh0 = kvh * a.group + hg * a.hp;
+#pragma unroll 1
+        for (int it = tid; it < C::ITEMS; it += kF8Threads) {
+            const int ln = it & 31, n = (it >> 5) % NT, i = (it >> 5) / NT, h = 8 * n + 2 * (ln & 3);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int k0 = 0; k0 < count; k0 += 16) {
+                float4 x[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    x[k] = k0 + k < count ? __ldcg(a.part + slot(k0 + k) * C::ITEMS + it) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (it == tid && k0 == 0) __syncthreads();  // the factors (every thread has a first item)
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k0 + k < count) {
+                        const float2 f = *reinterpret_cast<const float2*>(&js.fac[k0 + k][h]);
+                        v.x += x[k].x * f.x, v.y += x[k].y * f.y, v.z += x[k].z * f.x, v.w += x[k].w * f.y;
+                    }
+            }
+            if (!fin) {
+                a.part[(int64_t)s0 * C::ITEMS + it] = v;
+            } else if (h < nh) {
+                const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
+                const int64_t at = ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
+                f8_store2(a.out, at, t0.z == 0.f ? 0.f : v.x * t0.w, t0.z == 0.f ? 0.f : v.z * t0.w, a.out_dtype);
+                if (h + 1 < nh)
+                    f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v.y * t1.w, t1.z == 0.f ? 0.f : v.w * t1.w,
+                              a.out_dtype);
+            }
+        }
+        if (!fin) {
+            if (tid < HEADS) a.meta[s0 * HEADS + tid] = js.tot[tid];
+            __threadfence();
+        }
+        __syncthreads();
+    };
+    // one more of `all` has arrived at *cnt: is it the last?  (leaves the counter ready for the next call)
+    auto arrive = [&](uint32_t* cnt, int all) {
+        if (tid == 0) {
+            s_last = atomicAdd(cnt, 1u) == (uint32_t)(all - 1);
+            if (s_last) *cnt = 0;
+        }
+        __syncthreads();
+        const bool last = s_last != 0;
+        __threadfence();
+        __syncthreads();
+        return last;
+    };
+    for (int x = 0; x < 2 * W;) {
+        const F8Seg sg = s_part[x >> 1][x & 1];
+        if (sg.b < 0) {
+            ++x;
+            continue;
+        }
+        // the segments of this unit in this block (x0, and the first ones of the next warps)
+        const int x0 = x;
+        int count = 1, p1 = sg.p1;
+        for (++x; x < 2 * W; ++x) {
+            const F8Seg& nx = s_part[x >> 1][x & 1];
+            if (nx.b < 0) continue;
+            if (nx.b != sg.b || nx.j != sg.j) break;
+            p1 = nx.p1;
+            ++count;
+        }
+        // the blocks of this unit, from the one that holds its first page on
+        const int w0 = x0 >> 1;
+        const uint32_t i = run0 + w0;
+        const int v0 = (x0 & 1) ? (int)runs.start(i + 1) - sg.p1 : (int)runs.start(i) - sg.p0, v1 = v0 + sg.np();
+        const int i0 = (int)runs.owner(v0), i1 = (int)runs.owner(v1 - 1);
+        const int c0 = i0 / rpb, c1 = i1 / rpb, n = c1 - c0 + 1, st = 2 * rpb;  // st: slots of a block
+        const int first = 2 * i0 + ((int)runs.start(i0) >= v0 ? 0 : 1);         // slot of block c0
+        const int gi = ((int)blockIdx.x - c0) / kF8Join, g0 = c0 + gi * kF8Join;
+        // this block's sums, then those of its group of blocks (where there are
+        // more than one group), then those of all blocks or groups
+        int jn = count, j0 = 2 * (int)run0 + x0, j1 = 2 * (int)(run0 + w0), jst = 2;
+        bool fin = sg.p0 == 0 && p1 == sg.np();
+        for (bool grouped = n <= kF8Join;; grouped = true) {
+            if (jn > 1 || fin) join(jn, j0, j1, jst, fin, sg);
+            if (fin) break;
+            uint32_t* cnt;
+            if (!grouped) {
+                jn = min(kF8Join, c1 - g0 + 1);
+                j0 = gi == 0 ? first : st * g0;
+                j1 = st * g0;
+                jst = st;
+                cnt = a.gcnt + j0;
+            } else {
+                fin = true;
+                jn = n <= kF8Join ? n : (n + kF8Join - 1) / kF8Join;
+                j0 = first;
+                j1 = st * c0;
+                jst = n <= kF8Join ? st : st * kF8Join;
+                cnt = a.cnt + (int64_t)sg.b * nj + sg.j;
+            }
+            if (!arrive(cnt, jn)) break;
+        }
+    }
 }
 
 template <int D, int NT, bool PREC>
@@ -640,9 +808,10 @@ static tq_status launch_f8_decode(const F8DecodeArgs& a, cudaStream_t s) {
     st = ensure_dynamic_smem((const void*)f8_decode_kernel<D, NT, PREC>, C::total, "f8_decode_kernel");
     if (st != TQ_OK) return st;
     // one wave of resident blocks
-    const int grid = std::min(C::CTAS * sms, kF8MaxCtas);
-    f8_decode_kernel<D, NT, PREC><<<grid, kF8Threads, C::total, s>>>(a);
-    return cuda_status(cudaGetLastError());
+    const int grid = C::CTAS * std::min(sms, kF8MaxSms);
+    // launched programmatically: the launch overlaps the previous kernel's end,
+    // and the kernel waits for it before its first read
+    return cuda_status(launch_pdl(true, f8_decode_kernel<D, NT, PREC>, dim3(grid), dim3(kF8Threads), C::total, s, a));
 }
 
 template <int D>
@@ -676,6 +845,7 @@ extern "C" tq_status tq_f8_decode_attention(const tq_f8_cache* c, const void* q,
     a.out = out;
     a.err = c->err;
     a.cnt = c->cnt;
+    a.gcnt = c->gcnt;
     a.part = c->part;
     a.meta = c->meta;
     a.num_blocks = c->cfg.num_blocks;
