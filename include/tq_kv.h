@@ -511,6 +511,62 @@ tq_status tq_f8_decode_attention(const tq_f8_cache* cache, const void* q, int q_
 /* Read and clear the handle's device error word, like tq_get_device_error. */
 tq_status tq_f8_get_device_error(const tq_f8_cache* cache, uint32_t* flags, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Prompt attention: packed prompts of different lengths over exact 16-bit keys
+ * and values, before (or beside) anything is stored in a cache.  The pages have
+ * no counterpart.  With cu_k longer than cu_q it is the next chunk of a prompt
+ * whose earlier keys and values were read back with tq_f8_load.
+ * ------------------------------------------------------------------------ */
+typedef struct tq_prompt_config {
+    int32_t head_dim;     /* d, 128 or 256 */
+    int32_t num_kv_heads; /* H_kv >= 1 */
+    int32_t num_q_heads;  /* H_q = G * H_kv, 1 <= G <= 128; q head h reads KV head h / G */
+    int32_t dtype;        /* TQ_DTYPE_BF16 or TQ_DTYPE_F16, of q, k, v and out */
+    int32_t max_batch;    /* sequences per call */
+    int32_t max_tokens;   /* query rows per call */
+} tq_prompt_config;
+
+typedef struct tq_prompt tq_prompt;
+
+/* Bytes of the caller-owned device workspace of a configuration. */
+tq_status tq_prompt_sizes(const tq_prompt_config* cfg, size_t* workspace_bytes);
+
+/*
+ * Make a handle that records workspace_dev (>= workspace_bytes, 16-byte
+ * aligned); synchronises `stream` once (set-up only).  As with the caches, calls
+ * and captured graphs of one handle must not overlap on the GPU.
+ */
+tq_status tq_prompt_create(const tq_prompt_config* cfg, void* workspace_dev, void* stream, tq_prompt** out);
+tq_status tq_prompt_destroy(tq_prompt* p);
+
+/*
+ * For sequence b, query row i of its lq = cu_q[b+1] - cu_q[b] and key j of its
+ * lk = cu_k[b+1] - cu_k[b] (rows cu_q[b] + i of q, cu_k[b] + j of k and v):
+ *   out_i = sum_j softmax_j(scale <q_i, k_j>) v_j   per query head,
+ *   lse_i = ln sum_j exp(scale <q_i, k_j>),
+ * over all keys j, or, if causal, over j <= i + lk - lq (the last query sees
+ * the last key).  A row that sees no key gets out = 0 and lse = -inf.  A key or
+ * value that a row does not see has no influence on it, whatever it holds.
+ *   q          device [n_q][H_q][d], row t starting q_stride elements after row
+ *              t - 1; k, v device [n_k][H_kv][d], alike.  Bases and strides:
+ *              multiples of 16 bytes
+ *   cu_q/cu_k  device int32 [batch + 1], non-decreasing, within [0, n_q] and
+ *              [0, n_k] (otherwise clamped, TQ_DEVERR_CHUNK, and the outputs of
+ *              the sequences concerned are unspecified)
+ *   scale      <= 0 means 1/sqrt(d)
+ *   out        device [n_q][H_q][d], 16-byte aligned; lse device fp32
+ *              [n_q][H_q] or NULL.  Rows no sequence names are left as they were
+ * Products and sums in fp32, the probabilities rounded to dtype for the value
+ * product (their sum is of the unrounded ones).  n_q == 0 is a no-op.
+ */
+tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                              int batch, int n_q, int n_k, float scale, int causal, void* out, float* lse,
+                              void* stream);
+
+/* Read and clear the handle's device error word, like tq_get_device_error. */
+tq_status tq_prompt_get_device_error(const tq_prompt* p, uint32_t* flags, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,8 @@ __all__ = [
     "TQ_PROF_STORE", "TQ_PROF_DECODE_SPLIT", "tq_check_wait_timeout", "tq_store_decode_attention",
     "TQ_DTYPE_F16", "tq_f8_config", "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store",
     "tq_f8_load", "tq_f8_decode_attention", "tq_f8_get_device_error", "TQF8Cache",
+    "tq_prompt_config", "tq_prompt_sizes", "tq_prompt_create", "tq_prompt_destroy", "tq_prompt_attention",
+    "tq_prompt_get_device_error", "TQPrompt",
 ]
 
 TQ_DTYPE_F32, TQ_DTYPE_BF16, TQ_DTYPE_F16 = 0, 1, 2
@@ -43,6 +45,7 @@ EXPORTED = [
     "tq_store_decode_attention",
     "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store", "tq_f8_load",
     "tq_f8_decode_attention", "tq_f8_get_device_error",
+    "tq_prompt_sizes", "tq_prompt_create", "tq_prompt_destroy", "tq_prompt_attention", "tq_prompt_get_device_error",
 ]
 TQ_PROF_STORE, TQ_PROF_DECODE_SPLIT = 0, 1
 
@@ -98,6 +101,20 @@ class tq_f8_config(ctypes.Structure):
         super().__init__(**{**dict(block_size=16, max_batch=1), **kw})
 
 
+class tq_prompt_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("max_tokens", ctypes.c_int32),
+    ]
+
+    def __init__(self, **kw):
+        super().__init__(**{**dict(dtype=TQ_DTYPE_BF16, max_batch=1), **kw})
+
+
 _LIB = None
 _P = ctypes.c_void_p
 
@@ -151,6 +168,15 @@ def load_library():
             "tq_f8_decode_attention": (
                 i32, [_P, _P, i32, i64, _P, _P, _P, ctypes.c_float, i32, _P, i32, _P]),
             "tq_f8_get_device_error": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
+        })
+        pcp = ctypes.POINTER(tq_prompt_config)
+        sig.update({
+            "tq_prompt_sizes": (i32, [pcp, sz]),
+            "tq_prompt_create": (i32, [pcp, _P, _P, ctypes.POINTER(_P)]),
+            "tq_prompt_destroy": (i32, [_P]),
+            "tq_prompt_attention": (
+                i32, [_P, _P, _P, _P, i64, i64, i64, _P, _P, i32, i32, i32, ctypes.c_float, i32, _P, _P, _P]),
+            "tq_prompt_get_device_error": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
         })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -457,76 +483,93 @@ class TQCache:
             pass
 
 
-# ------------------------------------------------------------- 8-bit cache
+# ------------------------------------- 8-bit cache and prompt attention
+# These calls run for a few microseconds on the GPU, so their checks are kept
+# short: every tensor is asked for its device index, shape and strides once.
+_TORCH = None
 _DTYPE_CODES = None
 
 
-def _code(t, name):
-    """dtype code of a tensor of the 8-bit cache and prompt calls."""
-    global _DTYPE_CODES
-    if _DTYPE_CODES is None:
+def _torch():
+    global _TORCH, _DTYPE_CODES
+    if _TORCH is None:
         import torch
 
+        _TORCH = torch
         _DTYPE_CODES = {torch.float32: TQ_DTYPE_F32, torch.bfloat16: TQ_DTYPE_BF16, torch.float16: TQ_DTYPE_F16}
+    return _TORCH
+
+
+def _code(t, name):
+    _torch()
     code = _DTYPE_CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}: float32, bfloat16 or float16")
     return code
 
 
-def _rows(t, name, heads, d):
-    """Pointer and row stride of a CUDA tensor [rows, heads, d] whose rows are
-    contiguous (the rows themselves may lie apart, as in a fused projection)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(t.shape)}")
+def _wrong_device(t, name, dev):
+    if dev is None or dev < 0 or not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor")
+    return ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _rows(t, name, heads, d, dev):
+    """Pointer and row stride of a tensor [rows, heads, d] on device `dev` whose
+    rows are contiguous (they may lie apart, as in a fused projection)."""
+    if t.get_device() != dev or dev < 0:
+        raise _wrong_device(t, name, dev)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(shape)}")
     row, head, el = t.stride()
-    if el != 1 or (heads > 1 and head != d):
+    if el != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the [{heads}, {d}] part of a row must be contiguous")
-    if t.shape[0] <= 1:
+    if row < heads * d:
+        if shape[0] > 1:
+            raise ValueError(f"{name}: rows overlap (row stride {row})")
         row = heads * d
-    elif row < heads * d:
-        raise ValueError(f"{name}: rows overlap (row stride {row})")
     return t.data_ptr(), row
 
 
-def _out_rows(t, name, rows, heads, d):
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {heads}, {d}], got {tuple(t.shape)}")
+def _plain(t, name, shape, dtype, dev):
+    """Pointer of a contiguous tensor of exactly this shape."""
+    if t.get_device() != dev or dev < 0:
+        raise _wrong_device(t, name, dev)
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}, strides {t.stride()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
 
 
-def _index(t, name, dtype, least):
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+def _index(t, name, dtype, least, dev):
+    """Pointer of a contiguous index tensor of at least this many entries."""
+    if t.get_device() != dev or dev < 0:
+        raise _wrong_device(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() < least:
-        raise ValueError(f"{name} must have at least {least} entries, got {t.numel()}")
+    if t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with at least {least} entries, got {list(t.shape)}")
     return t.data_ptr()
 
 
-def _table(t, batch, columns):
-    import torch
-
+def _table(t, batch, columns, dev):
     if t.dim() != 2 or t.shape[0] < batch or t.shape[1] != columns:
-        raise ValueError(f"block_table must be [>= {batch}, {columns}], got {tuple(t.shape)}")
-    return _index(t, "block_table", torch.int32, 0)
+        raise ValueError(f"block_table must be [>= {batch}, {columns}], got {list(t.shape)}")
+    return _index(t, "block_table", _TORCH.int32, 0, dev)
 
 
-def _same_device(device, **tensors):
-    """Every tensor on the handle's device, which must be the current one (the
-    calls launch on the current device)."""
-    import torch
-
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the handle's buffers on {device}")
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"the current device is cuda:{torch.cuda.current_device()}, the handle's buffers are on {device}")
+def _launch_stream(stream, dev):
+    """The stream to launch on.  Calls launch on the current device, which must be the tensors'."""
+    cuda = _TORCH._C
+    if cuda._cuda_getDevice() != dev:
+        raise ValueError(f"the current device is cuda:{cuda._cuda_getDevice()}, the tensors are on cuda:{dev}")
+    if stream is None:
+        return cuda._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def tq_f8_cache_sizes(cfg):
@@ -549,49 +592,54 @@ def tq_f8_cache_destroy(handle):
 def tq_f8_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
     """k, v [T, H_kv, d] (f32, bf16 or f16, same dtype; rows may lie apart);
     slot_mapping int64 [T]."""
-    import torch
-
+    dt = _code(k, "k")
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have the same shape and dtype")
-    kp, ks = _rows(k, "k", cfg.num_kv_heads, cfg.head_dim)
-    vp, vs = _rows(v, "v", cfg.num_kv_heads, cfg.head_dim)
+    dev = cache.get_device() if cache is not None else k.get_device()
+    heads, d = cfg.num_kv_heads, cfg.head_dim
+    kp, ks = _rows(k, "k", heads, d, dev)
+    vp, vs = _rows(v, "v", heads, d, dev)
     n = k.shape[0]
-    _check(load_library().tq_f8_store(handle, kp, vp, _code(k, "k"), ks, vs, n,
-                                      _index(slot_mapping, "slot_mapping", torch.int64, n), _dev(cache, "cache"),
-                                      _stream_ptr(stream)), "tq_f8_store")
+    st = load_library().tq_f8_store(handle, kp, vp, dt, ks, vs, n,
+                                    _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _dev(cache, "cache"),
+                                    _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_f8_store")
 
 
 def tq_f8_load(handle, cfg, cache, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
     """block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]; cu_out
     int32 [B] (or more): first row of each sequence in k_out, v_out [rows,
     H_kv, d] (f32, bf16 or f16)."""
-    import torch
-
+    dt = _code(k_out, "k_out")
     if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
         raise ValueError("k_out and v_out must have the same shape and dtype")
-    b, n = seq_lens.shape[0], k_out.shape[0]
-    _check(load_library().tq_f8_load(
-        handle, _dev(cache, "cache"),
-        _table(block_table, b, cfg.max_blocks_per_seq),
-        _index(seq_lens, "seq_lens", torch.int32, b), _index(cu_out, "cu_out", torch.int32, b), b, n,
-        _out_rows(k_out, "k_out", None, cfg.num_kv_heads, cfg.head_dim),
-        _out_rows(v_out, "v_out", n, cfg.num_kv_heads, cfg.head_dim), _code(k_out, "k_out"), _stream_ptr(stream)),
-        "tq_f8_load")
+    dev = cache.get_device() if cache is not None else k_out.get_device()
+    b, n, i32 = seq_lens.shape[0], k_out.shape[0], _TORCH.int32
+    shape = (n, cfg.num_kv_heads, cfg.head_dim)
+    st = load_library().tq_f8_load(
+        handle, _dev(cache, "cache"), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        _index(seq_lens, "seq_lens", i32, b, dev), _index(cu_out, "cu_out", i32, b, dev), b, n,
+        _plain(k_out, "k_out", shape, None, dev), _plain(v_out, "v_out", shape, None, dev), dt,
+        _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_f8_load")
 
 
 def tq_f8_decode_attention(handle, cfg, q, cache, block_table, seq_lens, out, scale=0.0, stream=None):
     """q, out [B, H_q, d] (f32, bf16 or f16 each; q's rows may lie apart);
     block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]."""
-    import torch
-
-    qp, qs = _rows(q, "q", cfg.num_q_heads, cfg.head_dim)
+    qt, ot = _code(q, "q"), _code(out, "out")
+    dev = cache.get_device() if cache is not None else q.get_device()
+    heads, d = cfg.num_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", heads, d, dev)
     b = q.shape[0]
-    _check(load_library().tq_f8_decode_attention(
-        handle, qp, _code(q, "q"), qs, _dev(cache, "cache"),
-        _table(block_table, b, cfg.max_blocks_per_seq),
-        _index(seq_lens, "seq_lens", torch.int32, b), float(scale), b,
-        _out_rows(out, "out", b, cfg.num_q_heads, cfg.head_dim), _code(out, "out"), _stream_ptr(stream)),
-        "tq_f8_decode_attention")
+    st = load_library().tq_f8_decode_attention(
+        handle, qp, qt, qs, _dev(cache, "cache"), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        _index(seq_lens, "seq_lens", _TORCH.int32, b, dev), scale, b, _plain(out, "out", (b, heads, d), None, dev), ot,
+        _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_f8_decode_attention")
 
 
 def tq_f8_get_device_error(handle, stream=None):
@@ -601,19 +649,23 @@ def tq_f8_get_device_error(handle, stream=None):
     return flags.value
 
 
+def _cuda_device(device):
+    device = _torch().device(device)
+    if device.type == "cuda" and device.index is None:
+        device = _TORCH.device("cuda", _TORCH.cuda.current_device())
+    return device
+
+
 class TQF8Cache:
     """Owns (or adopts) the pages of an 8-bit cache, its workspace and the
     library handle.  ``cache``: an existing uint8 tensor of cache_bytes."""
 
     def __init__(self, device="cuda", cache=None, **cfg_kwargs):
-        import torch
-
         self.handle = None
         self.cfg = tq_f8_config(**cfg_kwargs)
         self.sizes = tq_f8_cache_sizes(self.cfg)
-        self.device = torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _cuda_device(device)
+        torch = _TORCH
         if cache is None:
             cache = torch.zeros(self.sizes["cache_bytes"], dtype=torch.uint8, device=self.device)
         elif (cache.dtype != torch.uint8 or cache.numel() != self.sizes["cache_bytes"] or not cache.is_contiguous()
@@ -633,20 +685,15 @@ class TQF8Cache:
         return self.cache.view(self.cfg.num_blocks, self.cfg.num_kv_heads, self.page_bytes)
 
     def store(self, k, v, slot_mapping, stream=None):
-        _same_device(self.device, k=k, v=v, slot_mapping=slot_mapping)
         tq_f8_store(self.handle, self.cfg, k, v, slot_mapping, self.cache, stream)
 
     def load(self, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
-        _same_device(self.device, block_table=block_table, seq_lens=seq_lens, cu_out=cu_out, k_out=k_out, v_out=v_out)
         tq_f8_load(self.handle, self.cfg, self.cache, block_table, seq_lens, cu_out, k_out, v_out, stream)
         return k_out, v_out
 
     def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
-        import torch
-
         if out is None:
-            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-        _same_device(self.device, q=q, block_table=block_table, seq_lens=seq_lens, out=out)
+            out = _TORCH.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
         tq_f8_decode_attention(self.handle, self.cfg, q, self.cache, block_table, seq_lens, out, scale, stream)
         return out
 
@@ -656,6 +703,95 @@ class TQF8Cache:
     def close(self):
         if self.handle:
             tq_f8_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def tq_prompt_sizes(cfg):
+    n = ctypes.c_size_t()
+    _check(load_library().tq_prompt_sizes(ctypes.byref(cfg), ctypes.byref(n)), "tq_prompt_sizes")
+    return dict(workspace_bytes=n.value)
+
+
+def tq_prompt_create(cfg, workspace, stream=None):
+    h = _P()
+    _check(load_library().tq_prompt_create(ctypes.byref(cfg), _P(workspace.data_ptr()), _stream_ptr(stream),
+                                           ctypes.byref(h)), "tq_prompt_create")
+    return h
+
+
+def tq_prompt_destroy(handle):
+    _check(load_library().tq_prompt_destroy(handle), "tq_prompt_destroy")
+
+
+def tq_prompt_attention(handle, cfg, q, k, v, cu_q, cu_k, out, lse=None, causal=True, scale=0.0, stream=None):
+    """q, out [n_q, H_q, d], k, v [n_k, H_kv, d], all of the handle's dtype (the
+    rows of q, k and v may lie apart); cu_q, cu_k int32 [B + 1]; lse f32
+    [n_q, H_q] or None."""
+    dt = _code(q, "q")
+    if dt != cfg.dtype or k.dtype != q.dtype or v.dtype != q.dtype or out.dtype != q.dtype:
+        raise TypeError(f"q, k, v and out must all have the handle's dtype (code {cfg.dtype})")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    dev = q.get_device()
+    hq, hk, d, i32 = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, _TORCH.int32
+    qp, qs = _rows(q, "q", hq, d, dev)
+    kp, ks = _rows(k, "k", hk, d, dev)
+    vp, vs = _rows(v, "v", hk, d, dev)
+    n, b = q.shape[0], cu_q.shape[0] - 1
+    if cu_k.shape[0] != b + 1:
+        raise ValueError("cu_q and cu_k must both have batch + 1 entries")
+    st = load_library().tq_prompt_attention(
+        handle, qp, kp, vp, qs, ks, vs, _index(cu_q, "cu_q", i32, 2, dev), _index(cu_k, "cu_k", i32, 2, dev), b, n,
+        k.shape[0], scale, 1 if causal else 0, _plain(out, "out", (n, hq, d), None, dev),
+        None if lse is None else _plain(lse, "lse", (n, hq), _TORCH.float32, dev), _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_prompt_attention")
+
+
+def tq_prompt_get_device_error(handle, stream=None):
+    flags = ctypes.c_uint32()
+    _check(load_library().tq_prompt_get_device_error(handle, ctypes.byref(flags), _stream_ptr(stream)),
+           "tq_prompt_get_device_error")
+    return flags.value
+
+
+class TQPrompt:
+    """Owns the workspace and library handle of prompt attention for one head
+    configuration, up to max_batch sequences and max_tokens query rows a call."""
+
+    def __init__(self, device="cuda", dtype=None, **cfg_kwargs):
+        self.handle = None
+        torch = _torch()
+        code = _DTYPE_CODES.get(dtype or torch.bfloat16)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}: bfloat16 or float16")
+        self.cfg = tq_prompt_config(dtype=code, **cfg_kwargs)
+        self.sizes = tq_prompt_sizes(self.cfg)
+        self.device = _cuda_device(device)
+        self.workspace = torch.empty(self.sizes["workspace_bytes"], dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            self.handle = tq_prompt_create(self.cfg, self.workspace)
+
+    def attention(self, q, k, v, cu_q, cu_k, out=None, lse=None, causal=True, scale=0.0, stream=None):
+        if q.get_device() != self.device.index:
+            raise _wrong_device(q, "q", self.device.index)
+        if out is None:
+            out = _TORCH.empty(q.shape, dtype=q.dtype, device=q.device)
+        tq_prompt_attention(self.handle, self.cfg, q, k, v, cu_q, cu_k, out, lse, causal, scale, stream)
+        return out
+
+    def device_error(self, stream=None):
+        return tq_prompt_get_device_error(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            tq_prompt_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

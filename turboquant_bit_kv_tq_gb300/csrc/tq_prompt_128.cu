@@ -1,0 +1,10 @@
+// Prompt attention kernels of head dim 128 (one translation unit per head dim, compiled in parallel).
+#include "tq_prompt.cuh"
+
+namespace tq {
+tq_status launch_prompt_128(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                            bool bf16, cudaStream_t s) {
+    return bf16 ? launch_prompt<PromptCfg<128, true>>(a, mq, mk, mv, s)
+                : launch_prompt<PromptCfg<128, false>>(a, mq, mk, mv, s);
+}
+}  // namespace tq

@@ -37,6 +37,7 @@
 #include <mutex>
 
 #include "tq_store.cuh"
+#include "tq_tma.h"
 
 namespace tq {
 
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // The driver's tensor-map encoder: from the runtime's entry-point query, else
 // the driver library's own export; looked up under a lock until found.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(char* why, size_t why_len) {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(char* why, size_t why_len) {
     static std::mutex mu;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::lock_guard<std::mutex> lock(mu);
@@ -691,13 +692,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder(char* why, size_t wh
     return fn;
 }
 
-// rows [n][128] bf16 at base as a 2-D map with 8 x 128 boxes (zero fill past n)
-static tq_status rows_map(CUtensorMap* m, const void* base, int64_t n) {
-    char why[200] = "";
-    auto enc = tensor_map_encoder(why, sizeof why);
-    if (!enc) return driver_failure("%s", why);
-    // the encoder wants a current context: a host thread whose first call this
-    // is has none until the runtime binds the device's primary context
+tq_status bind_device_context() {
     static thread_local bool bound = false;
     if (!bound) {
         int dev = 0;
@@ -705,6 +700,16 @@ static tq_status rows_map(CUtensorMap* m, const void* base, int64_t n) {
         if (st == TQ_OK) bound = cuda_status_detail(cudaSetDevice(dev), "binding the device context") == TQ_OK;
         if (!bound) return TQ_ERR_CUDA;
     }
+    return TQ_OK;
+}
+
+// rows [n][128] bf16 at base as a 2-D map with 8 x 128 boxes (zero fill past n)
+static tq_status rows_map(CUtensorMap* m, const void* base, int64_t n) {
+    char why[200] = "";
+    auto enc = tensor_map_encoder(why, sizeof why);
+    if (!enc) return driver_failure("%s", why);
+    const tq_status bs = bind_device_context();
+    if (bs != TQ_OK) return bs;
     const cuuint64_t dims[2] = {128, (cuuint64_t)n};
     const cuuint64_t strides[1] = {256};
     const cuuint32_t box[2] = {8, 128};
