@@ -108,6 +108,8 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
         k_stride = v_stride = q_stride;
     }
     PromptArgs a;
+    a.q = q;
+    a.q_stride = q_stride;
     a.out = out;
     a.lse = lse;
     a.cu_q = cu_q;

@@ -15,18 +15,18 @@
 //   step i uses score buffer i & 1; d = 128: key tile i / 2 of query tile i & 1,
 //   d = 256: key tile i.
 //   MMA order: ... P V of step i, scores of step i + 2, P V of step i + 1, ...
-// The scores of step i + 2 overwrite the probabilities of step i in place, which
-// is safe without a wait because the tensor cores take MMAs in order.
+// The scores of step i + 2 overwrite the probabilities of step i in place.
 //
 // Softmax: thread = row; its scores come from tensor memory into registers, the
 // probabilities (rounded to the inputs' 16-bit type, the row sum is of the
-// unrounded ones) go back as the A operand of P V.  The reference m moves only
+// unrounded ones) go back as the A operand of P V, in two halves of the keys so
+// that the products of the first run beside the exponentials of the second.  The reference m moves only
 // when it falls 2^8 behind, so that the output in tensor memory is rescaled
 // rarely; that is exact, the final quotient does not depend on m.
 //
 // Warps: 0-3 (and 4-7 at d = 128) softmax and output of query tile 0 (1), then
-// one for the copies (TMA), one for the MMAs and two idle ones that complete the
-// warpgroup of the register split.
+// one for the copies (TMA), two that issue MMAs and an idle one that completes
+// the warpgroup of the register split.
 #pragma once
 
 #include <cuda.h>
@@ -36,6 +36,8 @@
 namespace tq {
 
 struct PromptArgs {
+    const void* q;
+    int64_t q_stride;
     void* out;
     float* lse;
     const int32_t *cu_q, *cu_k;
@@ -54,15 +56,25 @@ struct PromptCfg {
     static constexpr int BN = D == 128 ? 128 : 64;
     static constexpr int CH = D / 64;            // 64-element chunks (128-byte swizzled rows)
     static constexpr int QB = 128 * D * 2, KB = BN * D * 2;  // bytes of a query / key tile
-    static constexpr int STAGES = 5;
+    // d = 256: the query tile goes to tensor memory (the score products' shared-memory
+    // traffic, 6 KB per MMA of 32 cycles with both operands there, would bound them)
+    static constexpr bool QT = D == 256;
+    static constexpr int STAGES = QT ? 7 : 5;
+    // ring order: AHEAD key tiles, then value tile 0, key tile AHEAD, value tile 1, ...
+    static constexpr int AHEAD = NQ == 2 ? 1 : 2;
+    static __host__ __device__ constexpr int key_pos(int j) { return j < AHEAD ? j : 2 * j - AHEAD + 1; }
+    static __host__ __device__ constexpr int value_pos(int j, int n) {
+        const int pos = 2 * j + AHEAD, keys_out = n - AHEAD;  // value tiles from keys_out on have no key tile between them
+        return j <= keys_out ? pos : n + j;
+    }
     static constexpr int SOFT = 128 * NQ;        // softmax threads
     static constexpr int THREADS = SOFT + 128;
     // tensor memory: scores (probabilities in place), then outputs
-    static constexpr int COL_S = 0, COL_O = 2 * BN;
-    static constexpr int off_ring = NQ * QB;
+    static constexpr int COL_S = 0, COL_O = 2 * BN, COL_Q = COL_O + NQ * D;
+    static constexpr int off_ring = QT ? 0 : NQ * QB;
     static constexpr int off_bar = off_ring + STAGES * KB;
     static constexpr int total = off_bar + 256 + 1024;  // + alignment to 1024
-    static_assert(COL_O + NQ * D <= 512, "tensor memory");
+    static_assert(COL_Q + (QT ? D / 2 : 0) <= 512, "tensor memory");
     static_assert(total <= 232448, "shared memory");
 };
 
@@ -118,6 +130,25 @@ __device__ __forceinline__ uint32_t prompt_pack(float lo, float hi) {
         const __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+}
+// pairs of fp32 (one instruction for two lanes' worth of work)
+__device__ __forceinline__ uint64_t prompt_pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void prompt_unpair(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t prompt_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t prompt_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 // a wait that a stuck barrier ends once for the whole role: later waits of the
 // thread are skipped and the block runs to its end
@@ -201,8 +232,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::off_bar);
     const uint32_t full = smem_u32(bars), empty = full + 8 * S, qfull = empty + 8 * S, sfull = qfull + 8,
-                   pready = sfull + 16, pvdone = pready + 16, vclean = pvdone + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * S + 8);
+                   pready = sfull + 16, pvdone = pready + 32, vclean = pvdone + 16, turn = vclean + 8;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * S + 12);
     __shared__ PromptWork s_w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int W0 = C::SOFT / 32;  // first of the other four warps: copies, MMA
@@ -222,13 +253,15 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             s_w = w;
             for (int s = 0; s < S; ++s) {
                 mbar_init(full + 8 * s, 1);
-                mbar_init(empty + 8 * s, 1);
+                mbar_init(empty + 8 * s, NQ);
             }
-            mbar_init(qfull, 1);
+            mbar_init(qfull, C::QT ? 4 : 1);
             for (int t = 0; t < 2; ++t) {
                 mbar_init(sfull + 8 * t, 1);
-                mbar_init(pready + 8 * t, 4);
+                mbar_init(pready + 16 * t, 4);  // the first and the second half of the keys
+                mbar_init(pready + 16 * t + 8, 4);
                 mbar_init(pvdone + 8 * t, 1);
+                mbar_init(turn + 8 * t, 1);
             }
             mbar_init(vclean, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -249,12 +282,14 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             // ---------------------------------------------------- copies
             if (lane == 0 && n > 0) {
                 // the tokens of both tiles that exist (rows of others come along and are not used)
-                const int tiles = NQ == 2 && n1 > 0 ? 2 : 1;
-                mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
-                for (int t = 0; t < tiles; ++t)
-                    for (int c = 0; c < CH; ++c)
-                        tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
-                               w.q0 + w.t0 + t * a.tile_tok, qfull);
+                if constexpr (!C::QT) {
+                    const int tiles = NQ == 2 && n1 > 0 ? 2 : 1;
+                    mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < CH; ++c)
+                            tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
+                                   w.q0 + w.t0 + t * a.tile_tok, qfull);
+                }
                 int r = 0;
                 auto load = [&](const CUtensorMap* m, int j) {
                     const int s = r % S;
@@ -267,18 +302,17 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         ++r;
                     }
                 };
-                constexpr int AHEAD = NQ == 2 ? 1 : 2;  // key tiles before the first value tile
-                for (int j = 0; j < AHEAD && j < n; ++j) load(&mk, j);
+                for (int j = 0; j < C::AHEAD && j < n; ++j) load(&mk, j);
                 for (int j = 0; j < n; ++j) {
                     load(&mv, j);
-                    if (j + AHEAD < n) load(&mk, j + AHEAD);
+                    if (j + C::AHEAD < n) load(&mk, j + C::AHEAD);
                 }
                 // copies still in flight land before the block exits
                 if (dead) {
                     bool d2 = false;
                     for (int i = max(0, r - S); i < r; ++i) prompt_wait(full + 8 * (i % S), (i / S) & 1, d2, err);
                     d2 = false;
-                    prompt_wait(qfull, 0, d2, err);
+                    if (!C::QT) prompt_wait(qfull, 0, d2, err);
                 }
             }
             // zero the value rows behind the sequence's last key: 0 * NaN or inf
@@ -296,80 +330,108 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 __syncwarp();
                 if (lane == 0) mbar_arrive(vclean);
             }
-        } else if (warp == W0 + 1) {
+        } else if (warp <= W0 + 2) {
             // -------------------------------------------------------- MMA
+            // Two issuing threads, so that the waits of one are hidden behind the
+            // products of the other (a wait and the first MMA after it cost about
+            // 165 cycles, and the tensor cores queue only two or three MMAs of 64).
+            // d = 128: one per query tile; they take turns, so that one tile's
+            // products run beside the other's softmax.  d = 256: one for the
+            // scores, one for the value products.
             if (lane == 0 && n > 0) {
                 constexpr uint32_t id_s = prompt_idesc(C::BF16, BN, 0), id_o = prompt_idesc(C::BF16, D, 1);
-                int r = 0;
-                auto take = [&]() {  // the next tile of the ring
-                    const int s = r % S;
-                    prompt_wait(full + 8 * s, (r / S) & 1, dead, err);
-                    ++r;
-                    return s;
+                const int me = warp - (W0 + 1);
+                const uint64_t q_desc = prompt_desc(smem_u32(smem), 16);
+                const uint64_t k_desc = prompt_desc(smem_u32(smem) + C::off_ring, 16);
+                const uint64_t v_desc = prompt_desc(smem_u32(smem) + C::off_ring, BN * 128);
+                auto take = [&](int r) {  // ring position r
+                    prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
+                    return r % S;
                 };
                 auto scores = [&](int buf, int t, int s) {
-                    const uint32_t qa = smem_u32(smem) + t * C::QB, ka = smem_u32(smem) + C::off_ring + s * C::KB;
+                    const uint64_t qd = q_desc + (uint64_t)(t * (C::QB >> 4));
+                    const uint64_t kd = k_desc + (uint64_t)(s * (C::KB >> 4));
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        prompt_mma_ss(tmem + C::COL_S + buf * BN,
-                                      prompt_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 16),
-                                      prompt_desc(ka + (k >> 2) * (BN * 128) + (k & 3) * 32, 16), id_s, k > 0);
+                    {
+                        const uint64_t b = kd + (uint64_t)(((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4);
+                        if constexpr (C::QT)
+                            prompt_mma_ts(tmem + C::COL_S + buf * BN, tmem + C::COL_Q + 8 * k, b, id_s, k > 0);
+                        else
+                            prompt_mma_ss(tmem + C::COL_S + buf * BN,
+                                          qd + (uint64_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), b, id_s, k > 0);
+                    }
                     tc_commit(sfull + 8 * buf);
                 };
-                auto values = [&](int buf, int t, int s, bool first) {
-                    const uint32_t va = smem_u32(smem) + C::off_ring + s * C::KB;
-                    tc_fence_after();
+                auto values = [&](int buf, int t, int s, bool first, uint32_t parity) {
+                    const uint64_t vd = v_desc + (uint64_t)(s * (C::KB >> 4));
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * k,
-                                      prompt_desc(va + k * 2048, BN * 128), id_o, !(first && k == 0));
-                    tc_commit(pvdone + 8 * t);
+                    for (int h = 0; h < 2; ++h) {
+                        if (NQ == 1) prompt_wait(pready + 16 * buf + 8 * h, parity, dead, err);
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
+                            prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * k,
+                                          vd + (uint64_t)((k * 2048) >> 4), id_o, !(first && k == 0));
+                    }
+                    tc_commit(pvdone + 8 * buf);
                 };
                 const bool ragged = w.lk % BN != 0;
-                auto value_tile = [&](int j) {
-                    const int s = take();
+                auto value_tile = [&](int r, int j) {
+                    const int s = take(r);
                     if (ragged && j == w.lk / BN) prompt_wait(vclean, 0, dead, err);
                     return s;
                 };
-                prompt_wait(qfull, 0, dead, err);
                 if constexpr (NQ == 2) {
-                    int ks = take();
-                    if (n0 > 0) scores(0, 0, ks);
-                    if (n1 > 0) scores(1, 1, ks);
+                    // both threads see every ring position and release every stage
+                    const int mine = me == 0 ? n0 : n1;
+                    const bool both = n0 > 0 && n1 > 0;
+                    int turns = 0;
+                    auto begin = [&]() {
+                        if (both && (me == 1 || turns > 0)) prompt_wait(turn + 8 * me, (turns - (me == 0)) & 1, dead, err);
+                        ++turns;
+                    };
+                    auto pass = [&]() {
+                        if (both) mbar_arrive(turn + 8 * (1 - me));
+                    };
+                    prompt_wait(qfull, 0, dead, err);
+                    int ks = take(C::key_pos(0));
+                    begin();
+                    if (mine > 0) scores(me, me, ks);
+                    pass();
                     tc_commit(empty + 8 * ks);
                     for (int j = 0; j < n; ++j) {
-                        const int vs = value_tile(j);
-                        ks = j + 1 < n ? take() : 0;
-                        if (j < n0) {
-                            prompt_wait(pready, j & 1, dead, err);
-                            values(0, 0, vs, j == 0);
-                            if (j + 1 < n0) scores(0, 0, ks);
-                        }
-                        if (j < n1) {
-                            prompt_wait(pready + 8, j & 1, dead, err);
-                            values(1, 1, vs, j == 0);
-                        }
+                        const int vs = value_tile(C::value_pos(j, n), j);
+                        if (j + 1 < n) ks = take(C::key_pos(j + 1));
+                        if (j < mine) prompt_wait(pready + 16 * me + 8, j & 1, dead, err);
+                        begin();
+                        if (j < mine) values(me, me, vs, j == 0, j & 1);
+                        // (these scores overwrite the probabilities, whose products this
+                        // thread issued before: MMAs of a thread run in order)
+                        if (j + 1 < mine) scores(me, me, ks);
+                        pass();
                         tc_commit(empty + 8 * vs);
-                        if (j + 1 < n1) scores(1, 1, ks);
                         if (j + 1 < n) tc_commit(empty + 8 * ks);
                     }
-                } else {
-                    for (int j = 0; j < 2 && j < n; ++j) {
-                        const int ks = take();
-                        scores(j, 0, ks);
+                } else if (me == 0) {
+                    // A thread that comes to a ring position has seen what orders the
+                    // stage's earlier phases before it: here the value products of tile
+                    // j - 2, below the probabilities of tile j.
+                    prompt_wait(qfull, 0, dead, err);
+                    for (int j = 0; j < n; ++j) {
+                        // the buffer's probabilities are used up
+                        if (j >= 2) prompt_wait(pvdone + 8 * (j & 1), ((j >> 1) - 1) & 1, dead, err);
+                        const int ks = take(C::key_pos(j));
+                        scores(j & 1, 0, ks);
                         tc_commit(empty + 8 * ks);
                     }
+                } else {
                     for (int j = 0; j < n; ++j) {
-                        const int vs = value_tile(j);
-                        prompt_wait(pready + 8 * (j & 1), (j >> 1) & 1, dead, err);
-                        values(j & 1, 0, vs, j == 0);
+                        prompt_wait(pready + 16 * (j & 1), (j >> 1) & 1, dead, err);
+                        const int vs = value_tile(C::value_pos(j, n), j);
+                        values(j & 1, 0, vs, j == 0, (j >> 1) & 1);
                         tc_commit(empty + 8 * vs);
-                        if (j + 2 < n) {
-                            const int ks = take();
-                            scores(j & 1, 0, ks);
-                            tc_commit(empty + 8 * ks);
-                        }
                     }
                 }
             }
@@ -388,6 +450,26 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const int whole = w.ok ? prompt_limit(a, w, min(w.t0 + t * a.tile_tok, w.lq)) / BN : 0;
         const uint32_t so = tmem + lanes + C::COL_O + t * D;
         const float c = a.scale_log2;
+        if constexpr (C::QT) {
+            if (n > 0) {
+                const uint4* q = reinterpret_cast<const uint4*>(
+                    static_cast<const uint16_t*>(a.q) + (live ? (int64_t)(w.q0 + tok) * a.q_stride + (int64_t)(w.row * a.group + head) * D : 0));
+#pragma unroll 1
+                for (int i = 0; i < D / 64; ++i) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 v = live ? __ldg(q + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+                        x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+                    }
+                    tmem_st32(tmem + lanes + C::COL_Q + 32 * i, x);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull);
+            }
+        }
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt; ++j) {
             const int buf = NQ == 2 ? t : j & 1;
@@ -422,7 +504,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 l *= f;
                 if (j > 0) {
                     if constexpr (NQ == 1) {
-                        prompt_wait(pvdone, (j - 1) & 1, dead, err);
+                        prompt_wait(pvdone + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, dead, err);
                         tc_fence_after();
                     }
 #pragma unroll 1
@@ -437,30 +519,43 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 }
             }
             const float mc = m == -INFINITY ? 0.f : m * c;
-            float l0 = 0.f, l1 = 0.f;
+            const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
+            uint64_t la = 0, lb = 0;  // sums of even and odd pairs
 #pragma unroll
             for (int i = 0; i < BN / 32; ++i) {
                 uint32_t p[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    const float x = prompt_exp2(fmaf(__uint_as_float(s[i][k]), c, -mc));
-                    const float y = prompt_exp2(fmaf(__uint_as_float(s[i][k + 1]), c, -mc));
-                    l0 += x;
-                    l1 += y;
-                    p[k / 2] = prompt_pack<C::BF16>(x, y);
+                for (int k = 0; k < 32; k += 4) {
+                    float x[4];
+                    prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])), c2, mc2),
+                                  x[0], x[1]);
+                    prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])), c2, mc2),
+                                  x[2], x[3]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[u] = prompt_exp2(x[u]);
+                    la = prompt_add2(la, prompt_pair(x[0], x[1]));
+                    lb = prompt_add2(lb, prompt_pair(x[2], x[3]));
+                    p[k / 2] = prompt_pack<C::BF16>(x[0], x[1]);
+                    p[k / 2 + 1] = prompt_pack<C::BF16>(x[2], x[3]);
                 }
                 tmem_st16(ss + 16 * i, p);
+                if (i == BN / 64 - 1 || i == BN / 32 - 1) {
+                    // half of the keys: their value products may start
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pready + 16 * buf + (i == BN / 32 - 1 ? 8 : 0));
+                }
             }
-            l += l0 + l1;
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pready + 8 * buf);
-            // (the barrier never gets two phases ahead of this thread)
-            if (NQ == 1 && j > 0) prompt_wait(pvdone, (j - 1) & 1, dead, err);
+            {
+                float x0, x1;
+                prompt_unpair(prompt_add2(la, lb), x0, x1);
+                l += x0 + x1;
+            }
         }
         if (nt > 0) {
-            prompt_wait(pvdone + 8 * t, (nt - 1) & 1, dead, err);
+            if constexpr (NQ == 2) prompt_wait(pvdone + 8 * t, (nt - 1) & 1, dead, err);
+            else prompt_wait(pvdone + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, dead, err);
             tc_fence_after();
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
