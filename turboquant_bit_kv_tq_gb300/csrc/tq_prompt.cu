@@ -1,5 +1,6 @@
 // Prompt attention: handle, argument checks and tensor maps.
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -8,7 +9,10 @@
 
 struct tq_prompt {
     tq_prompt_config cfg;
-    uint32_t* err;
+    uint32_t *err, *next;
+    float* part;
+    float2* meta;
+    int64_t part_rows;
 };
 
 namespace tq {
@@ -20,6 +24,18 @@ static tq_status prompt_check(const tq_prompt_config& c) {
     if (c.num_q_heads / c.num_kv_heads > 128) return TQ_ERR_UNSUPPORTED;
     if (c.max_batch < 1 || c.max_tokens < 1) return TQ_ERR_INVALID_ARG;
     return TQ_OK;
+}
+
+// The workspace: error word and item counters (256 bytes), then the sums and
+// {m, l} of part_rows rows.  A call is cut into parts only while its blocks fit
+// two waves of kPromptSms SMs with 128 (d = 256) or 256 (d = 128) rows each.
+constexpr int kPromptSms = 160;
+static int64_t prompt_part_rows(const tq_prompt_config& c) {
+    const int64_t all = (int64_t)kPromptParts * c.max_tokens * c.num_q_heads;
+    return std::min<int64_t>(all, 2 * kPromptSms * (c.head_dim == 128 ? 256 : 128));
+}
+static size_t prompt_meta_off(const tq_prompt_config& c) {
+    return 256 + (size_t)prompt_part_rows(c) * c.head_dim * 4;
 }
 
 // 16-bit rows [n][heads][d] `stride` elements apart as a map over (d, [group,]
@@ -57,7 +73,7 @@ extern "C" {
 tq_status tq_prompt_sizes(const tq_prompt_config* cfg, size_t* workspace_bytes) {
     if (!cfg) return TQ_ERR_INVALID_ARG;
     const tq_status st = prompt_check(*cfg);
-    if (st == TQ_OK && workspace_bytes) *workspace_bytes = 256;
+    if (st == TQ_OK && workspace_bytes) *workspace_bytes = prompt_meta_off(*cfg) + (size_t)prompt_part_rows(*cfg) * 8;
     return st;
 }
 
@@ -70,7 +86,12 @@ tq_status tq_prompt_create(const tq_prompt_config* cfg, void* workspace_dev, voi
     tq_prompt* h = new (std::nothrow) tq_prompt();
     if (!h) return TQ_ERR_INVALID_ARG;
     h->cfg = *cfg;
-    h->err = static_cast<uint32_t*>(workspace_dev);
+    uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
+    h->err = reinterpret_cast<uint32_t*>(ws);
+    h->next = h->err + 2;
+    h->part = reinterpret_cast<float*>(ws + 256);
+    h->meta = reinterpret_cast<float2*>(ws + prompt_meta_off(*cfg));
+    h->part_rows = prompt_part_rows(*cfg);
     cudaStream_t s = (cudaStream_t)stream;
     tq_status cs = cuda_status(cudaMemsetAsync(workspace_dev, 0, 256, s));
     if (cs == TQ_OK) cs = cuda_status(cudaStreamSynchronize(s));
@@ -115,6 +136,10 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
     a.cu_q = cu_q;
     a.cu_k = cu_k;
     a.err = p->err;
+    a.next = p->next;
+    a.part = p->part;
+    a.meta = p->meta;
+    a.parts = 1;
     a.batch = batch;
     a.n_q = n_q;
     a.n_k = n_k;
@@ -133,7 +158,8 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
     if (st == TQ_OK) st = prompt_map(&mv, v, bf16, d, 0, a.heads, n_k > 0 ? n_k : n_q, v_stride, bn);
     if (st != TQ_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    return d == 128 ? launch_prompt_128(a, mq, mk, mv, bf16, s) : launch_prompt_256(a, mq, mk, mv, bf16, s);
+    return d == 128 ? launch_prompt_128(a, p->part_rows, mq, mk, mv, bf16, s)
+                    : launch_prompt_256(a, p->part_rows, mq, mk, mv, bf16, s);
 }
 
 tq_status tq_prompt_get_device_error(const tq_prompt* p, uint32_t* flags, void* stream) {

@@ -4,9 +4,8 @@
 //   s_ij = <q_i, k_j>;  m_i = max_j s_ij;  p_ij = 2^(c (s_ij - m_i)), c = scale log2(e)
 //   out_i = sum_j p_ij v_j / sum_j p_ij;   lse_i = scale m_i + ln sum_j p_ij
 //
-// Bound by the tensor cores (4 d multiply-adds per query head, row and visible
-// key, times 2 flops).  A block takes 128-row query tiles of one sequence and KV
-// head; a tile's rows are the G query heads of floor(128 / G) tokens, so a group
+// Bound by the tensor cores (2 d multiply-adds per query head, row and visible
+// key).  A work item is 128-row query tiles of one sequence and KV head; a tile's rows are the G query heads of floor(128 / G) tokens, so a group
 // shares every key tile and short prompts still fill the rows.  d = 128: two
 // tiles of queries, 128 keys at a time; d = 256: one tile, 64 keys at a time
 // (its output alone fills half of tensor memory).  Either way a block has two
@@ -24,12 +23,20 @@
 // when it falls 2^8 behind, so that the output in tensor memory is rescaled
 // rarely; that is exact, the final quotient does not depend on m.
 //
+// One block per SM takes items until none is left (the first by its index, the
+// next from a counter), longest first, so that the copies and score products of
+// the next item run beside the output of the last.  With few items and many keys
+// an item covers a part of the keys only (`parts` of them); its unnormalised
+// output goes to the workspace and prompt_join_kernel adds the parts up.
+//
 // Warps: 0-3 (and 4-7 at d = 128) softmax and output of query tile 0 (1), then
 // one for the copies (TMA), two that issue MMAs and an idle one that completes
 // the warpgroup of the register split.
 #pragma once
 
 #include <cuda.h>
+
+#include <algorithm>
 
 #include "tq_device.cuh"
 
@@ -41,7 +48,10 @@ struct PromptArgs {
     void* out;
     float* lse;
     const int32_t *cu_q, *cu_k;
-    uint32_t* err;
+    uint32_t *err, *next;    // next: the item counter and the count of blocks that are through
+    float* part;             // parts > 1: [parts][n_q * q_heads][d] sums
+    float2* meta;            //            [parts][n_q * q_heads] {m, l}
+    int parts;
     int batch, n_q, n_k;
     int q_heads, heads, group, tile_tok;  // tile_tok: tokens per 128-row tile
     float scale, scale_log2;
@@ -73,7 +83,8 @@ struct PromptCfg {
     static constexpr int COL_S = 0, COL_O = 2 * BN, COL_Q = COL_O + NQ * D;
     static constexpr int off_ring = QT ? 0 : NQ * QB;
     static constexpr int off_bar = off_ring + STAGES * KB;
-    static constexpr int total = off_bar + 256 + 1024;  // + alignment to 1024
+    static constexpr int BAR = 320;
+    static constexpr int total = off_bar + BAR + 1024;  // + alignment to 1024
     static_assert(COL_Q + (QT ? D / 2 : 0) <= 512, "tensor memory");
     static_assert(total <= 232448, "shared memory");
 };
@@ -121,6 +132,8 @@ __device__ __forceinline__ float prompt_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+constexpr int kPromptParts = 16;  // key parts at most (a lane each in the join)
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t prompt_pack(float lo, float hi) {
     if constexpr (BF16) {
@@ -156,13 +169,19 @@ __device__ __forceinline__ void prompt_wait(uint32_t bar, uint32_t parity, bool&
     if (!dead) dead = !mbar_wait(bar, parity, err);
 }
 
-// What a block works on: rows [q0 + t0, ...) of a sequence, its keys.
+// A work item: rows [q0 + t0, ...) of a sequence, a range of its keys.
 struct PromptWork {
     int ok;
     int q0, lq, k0, lk;  // first row and length of the sequence's queries and keys
     int t0;              // first token of query tile 0
-    int n[2];            // key tiles of each query tile
-    int row;             // KV head
+    int row, part;       // KV head, part of the keys
+    int j0, n[2];        // first key tile; key tiles of each query tile from there on
+    __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
+    // the last value tile of the item reaches behind the sequence's last key
+    template <int BN>
+    __device__ __forceinline__ bool ragged() const {
+        return tiles() > 0 && lk % BN != 0 && lk / BN == j0 + tiles() - 1;
+    }
 };
 
 // keys that token t of the sequence sees
@@ -170,18 +189,18 @@ __device__ __forceinline__ int prompt_limit(const PromptArgs& a, const PromptWor
     return a.causal ? max(0, min(w.lk, t + 1 + w.lk - w.lq)) : w.lk;
 }
 
-// Work item `item` of the sequences' query tiles (the last first: with causal
-// rows those have the most keys), run by one warp.
+// Item `item` (query tiles from the last on: with causal rows those have the
+// most keys; KV heads and key parts of a tile side by side), run by one warp.
+// `total`: the query tiles of all sequences, counted by the first call (-1).
 template <class C>
-__device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int item, int lane) {
-    const int per = C::NQ * a.tile_tok;
+__device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int64_t item, int lane, int& total) {
+    const int per = C::NQ * a.tile_tok, sub = a.heads * a.parts;
     PromptWork w;
     w.ok = 0;
-    int total = 0;
-    // total first, then the item counted from the end
-    for (int pass = 0; pass < 2; ++pass) {
+    w.q0 = w.lq = w.k0 = w.lk = w.t0 = w.row = w.part = w.j0 = w.n[0] = w.n[1] = 0;
+    for (int pass = total < 0 ? 0 : 1; pass < 2; ++pass) {
         int seen = 0;
-        const int want = total - 1 - item;
+        const int64_t want = (int64_t)total - 1 - item / sub;
         if (pass == 1 && want < 0) break;
         for (int b0 = 0; b0 < a.batch; b0 += 32) {
             const int b = b0 + lane;
@@ -212,13 +231,30 @@ __device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int item,
                     w.lq = __shfl_sync(0xffffffffu, q1, src) - w.q0;
                     w.k0 = __shfl_sync(0xffffffffu, k0, src);
                     w.lk = __shfl_sync(0xffffffffu, k1, src) - w.k0;
-                    w.t0 = (want - __shfl_sync(0xffffffffu, seen + incl - n, src)) * per;
-                    return w;
+                    w.t0 = (int)(want - __shfl_sync(0xffffffffu, seen + incl - n, src)) * per;
+                    break;
                 }
             }
             seen += __shfl_sync(0xffffffffu, incl, 31);
         }
-        total = seen;
+        if (pass == 0) total = seen;
+    }
+    if (w.ok) {
+        const int x = (int)(item % sub);
+        w.row = x / a.parts;
+        w.part = x - w.row * a.parts;
+        int all[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            // key tiles that the query tile's last token sees
+            const int first = w.t0 + t * a.tile_tok, last = min(first + a.tile_tok, w.lq) - 1;
+            all[t] = t < C::NQ && first < w.lq ? (prompt_limit(a, w, last) + C::BN - 1) / C::BN : 0;
+        }
+        const int most = max(all[0], all[1]);
+        w.j0 = (int)((int64_t)most * w.part / a.parts);
+        const int j1 = (int)((int64_t)most * (w.part + 1) / a.parts);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) w.n[t] = max(0, min(j1, all[t]) - w.j0);
     }
     return w;
 }
@@ -231,104 +267,135 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::off_bar);
-    const uint32_t full = smem_u32(bars), empty = full + 8 * S, qfull = empty + 8 * S, sfull = qfull + 8,
-                   pready = sfull + 16, pvdone = pready + 32, vclean = pvdone + 16, turn = vclean + 8;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * S + 12);
-    __shared__ PromptWork s_w;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S, qfull = empty + 8 * S, qfree = qfull + 8,
+                   sfull = qfree + 8, pready = sfull + 16, pvdone = pready + 32, turn = pvdone + 16, wfull = turn + 16,
+                   wfree = wfull + 16, vclean = wfree + 16;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 3 * S + 16);
+    static_assert((3 * S + 16) * 8 + 4 <= C::BAR, "barriers");
+    __shared__ PromptWork s_w[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int W0 = C::SOFT / 32;  // first of the other four warps: copies, MMA
     uint32_t* err = a.err;
 
-    if (warp == W0) {
-        PromptWork w = prompt_find<C>(a, blockIdx.x / a.heads, lane);
-        if (w.ok) {
-            w.row = blockIdx.x % a.heads;
-            for (int t = 0; t < 2; ++t) {
-                // keys that the tile's last token sees
-                const int first = w.t0 + t * a.tile_tok, last = min(first + a.tile_tok, w.lq) - 1;
-                w.n[t] = t < NQ && first < w.lq ? (prompt_limit(a, w, last) + BN - 1) / BN : 0;
-            }
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, NQ);
+            mbar_init(vclean + 8 * s, 1);
         }
-        if (lane == 0) {
-            s_w = w;
-            for (int s = 0; s < S; ++s) {
-                mbar_init(full + 8 * s, 1);
-                mbar_init(empty + 8 * s, NQ);
-            }
-            mbar_init(qfull, C::QT ? 4 : 1);
-            for (int t = 0; t < 2; ++t) {
-                mbar_init(sfull + 8 * t, 1);
-                mbar_init(pready + 16 * t, 4);  // the first and the second half of the keys
-                mbar_init(pready + 16 * t + 8, 4);
-                mbar_init(pvdone + 8 * t, 1);
-                mbar_init(turn + 8 * t, 1);
-            }
-            mbar_init(vclean, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_init(qfull, C::QT ? 4 : 1);
+        mbar_init(qfree, 2);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(sfull + 8 * t, 1);
+            mbar_init(pready + 16 * t, 4);  // the first and the second half of the keys
+            mbar_init(pready + 16 * t + 8, 4);
+            mbar_init(pvdone + 8 * t, 1);
+            mbar_init(turn + 8 * t, 1);
+            mbar_init(wfull + 8 * t, 1);
+            mbar_init(wfree + 8 * t, 2 + W0);  // the two issuing threads and the softmax warps
         }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const PromptWork w = s_w;
-    const int n0 = w.ok ? w.n[0] : 0, n1 = w.ok && NQ == 2 ? w.n[1] : 0, n = max(n0, n1);
     bool dead = false;
+    // Every role walks the same items; what it counts over them (ring positions,
+    // uses of a score buffer) gives the parities of its waits.
+    int ring = 0, use0 = 0, use1 = 0;
+    auto advance = [&](const PromptWork& w) {
+        ring += 2 * w.tiles();
+        use0 += NQ == 2 ? w.n[0] : (w.tiles() + 1) / 2;
+        use1 += NQ == 2 ? w.n[1] : w.tiles() / 2;
+    };
+    // item number `it` of this block
+    auto fetch = [&](int it, PromptWork& w) {
+        prompt_wait(wfull + 8 * (it & 1), (it >> 1) & 1, dead, err);
+        w = s_w[it & 1];
+        if (dead) w.ok = 0;
+    };
 
     if (warp >= W0) {
         if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
         if (warp == W0) {
             // ---------------------------------------------------- copies
-            if (lane == 0 && n > 0) {
-                // the tokens of both tiles that exist (rows of others come along and are not used)
-                if constexpr (!C::QT) {
-                    const int tiles = NQ == 2 && n1 > 0 ? 2 : 1;
-                    mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
-                    for (int t = 0; t < tiles; ++t)
-                        for (int c = 0; c < CH; ++c)
-                            tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
-                                   w.q0 + w.t0 + t * a.tile_tok, qfull);
+            int total = -1, loads = 0, q_loads = 0;
+            int64_t item = blockIdx.x;
+            for (int it = 0;; ++it) {
+                const PromptWork w = prompt_find<C>(a, item, lane, total);
+                if (it >= 2) prompt_wait(wfree + 8 * (it & 1), ((it >> 1) - 1) & 1, dead, err);
+                __syncwarp();
+                if (lane == 0) {
+                    s_w[it & 1] = w;
+                    mbar_arrive(wfull + 8 * (it & 1));
                 }
-                int r = 0;
-                auto load = [&](const CUtensorMap* m, int j) {
-                    const int s = r % S;
-                    if (r >= S) prompt_wait(empty + 8 * s, ((r / S) - 1) & 1, dead, err);
-                    if (!dead) {
-                        mbar_expect_tx(full + 8 * s, C::KB);
-                        for (int c = 0; c < CH; ++c)
-                            tma_3d(smem_u32(smem) + C::off_ring + s * C::KB + c * (BN * 128), m, 64 * c, w.row,
-                                   w.k0 + j * BN, full + 8 * s);
-                        ++r;
+                if (!w.ok) break;
+                const int n = w.tiles();
+                if (lane == 0 && n > 0 && !dead) {
+                    if constexpr (!C::QT) {
+                        if (q_loads > 0) prompt_wait(qfree, (q_loads - 1) & 1, dead, err);
+                        if (!dead) {
+                            ++q_loads;
+                            // the tokens of both tiles that exist (rows of others come along and are not used)
+                            const int tiles = NQ == 2 && w.n[1] > 0 ? 2 : 1;
+                            mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
+                            for (int t = 0; t < tiles; ++t)
+                                for (int c = 0; c < CH; ++c)
+                                    tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
+                                           w.q0 + w.t0 + t * a.tile_tok, qfull);
+                        }
                     }
-                };
-                for (int j = 0; j < C::AHEAD && j < n; ++j) load(&mk, j);
-                for (int j = 0; j < n; ++j) {
-                    load(&mv, j);
-                    if (j + C::AHEAD < n) load(&mk, j + C::AHEAD);
+                    auto load = [&](const CUtensorMap* m, int j) {
+                        const int s = loads % S;
+                        if (loads >= S) prompt_wait(empty + 8 * s, ((loads / S) - 1) & 1, dead, err);
+                        if (!dead) {
+                            mbar_expect_tx(full + 8 * s, C::KB);
+                            for (int c = 0; c < CH; ++c)
+                                tma_3d(smem_u32(smem) + C::off_ring + s * C::KB + c * (BN * 128), m, 64 * c, w.row,
+                                       w.k0 + (w.j0 + j) * BN, full + 8 * s);
+                            ++loads;
+                        }
+                    };
+                    for (int j = 0; j < C::AHEAD && j < n; ++j) load(&mk, j);
+                    for (int j = 0; j < n; ++j) {
+                        load(&mv, j);
+                        if (j + C::AHEAD < n) load(&mk, j + C::AHEAD);
+                    }
                 }
+                __syncwarp();
+                // the next item: asked for when this one's copies are under way (not
+                // before: who is through first shall have the longest that is left)
+                uint32_t next = 0;
+                if (lane == 0) next = atomicAdd(a.next, 1u);
+                dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
+                ring += 2 * n;
+                // zero the value rows behind the sequence's last key: 0 * NaN or inf
+                // of a neighbour's row would be NaN.  The item's last copy has them.
+                if (w.ragged<BN>()) {
+                    const int s = (ring - 1) % S;
+                    prompt_wait(full + 8 * s, ((ring - 1) / S) & 1, dead, err);
+                    uint8_t* v = smem + C::off_ring + s * C::KB;
+                    for (int i = lane; i < CH * BN * 8; i += 32)
+                        if ((i >> 3) % BN >= w.lk % BN) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(vclean + 8 * s);
+                }
+                dead = __any_sync(0xffffffffu, (int)dead);
+                item = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
+            }
+            if (lane == 0) {
                 // copies still in flight land before the block exits
                 if (dead) {
                     bool d2 = false;
-                    for (int i = max(0, r - S); i < r; ++i) prompt_wait(full + 8 * (i % S), (i / S) & 1, d2, err);
+                    for (int i = max(0, loads - S); i < loads; ++i) prompt_wait(full + 8 * (i % S), (i / S) & 1, d2, err);
                     d2 = false;
-                    if (!C::QT) prompt_wait(qfull, 0, d2, err);
+                    if (!C::QT && q_loads > 0) prompt_wait(qfull, (q_loads - 1) & 1, d2, err);
                 }
-            }
-            // zero the value rows behind the sequence's last key: 0 * NaN or inf
-            // of a neighbour's row would be NaN.  The last value tile was the
-            // last copy, the 2 n-th of the ring.
-            __syncwarp();
-            dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
-            if (n > 0 && w.lk % BN != 0 && w.lk / BN == n - 1) {
-                const int s = (2 * n - 1) % S;
-                prompt_wait(full + 8 * s, ((2 * n - 1) / S) & 1, dead, err);
-                uint8_t* v = smem + C::off_ring + s * C::KB;
-                for (int i = lane; i < CH * BN * 8; i += 32)
-                    if ((i >> 3) % BN >= w.lk % BN) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(vclean);
+                // the last block leaves the counters ready for the next call
+                if (atomicAdd(a.next + 1, 1u) == gridDim.x - 1) a.next[0] = a.next[1] = 0;
             }
         } else if (warp <= W0 + 2) {
             // -------------------------------------------------------- MMA
@@ -338,13 +405,14 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             // d = 128: one per query tile; they take turns, so that one tile's
             // products run beside the other's softmax.  d = 256: one for the
             // scores, one for the value products.
-            if (lane == 0 && n > 0) {
+            if (lane == 0) {
                 constexpr uint32_t id_s = prompt_idesc(C::BF16, BN, 0), id_o = prompt_idesc(C::BF16, D, 1);
                 const int me = warp - (W0 + 1);
                 const uint64_t q_desc = prompt_desc(smem_u32(smem), 16);
                 const uint64_t k_desc = prompt_desc(smem_u32(smem) + C::off_ring, 16);
                 const uint64_t v_desc = prompt_desc(smem_u32(smem) + C::off_ring, BN * 128);
-                auto take = [&](int r) {  // ring position r
+                auto take = [&](int pos) {  // ring position `pos` of the item
+                    const int r = ring + pos;
                     prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
                     return r % S;
                 };
@@ -353,8 +421,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     const uint64_t kd = k_desc + (uint64_t)(s * (C::KB >> 4));
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                    {
+                    for (int k = 0; k < D / 16; ++k) {
                         const uint64_t b = kd + (uint64_t)(((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4);
                         if constexpr (C::QT)
                             prompt_mma_ts(tmem + C::COL_S + buf * BN, tmem + C::COL_Q + 8 * k, b, id_s, k > 0);
@@ -364,6 +431,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     }
                     tc_commit(sfull + 8 * buf);
                 };
+                // (d = 128: both halves of the probabilities have been waited for)
                 auto values = [&](int buf, int t, int s, bool first, uint32_t parity) {
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::KB >> 4));
 #pragma unroll
@@ -377,62 +445,81 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     }
                     tc_commit(pvdone + 8 * buf);
                 };
-                const bool ragged = w.lk % BN != 0;
-                auto value_tile = [&](int r, int j) {
-                    const int s = take(r);
-                    if (ragged && j == w.lk / BN) prompt_wait(vclean, 0, dead, err);
-                    return s;
-                };
-                if constexpr (NQ == 2) {
-                    // both threads see every ring position and release every stage
-                    const int mine = me == 0 ? n0 : n1;
-                    const bool both = n0 > 0 && n1 > 0;
-                    int turns = 0;
-                    auto begin = [&]() {
-                        if (both && (me == 1 || turns > 0)) prompt_wait(turn + 8 * me, (turns - (me == 0)) & 1, dead, err);
-                        ++turns;
+                int q_uses = 0, turns = 0;
+                uint32_t clean = 0;  // parity of each stage's next cleaning
+                PromptWork w;
+                for (int it = 0;; ++it) {
+                    fetch(it, w);
+                    mbar_arrive(wfree + 8 * (it & 1));
+                    if (!w.ok) break;
+                    const int n = w.tiles();
+                    if (n == 0) continue;
+                    const bool rag = w.ragged<BN>();
+                    auto value_tile = [&](int j) {
+                        const int s = take(C::value_pos(j, n));
+                        if (rag && j == n - 1) {
+                            prompt_wait(vclean + 8 * s, (clean >> s) & 1, dead, err);
+                            clean ^= 1u << s;
+                        }
+                        return s;
                     };
-                    auto pass = [&]() {
-                        if (both) mbar_arrive(turn + 8 * (1 - me));
-                    };
-                    prompt_wait(qfull, 0, dead, err);
-                    int ks = take(C::key_pos(0));
-                    begin();
-                    if (mine > 0) scores(me, me, ks);
-                    pass();
-                    tc_commit(empty + 8 * ks);
-                    for (int j = 0; j < n; ++j) {
-                        const int vs = value_tile(C::value_pos(j, n), j);
-                        if (j + 1 < n) ks = take(C::key_pos(j + 1));
-                        if (j < mine) prompt_wait(pready + 16 * me + 8, j & 1, dead, err);
+                    if constexpr (NQ == 2) {
+                        // both threads see every ring position and release every stage
+                        const int mine = me == 0 ? w.n[0] : w.n[1], use = me == 0 ? use0 : use1;
+                        const bool both = w.n[0] > 0 && w.n[1] > 0;
+                        auto begin = [&]() {
+                            if (!both) return;
+                            if (me == 1 || turns > 0) prompt_wait(turn + 8 * me, (turns - (me == 0)) & 1, dead, err);
+                            ++turns;
+                        };
+                        auto pass = [&]() {
+                            if (both) mbar_arrive(turn + 8 * (1 - me));
+                        };
+                        prompt_wait(qfull, q_uses & 1, dead, err);
+                        int ks = take(C::key_pos(0));
                         begin();
-                        if (j < mine) values(me, me, vs, j == 0, j & 1);
-                        // (these scores overwrite the probabilities, whose products this
-                        // thread issued before: MMAs of a thread run in order)
-                        if (j + 1 < mine) scores(me, me, ks);
+                        if (mine > 0) scores(me, me, ks);
                         pass();
-                        tc_commit(empty + 8 * vs);
-                        if (j + 1 < n) tc_commit(empty + 8 * ks);
-                    }
-                } else if (me == 0) {
-                    // A thread that comes to a ring position has seen what orders the
-                    // stage's earlier phases before it: here the value products of tile
-                    // j - 2, below the probabilities of tile j.
-                    prompt_wait(qfull, 0, dead, err);
-                    for (int j = 0; j < n; ++j) {
-                        // the buffer's probabilities are used up
-                        if (j >= 2) prompt_wait(pvdone + 8 * (j & 1), ((j >> 1) - 1) & 1, dead, err);
-                        const int ks = take(C::key_pos(j));
-                        scores(j & 1, 0, ks);
                         tc_commit(empty + 8 * ks);
+                        if (mine <= 1) tc_commit(qfree);
+                        for (int j = 0; j < n; ++j) {
+                            const int vs = value_tile(j);
+                            if (j + 1 < n) ks = take(C::key_pos(j + 1));
+                            if (j < mine) prompt_wait(pready + 16 * me + 8, (use + j) & 1, dead, err);
+                            begin();
+                            if (j < mine) values(me, me, vs, j == 0, 0);
+                            // (these scores overwrite the probabilities, whose products this
+                            // thread issued before: MMAs of a thread run in order)
+                            if (j + 1 < mine) scores(me, me, ks);
+                            pass();
+                            tc_commit(empty + 8 * vs);
+                            if (j + 1 < n) tc_commit(empty + 8 * ks);
+                            if (j + 2 == mine) tc_commit(qfree);  // the tile's last scores are issued
+                        }
+                    } else if (me == 0) {
+                        // A thread that comes to a ring position has seen what orders the
+                        // stage's earlier phases before it: here the value products of the
+                        // buffer's last use, below the probabilities of the tile.
+                        prompt_wait(qfull, q_uses & 1, dead, err);
+                        for (int j = 0; j < n; ++j) {
+                            // the buffer's probabilities are used up
+                            const int use = (j & 1 ? use1 : use0) + (j >> 1);
+                            if (use > 0) prompt_wait(pvdone + 8 * (j & 1), (use - 1) & 1, dead, err);
+                            const int ks = take(C::key_pos(j));
+                            scores(j & 1, 0, ks);
+                            tc_commit(empty + 8 * ks);
+                        }
+                    } else {
+                        for (int j = 0; j < n; ++j) {
+                            const int use = (j & 1 ? use1 : use0) + (j >> 1);
+                            prompt_wait(pready + 16 * (j & 1), use & 1, dead, err);
+                            const int vs = value_tile(j);
+                            values(j & 1, 0, vs, j == 0, use & 1);
+                            tc_commit(empty + 8 * vs);
+                        }
                     }
-                } else {
-                    for (int j = 0; j < n; ++j) {
-                        prompt_wait(pready + 16 * (j & 1), (j >> 1) & 1, dead, err);
-                        const int vs = value_tile(C::value_pos(j, n), j);
-                        values(j & 1, 0, vs, j == 0, (j >> 1) & 1);
-                        tc_commit(empty + 8 * vs);
-                    }
+                    ++q_uses;
+                    advance(w);
                 }
             }
         }
@@ -442,146 +529,176 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const int t = NQ == 2 ? warp >> 2 : 0;
         const int rt = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const int nt = t == 0 ? n0 : n1;
-        const int tok = w.t0 + t * a.tile_tok + rt / a.group, head = rt % a.group;
-        const bool live = w.ok && rt < a.tile_tok * a.group && tok < w.lq;
-        const int lim = live ? prompt_limit(a, w, tok) : 0;
-        // key tiles that every row of the tile sees whole
-        const int whole = w.ok ? prompt_limit(a, w, min(w.t0 + t * a.tile_tok, w.lq)) / BN : 0;
+        const int tt = rt / a.group, head = rt - tt * a.group;
         const uint32_t so = tmem + lanes + C::COL_O + t * D;
         const float c = a.scale_log2;
-        if constexpr (C::QT) {
-            if (n > 0) {
-                const uint4* q = reinterpret_cast<const uint4*>(
-                    static_cast<const uint16_t*>(a.q) + (live ? (int64_t)(w.q0 + tok) * a.q_stride + (int64_t)(w.row * a.group + head) * D : 0));
+        PromptWork w;
+        for (int it = 0;; ++it) {
+            fetch(it, w);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wfree + 8 * (it & 1));
+            if (!w.ok) break;
+            const int nt = t == 0 ? w.n[0] : w.n[1], first = w.t0 + t * a.tile_tok, tok = first + tt;
+            const bool live = rt < a.tile_tok * a.group && tok < w.lq;
+            const int lim = live ? prompt_limit(a, w, tok) : 0;
+            // key tiles that every row of the tile sees whole
+            const int whole = prompt_limit(a, w, min(first, w.lq)) / BN;
+            const int64_t row = (int64_t)(w.q0 + tok) * a.q_heads + w.row * a.group + head;
+            if constexpr (C::QT) {
+                // (the last item's scores are done: this thread has seen them)
+                if (nt > 0) {
+                    const uint4* q = reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(a.q) +
+                        (live ? (int64_t)(w.q0 + tok) * a.q_stride + (int64_t)(w.row * a.group + head) * D : 0));
 #pragma unroll 1
-                for (int i = 0; i < D / 64; ++i) {
-                    uint32_t x[32];
+                    for (int i = 0; i < D / 64; ++i) {
+                        uint32_t x[32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 v = live ? __ldg(q + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
-                        x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+                        for (int k = 0; k < 8; ++k) {
+                            const uint4 v = live ? __ldg(q + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
+                            x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+                        }
+                        tmem_st32(tmem + lanes + C::COL_Q + 32 * i, x);
                     }
-                    tmem_st32(tmem + lanes + C::COL_Q + 32 * i, x);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qfull);
                 }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(qfull);
             }
-        }
-        float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < nt; ++j) {
-            const int buf = NQ == 2 ? t : j & 1;
-            const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
-            prompt_wait(sfull + 8 * buf, (NQ == 2 ? j : j >> 1) & 1, dead, err);
-            tc_fence_after();
-            uint32_t s[BN / 32][32];
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < nt; ++j) {
+                const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
+                const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
+                prompt_wait(sfull + 8 * buf, use & 1, dead, err);
+                tc_fence_after();
+                uint32_t s[BN / 32][32];
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) tmem_ld32(ss + 32 * i, s[i]);
-            tc_wait_ld();
-            if (j >= whole) {
-                const int cut = lim - j * BN;
+                for (int i = 0; i < BN / 32; ++i) tmem_ld32(ss + 32 * i, s[i]);
+                tc_wait_ld();
+                if (w.j0 + j >= whole) {
+                    const int cut = lim - (w.j0 + j) * BN;
+#pragma unroll
+                    for (int i = 0; i < BN / 32; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * i + k >= cut) s[i][k] = 0xFF800000u;
+                }
+                float mx = -INFINITY, mx2 = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < BN / 32; ++i)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * i + k >= cut) s[i][k] = 0xFF800000u;
-            }
-            float mx = -INFINITY, mx2 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < BN / 32; ++i)
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])));
-                    mx2 = fmaxf(mx2, fmaxf(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])));
-                }
-            mx = fmaxf(mx, mx2);
-            const bool move = (mx - m) * c > 8.f;  // also from -inf to the first score
-            if (__any_sync(0xffffffffu, move)) {
-                const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
-                if (move) m = mx;
-                l *= f;
-                if (j > 0) {
-                    if constexpr (NQ == 1) {
-                        prompt_wait(pvdone + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, dead, err);
-                        tc_fence_after();
+                    for (int k = 0; k < 32; k += 4) {
+                        mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])));
+                        mx2 = fmaxf(mx2, fmaxf(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])));
                     }
+                mx = fmaxf(mx, mx2);
+                const bool move = (mx - m) * c > 8.f;  // also from -inf to the first score
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
+                    if (move) m = mx;
+                    l *= f;
+                    if (j > 0) {
+                        if constexpr (NQ == 1) {
+                            // the products of the tile before, of the other buffer
+                            const int pb = (j - 1) & 1;
+                            prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(so + i, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st32(so + i, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
+                uint64_t la = 0, lb = 0;  // sums of even and odd pairs
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        float x[4];
+                        prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])), c2, mc2),
+                                      x[0], x[1]);
+                        prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])), c2, mc2),
+                                      x[2], x[3]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) x[u] = prompt_exp2(x[u]);
+                        la = prompt_add2(la, prompt_pair(x[0], x[1]));
+                        lb = prompt_add2(lb, prompt_pair(x[2], x[3]));
+                        p[k / 2] = prompt_pack<C::BF16>(x[0], x[1]);
+                        p[k / 2 + 1] = prompt_pack<C::BF16>(x[2], x[3]);
+                    }
+                    tmem_st16(ss + 16 * i, p);
+                    if ((NQ == 1 && i == BN / 64 - 1) || i == BN / 32 - 1) {
+                        // d = 256: half of the keys, whose value products may start
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pready + 16 * buf + (i == BN / 32 - 1 ? 8 : 0));
+                    }
+                }
+                float x0, x1;
+                prompt_unpair(prompt_add2(la, lb), x0, x1);
+                l += x0 + x1;
+            }
+            if (nt > 0) {
+                const int buf = NQ == 2 ? t : (nt - 1) & 1, use = (buf ? use1 : use0) + (NQ == 2 ? nt - 1 : (nt - 1) >> 1);
+                prompt_wait(pvdone + 8 * buf, use & 1, dead, err);
+                tc_fence_after();
+            }
+            if (a.parts > 1) {
+                const int64_t at = (int64_t)w.part * a.n_q * a.q_heads + row;
+                if (nt > 0) {
 #pragma unroll 1
                     for (int i = 0; i < D; i += 32) {
                         uint32_t o[32];
                         tmem_ld32(so + i, o);
                         tc_wait_ld();
+                        if (live) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.part + at * D + i);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st32(so + i, o);
+                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
                     }
                 }
-            }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
-            uint64_t la = 0, lb = 0;  // sums of even and odd pairs
-#pragma unroll
-            for (int i = 0; i < BN / 32; ++i) {
-                uint32_t p[16];
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    float x[4];
-                    prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])), c2, mc2),
-                                  x[0], x[1]);
-                    prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])), c2, mc2),
-                                  x[2], x[3]);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[u] = prompt_exp2(x[u]);
-                    la = prompt_add2(la, prompt_pair(x[0], x[1]));
-                    lb = prompt_add2(lb, prompt_pair(x[2], x[3]));
-                    p[k / 2] = prompt_pack<C::BF16>(x[0], x[1]);
-                    p[k / 2 + 1] = prompt_pack<C::BF16>(x[2], x[3]);
-                }
-                tmem_st16(ss + 16 * i, p);
-                if (i == BN / 64 - 1 || i == BN / 32 - 1) {
-                    // half of the keys: their value products may start
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(pready + 16 * buf + (i == BN / 32 - 1 ? 8 : 0));
-                }
-            }
-            {
-                float x0, x1;
-                prompt_unpair(prompt_add2(la, lb), x0, x1);
-                l += x0 + x1;
-            }
-        }
-        if (nt > 0) {
-            if constexpr (NQ == 2) prompt_wait(pvdone + 8 * t, (nt - 1) & 1, dead, err);
-            else prompt_wait(pvdone + 8 * ((nt - 1) & 1), ((nt - 1) >> 1) & 1, dead, err);
-            tc_fence_after();
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t row = (int64_t)(w.q0 + tok) * a.q_heads + w.row * a.group + head;
-        uint16_t* out = static_cast<uint16_t*>(a.out) + row * D;
+                if (live) a.meta[at] = make_float2(m, l);
+            } else {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint16_t* out = static_cast<uint16_t*>(a.out) + row * D;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            if (nt > 0) {
-                tmem_ld32(so + i, o);
-                tc_wait_ld();
-            }
-            if (live) {
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tmem_ld32(so + i, o);
+                        tc_wait_ld();
+                    }
+                    if (live) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    uint32_t p[4];
+                        for (int k = 0; k < 32; k += 8) {
+                            uint32_t p[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        p[u] = l == 0.f ? 0u
-                                        : prompt_pack<C::BF16>(__uint_as_float(o[k + 2 * u]) * inv,
-                                                               __uint_as_float(o[k + 2 * u + 1]) * inv);
-                    *reinterpret_cast<uint4*>(out + i + k) = make_uint4(p[0], p[1], p[2], p[3]);
+                            for (int u = 0; u < 4; ++u)
+                                p[u] = l == 0.f ? 0u
+                                                : prompt_pack<C::BF16>(__uint_as_float(o[k + 2 * u]) * inv,
+                                                                       __uint_as_float(o[k + 2 * u + 1]) * inv);
+                            *reinterpret_cast<uint4*>(out + i + k) = make_uint4(p[0], p[1], p[2], p[3]);
+                        }
+                    }
                 }
+                if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
             }
+            // (the next item's first value products wait for its probabilities,
+            // which this warp signals after these reads of the output)
+            advance(w);
         }
-        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
     }
     tc_fence_before();
     __syncthreads();
@@ -589,21 +706,88 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-template <class C>
-tq_status launch_prompt(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                        cudaStream_t s) {
-    const tq_status st = ensure_dynamic_smem((const void*)prompt_kernel<C>, C::total, "prompt_kernel");
-    if (st != TQ_OK) return st;
-    // every sequence's last block may be short of rows; blocks without work return at once
-    const int64_t items = (int64_t)a.n_q / (C::NQ * a.tile_tok) + a.batch;
-    if (items * a.heads > 0x7FFFFFFF) return TQ_ERR_INVALID_ARG;
-    prompt_kernel<C><<<(unsigned)(items * a.heads), C::THREADS, C::total, s>>>(a, mq, mk, mv);
-    return cuda_status(cudaGetLastError());
+// Add the parts of every row up.  One block per query row, one warp per head at a
+// time; a part without a key of the row has l = 0 and no sums.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = blockIdx.x;
+    pdl_wait();
+    // rows no sequence names are left as they were
+    bool mine = false;
+    for (int b = lane; b < a.batch; b += 32) mine |= __ldg(a.cu_q + b) <= tok && tok < __ldg(a.cu_q + b + 1);
+    if (!__any_sync(0xffffffffu, mine)) return;
+    const int64_t rows = (int64_t)a.n_q * a.q_heads;
+    for (int h = warp; h < a.q_heads; h += 8) {
+        const int64_t row = (int64_t)tok * a.q_heads + h;
+        // lane z: part z
+        const float2 ml = lane < a.parts ? __ldcg(a.meta + lane * rows + row) : make_float2(-INFINITY, 0.f);
+        const float M = warp_max(ml.x);
+        const float f = ml.y == 0.f ? 0.f : M == -INFINITY ? 1.f : prompt_exp2((ml.x - M) * a.scale_log2);
+        const float l = warp_sum(ml.y == 0.f ? 0.f : ml.y * f);
+        float o[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+        for (int z = 0; z < a.parts; ++z) {
+            const float fz = __shfl_sync(0xffffffffu, f, z);
+            if (__shfl_sync(0xffffffffu, ml.y, z) == 0.f) continue;
+            const float4* p = reinterpret_cast<const float4*>(a.part + (z * rows + row) * D) + lane;
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+                const float4 x = __ldcg(p + 32 * i);
+                o[4 * i] = fmaf(x.x, fz, o[4 * i]), o[4 * i + 1] = fmaf(x.y, fz, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(x.z, fz, o[4 * i + 2]), o[4 * i + 3] = fmaf(x.w, fz, o[4 * i + 3]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int i = 0; i < D / 128; ++i)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 128 * i + 4 * lane) =
+                make_uint2(prompt_pack<BF16>(o[4 * i] * inv, o[4 * i + 1] * inv),
+                           prompt_pack<BF16>(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
+        if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : M * a.scale + logf(l);
+    }
 }
 
-tq_status launch_prompt_128(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                            bool bf16, cudaStream_t s);
-tq_status launch_prompt_256(const PromptArgs& a, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
-                            bool bf16, cudaStream_t s);
+// Parts of the keys: as many as shorten the longest run of a block, the join
+// (about 5 us) counted in.  The lengths are on the device; what the host knows is
+// the row counts.
+template <class C>
+int prompt_parts(const PromptArgs& a, int64_t items, int sms, int64_t part_rows) {
+    const double keys = (double)a.n_k - (a.causal ? 0.5 * std::min(a.n_q, a.n_k) : 0.0);
+    const double tiles = keys / a.batch / C::BN, tile_us = C::D == 128 ? 1.4 : 0.85;
+    int best = 1;
+    double best_us = 0;
+    for (int z = 1; z <= kPromptParts; ++z) {
+        if (z > 1 && ((int64_t)z * a.n_q * a.q_heads > part_rows || tiles < 2 * z)) break;
+        const double waves = (double)((items * z + sms - 1) / sms);
+        const double us = waves * (tiles / z * tile_us + 2.0) + (z > 1 ? 5.0 + 0.3 * z : 0.0);
+        if (z == 1 || us < 0.95 * best_us) best = z, best_us = us;
+    }
+    return best;
+}
+
+template <class C>
+tq_status launch_prompt(PromptArgs a, int64_t part_rows, const CUtensorMap& mq, const CUtensorMap& mk,
+                        const CUtensorMap& mv, cudaStream_t s) {
+    int sms = 0;
+    tq_status st = device_sms(&sms);
+    if (st == TQ_OK) st = ensure_dynamic_smem((const void*)prompt_kernel<C>, C::total, "prompt_kernel");
+    if (st != TQ_OK) return st;
+    // at most this many items: the last tile of every sequence may be short of rows
+    const int per = C::NQ * a.tile_tok;
+    const int64_t items = ((int64_t)a.n_q + (int64_t)a.batch * (per - 1)) / per * a.heads;
+    a.parts = prompt_parts<C>(a, items, sms, part_rows);
+    const int grid = (int)std::min<int64_t>(items * a.parts, sms);
+    prompt_kernel<C><<<grid, C::THREADS, C::total, s>>>(a, mq, mk, mv);
+    st = cuda_status(cudaGetLastError());
+    if (st == TQ_OK && a.parts > 1)
+        st = cuda_status(launch_pdl(true, prompt_join_kernel<C::D, C::BF16>, dim3(a.n_q), dim3(256), 0, s, a));
+    return st;
+}
+
+tq_status launch_prompt_128(const PromptArgs& a, int64_t part_rows, const CUtensorMap& mq, const CUtensorMap& mk,
+                            const CUtensorMap& mv, bool bf16, cudaStream_t s);
+tq_status launch_prompt_256(const PromptArgs& a, int64_t part_rows, const CUtensorMap& mq, const CUtensorMap& mk,
+                            const CUtensorMap& mv, bool bf16, cudaStream_t s);
 
 }  // namespace tq
