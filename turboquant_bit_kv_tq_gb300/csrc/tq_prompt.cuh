@@ -18,10 +18,12 @@
 //
 // Softmax: thread = row; its scores come from tensor memory into registers, the
 // probabilities (rounded to the inputs' 16-bit type, the row sum is of the
-// unrounded ones) go back as the A operand of P V, in two halves of the keys so
-// that the products of the first run beside the exponentials of the second.  The reference m moves only
+// unrounded ones) go back as the A operand of P V.  The reference m moves only
 // when it falls 2^8 behind, so that the output in tensor memory is rescaled
-// rarely; that is exact, the final quotient does not depend on m.
+// rarely, and it moves a tile late: a tile's exponentials do not wait for its
+// maximum, unless that lies so far ahead that they might overflow (2^14 for fp16
+// probabilities, 2^20 for bf16), when they are done again.  That is exact, the
+// final quotient does not depend on m.
 //
 // One block per SM takes items until none is left (the first by its index, the
 // next from a counter), longest first, so that the copies and score products of
@@ -70,6 +72,9 @@ struct PromptCfg {
     // traffic, 6 KB per MMA of 32 cycles with both operands there, would bound them)
     static constexpr bool QT = D == 256;
     static constexpr int STAGES = QT ? 7 : 5;
+    // how far (log2) a score may lie above the reference before a tile is done again:
+    // the probabilities' range, with room for the sums
+    static constexpr float AHEAD_LOG2 = BF16 ? 20.f : 14.f;
     // ring order: AHEAD key tiles, then value tile 0, key tile AHEAD, value tile 1, ...
     static constexpr int AHEAD = NQ == 2 ? 1 : 2;
     static __host__ __device__ constexpr int key_pos(int j) { return j < AHEAD ? j : 2 * j - AHEAD + 1; }
@@ -134,6 +139,11 @@ __device__ __forceinline__ float prompt_exp2(float x) {
 }
 constexpr int kPromptParts = 16;  // key parts at most (a lane each in the join)
 
+__device__ __forceinline__ float prompt_max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t prompt_pack(float lo, float hi) {
     if constexpr (BF16) {
@@ -268,10 +278,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::off_bar);
     const uint32_t full = smem_u32(bars), empty = full + 8 * S, qfull = empty + 8 * S, qfree = qfull + 8,
-                   sfull = qfree + 8, pready = sfull + 16, pvdone = pready + 32, turn = pvdone + 16, wfull = turn + 16,
+                   sfull = qfree + 8, pready = sfull + 16, pvdone = pready + 16, turn = pvdone + 16, wfull = turn + 16,
                    wfree = wfull + 16, vclean = wfree + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 3 * S + 16);
-    static_assert((3 * S + 16) * 8 + 4 <= C::BAR, "barriers");
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 3 * S + 14);
+    static_assert((3 * S + 14) * 8 + 4 <= C::BAR, "barriers");
     __shared__ PromptWork s_w[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int W0 = C::SOFT / 32;  // first of the other four warps: copies, MMA
@@ -287,8 +297,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         mbar_init(qfree, 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(sfull + 8 * t, 1);
-            mbar_init(pready + 16 * t, 4);  // the first and the second half of the keys
-            mbar_init(pready + 16 * t + 8, 4);
+            mbar_init(pready + 8 * t, 4);
             mbar_init(pvdone + 8 * t, 1);
             mbar_init(turn + 8 * t, 1);
             mbar_init(wfull + 8 * t, 1);
@@ -416,13 +425,16 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
                     return r % S;
                 };
-                auto scores = [&](int buf, int t, int s) {
-                    const uint64_t qd = q_desc + (uint64_t)(t * (C::QB >> 4));
+                // `early` runs before the last three MMAs: what it lets another thread
+                // issue lines up behind them
+                auto scores = [&](int buf, int t, int s, auto early) {
+                    [[maybe_unused]] const uint64_t qd = q_desc + (uint64_t)(t * (C::QB >> 4));
                     const uint64_t kd = k_desc + (uint64_t)(s * (C::KB >> 4));
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t b = kd + (uint64_t)(((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4);
+                        if (k == D / 16 - 3) early();
                         if constexpr (C::QT)
                             prompt_mma_ts(tmem + C::COL_S + buf * BN, tmem + C::COL_Q + 8 * k, b, id_s, k > 0);
                         else
@@ -431,18 +443,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     }
                     tc_commit(sfull + 8 * buf);
                 };
-                // (d = 128: both halves of the probabilities have been waited for)
-                auto values = [&](int buf, int t, int s, bool first, uint32_t parity) {
+                auto values = [&](int buf, int t, int s, bool first) {
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::KB >> 4));
+                    tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (NQ == 1) prompt_wait(pready + 16 * buf + 8 * h, parity, dead, err);
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
-                            prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * k,
-                                          vd + (uint64_t)((k * 2048) >> 4), id_o, !(first && k == 0));
-                    }
+                    for (int k = 0; k < BN / 16; ++k)
+                        prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * k,
+                                      vd + (uint64_t)((k * 2048) >> 4), id_o, !(first && k == 0));
                     tc_commit(pvdone + 8 * buf);
                 };
                 int q_uses = 0, turns = 0;
@@ -478,20 +485,20 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         prompt_wait(qfull, q_uses & 1, dead, err);
                         int ks = take(C::key_pos(0));
                         begin();
-                        if (mine > 0) scores(me, me, ks);
-                        pass();
+                        if (mine > 0) scores(me, me, ks, pass);
+                        else pass();
                         tc_commit(empty + 8 * ks);
                         if (mine <= 1) tc_commit(qfree);
                         for (int j = 0; j < n; ++j) {
                             const int vs = value_tile(j);
                             if (j + 1 < n) ks = take(C::key_pos(j + 1));
-                            if (j < mine) prompt_wait(pready + 16 * me + 8, (use + j) & 1, dead, err);
                             begin();
-                            if (j < mine) values(me, me, vs, j == 0, 0);
+                            if (j < mine) prompt_wait(pready + 8 * me, (use + j) & 1, dead, err);
+                            if (j < mine) values(me, me, vs, j == 0);
                             // (these scores overwrite the probabilities, whose products this
                             // thread issued before: MMAs of a thread run in order)
-                            if (j + 1 < mine) scores(me, me, ks);
-                            pass();
+                            if (j + 1 < mine) scores(me, me, ks, pass);
+                            else pass();
                             tc_commit(empty + 8 * vs);
                             if (j + 1 < n) tc_commit(empty + 8 * ks);
                             if (j + 2 == mine) tc_commit(qfree);  // the tile's last scores are issued
@@ -506,15 +513,15 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                             const int use = (j & 1 ? use1 : use0) + (j >> 1);
                             if (use > 0) prompt_wait(pvdone + 8 * (j & 1), (use - 1) & 1, dead, err);
                             const int ks = take(C::key_pos(j));
-                            scores(j & 1, 0, ks);
+                            scores(j & 1, 0, ks, [] {});
                             tc_commit(empty + 8 * ks);
                         }
                     } else {
                         for (int j = 0; j < n; ++j) {
                             const int use = (j & 1 ? use1 : use0) + (j >> 1);
-                            prompt_wait(pready + 16 * (j & 1), use & 1, dead, err);
+                            prompt_wait(pready + 8 * (j & 1), use & 1, dead, err);
                             const int vs = value_tile(j);
-                            values(j & 1, 0, vs, j == 0, use & 1);
+                            values(j & 1, 0, vs, j == 0);
                             tc_commit(empty + 8 * vs);
                         }
                     }
@@ -566,7 +573,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     if (lane == 0) mbar_arrive(qfull);
                 }
             }
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, mx = -INFINITY;
             for (int j = 0; j < nt; ++j) {
                 const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
                 const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
@@ -584,70 +591,94 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         for (int k = 0; k < 32; ++k)
                             if (32 * i + k >= cut) s[i][k] = 0xFF800000u;
                 }
-                float mx = -INFINITY, mx2 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < BN / 32; ++i)
+                float xa = -INFINITY, xb = -INFINITY;  // maximum of the tile
+                auto chunk_max = [&](int i) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])));
-                        mx2 = fmaxf(mx2, fmaxf(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])));
+                        xa = prompt_max3(xa, __uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1]));
+                        xb = prompt_max3(xb, __uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3]));
                     }
-                mx = fmaxf(mx, mx2);
-                const bool move = (mx - m) * c > 8.f;  // also from -inf to the first score
-                if (__any_sync(0xffffffffu, move)) {
-                    const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
-                    if (move) m = mx;
-                    l *= f;
-                    if (j > 0) {
-                        if constexpr (NQ == 1) {
-                            // the products of the tile before, of the other buffer
-                            const int pb = (j - 1) & 1;
-                            prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
-                            tc_fence_after();
-                        }
-#pragma unroll 1
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(so + i, o);
-                            tc_wait_ld();
+                };
+                if (j == 0) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st32(so + i, o);
-                        }
-                    }
+                    for (int i = 0; i < BN / 32; ++i) chunk_max(i);
+                    mx = fmaxf(xa, xb);
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
-                uint64_t la = 0, lb = 0;  // sums of even and odd pairs
+                float lj;
+                bool again = false;
+                do {
+                    // mx: the maximum up to the last tile (the first time), or up to this one
+                    const bool move = (mx - m) * c > 8.f;  // also from -inf to the first score
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
+                        if (move) m = mx;
+                        l *= f;
+                        if (j > 0) {
+                            if constexpr (NQ == 1) {
+                                // the products of the tile before, of the other buffer
+                                const int pb = (j - 1) & 1;
+                                prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
+                                tc_fence_after();
+                            }
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(so + i, o);
+                                tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st32(so + i, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
+                    uint64_t la = 0, lb = 0;  // sums of even and odd pairs
+                    // groups of four scores in three stages (argument; exponential;
+                    // sum, rounding, maximum), a group apart, so that the
+                    // exponentials, 4 cycles each, have the rest in their shadow
+                    uint64_t arg[2][2];
+                    float x[2][4];
                     uint32_t p[16];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float x[4];
-                        prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k]), __uint_as_float(s[i][k + 1])), c2, mc2),
-                                      x[0], x[1]);
-                        prompt_unpair(prompt_fma2(prompt_pair(__uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3])), c2, mc2),
-                                      x[2], x[3]);
+                    for (int g = 0; g < BN / 4 + 2; ++g) {
+                        if (g < BN / 4) {
+                            const uint32_t* v = &s[g >> 3][4 * (g & 7)];
+                            arg[g & 1][0] = prompt_fma2(prompt_pair(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, mc2);
+                            arg[g & 1][1] = prompt_fma2(prompt_pair(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, mc2);
+                        }
+                        if (g >= 1 && g <= BN / 4) {
+                            float* y = x[(g - 1) & 1];
+                            prompt_unpair(arg[(g - 1) & 1][0], y[0], y[1]);
+                            prompt_unpair(arg[(g - 1) & 1][1], y[2], y[3]);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) x[u] = prompt_exp2(x[u]);
-                        la = prompt_add2(la, prompt_pair(x[0], x[1]));
-                        lb = prompt_add2(lb, prompt_pair(x[2], x[3]));
-                        p[k / 2] = prompt_pack<C::BF16>(x[0], x[1]);
-                        p[k / 2 + 1] = prompt_pack<C::BF16>(x[2], x[3]);
+                            for (int u = 0; u < 4; ++u) y[u] = prompt_exp2(y[u]);
+                        }
+                        if (g >= 2) {
+                            const int h = g - 2;
+                            const float* y = x[h & 1];
+                            const uint32_t* v = &s[h >> 3][4 * (h & 7)];
+                            la = prompt_add2(la, prompt_pair(y[0], y[1]));
+                            lb = prompt_add2(lb, prompt_pair(y[2], y[3]));
+                            p[2 * (h & 7)] = prompt_pack<C::BF16>(y[0], y[1]);
+                            p[2 * (h & 7) + 1] = prompt_pack<C::BF16>(y[2], y[3]);
+                            xa = prompt_max3(xa, __uint_as_float(v[0]), __uint_as_float(v[1]));
+                            xb = prompt_max3(xb, __uint_as_float(v[2]), __uint_as_float(v[3]));
+                            if ((h & 7) == 7) tmem_st16(ss + 16 * (h >> 3), p);
+                        }
                     }
-                    tmem_st16(ss + 16 * i, p);
-                    if ((NQ == 1 && i == BN / 64 - 1) || i == BN / 32 - 1) {
-                        // d = 256: half of the keys, whose value products may start
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pready + 16 * buf + (i == BN / 32 - 1 ? 8 : 0));
-                    }
-                }
-                float x0, x1;
-                prompt_unpair(prompt_add2(la, lb), x0, x1);
-                l += x0 + x1;
+                    float x0, x1;
+                    prompt_unpair(prompt_add2(la, lb), x0, x1);
+                    lj = x0 + x1;
+                    if (again) break;
+                    mx = prompt_max3(mx, xa, xb);
+                    again = __any_sync(0xffffffffu, (mx - m) * c > C::AHEAD_LOG2);
+                } while (again);
+                l += lj;
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready + 8 * buf);
             }
             if (nt > 0) {
                 const int buf = NQ == 2 ? t : (nt - 1) & 1, use = (buf ? use1 : use0) + (NQ == 2 ? nt - 1 : (nt - 1) >> 1);
@@ -672,7 +703,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 if (live) a.meta[at] = make_float2(m, l);
             } else {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t* out = static_cast<uint16_t*>(a.out) + row * D;
+                // four lanes write 64 bytes of one row side by side (a lane alone
+                // would touch 32 lines with every store): lane u of a quad ends up
+                // with 16-byte piece u of the quad's four rows
+                const int u = lane & 3;
+                int64_t rows[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(0xffffffffu, live ? row : -1, (lane & ~3) + r);
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
@@ -680,18 +717,30 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         tmem_ld32(so + i, o);
                         tc_wait_ld();
                     }
-                    if (live) {
+                    uint32_t p[4][4];  // [piece][word]
 #pragma unroll
-                        for (int k = 0; k < 32; k += 8) {
-                            uint32_t p[4];
+                    for (int k = 0; k < 16; ++k)
+                        p[k >> 2][k & 3] = l == 0.f ? 0u
+                                                    : prompt_pack<C::BF16>(__uint_as_float(o[2 * k]) * inv,
+                                                                           __uint_as_float(o[2 * k + 1]) * inv);
+                    // 4 x 4 transposition over the quad: swap pieces with lane ^ 1, then with lane ^ 2
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                p[u] = l == 0.f ? 0u
-                                                : prompt_pack<C::BF16>(__uint_as_float(o[k + 2 * u]) * inv,
-                                                                       __uint_as_float(o[k + 2 * u + 1]) * inv);
-                            *reinterpret_cast<uint4*>(out + i + k) = make_uint4(p[0], p[1], p[2], p[3]);
-                        }
-                    }
+                    for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (!(q & b))
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const uint32_t send = u & b ? p[q][x] : p[q | b][x];
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, send, b);
+                                    if (u & b) p[q][x] = got;
+                                    else p[q | b][x] = got;
+                                }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (rows[r] >= 0)
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + rows[r] * D + i + 8 * u) =
+                                make_uint4(p[r][0], p[r][1], p[r][2], p[r][3]);
                 }
                 if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
             }
