@@ -129,8 +129,6 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
         k_stride = v_stride = q_stride;
     }
     PromptArgs a;
-    a.q = q;
-    a.q_stride = q_stride;
     a.out = out;
     a.lse = lse;
     a.cu_q = cu_q;
@@ -153,9 +151,8 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
     const bool bf16 = c.dtype == TQ_DTYPE_BF16;
     CUtensorMap mq, mk, mv;
     tq_status st = prompt_map(&mq, q, bf16, d, a.group, a.heads, n_q, q_stride, a.tile_tok);
-    const int bn = d == 128 ? 128 : 64;
-    if (st == TQ_OK) st = prompt_map(&mk, k, bf16, d, 0, a.heads, n_k > 0 ? n_k : n_q, k_stride, bn);
-    if (st == TQ_OK) st = prompt_map(&mv, v, bf16, d, 0, a.heads, n_k > 0 ? n_k : n_q, v_stride, bn);
+    if (st == TQ_OK) st = prompt_map(&mk, k, bf16, d, 0, a.heads, n_k > 0 ? n_k : n_q, k_stride, 128);
+    if (st == TQ_OK) st = prompt_map(&mv, v, bf16, d, 0, a.heads, n_k > 0 ? n_k : n_q, v_stride, d == 128 ? 128 : 64);
     if (st != TQ_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
     return d == 128 ? launch_prompt_128(a, p->part_rows, mq, mk, mv, bf16, s)

@@ -5,12 +5,13 @@
 //   out_i = sum_j p_ij v_j / sum_j p_ij;   lse_i = scale m_i + ln sum_j p_ij
 //
 // Bound by the tensor cores (2 d multiply-adds per query head, row and visible
-// key).  A work item is 128-row query tiles of one sequence and KV head; a tile's rows are the G query heads of floor(128 / G) tokens, so a group
-// shares every key tile and short prompts still fill the rows.  d = 128: two
-// tiles of queries, 128 keys at a time; d = 256: one tile, 64 keys at a time
-// (its output alone fills half of tensor memory).  Either way a block has two
-// score buffers of one step each, and the tensor cores work on one step's
-// products while the softmax of the other runs:
+// key).  A work item is 128-row query tiles of one sequence and KV head; a tile's
+// rows are the G query heads of floor(128 / G) tokens, so a group shares every key
+// tile and short prompts still fill the rows.  d = 128: two tiles of queries; d =
+// 256: one (its output alone fills half of tensor memory); 128 keys at a time.
+// (64 keys were slower at d = 256: an MMA of 64 columns takes as long as one of
+// 128.)  Either way a block has two score buffers of one step each, and the tensor
+// cores work on one step's products while the softmax of the other runs:
 //   step i uses score buffer i & 1; d = 128: key tile i / 2 of query tile i & 1,
 //   d = 256: key tile i.
 //   MMA order: ... P V of step i, scores of step i + 2, P V of step i + 1, ...
@@ -45,8 +46,6 @@
 namespace tq {
 
 struct PromptArgs {
-    const void* q;
-    int64_t q_stride;
     void* out;
     float* lse;
     const int32_t *cu_q, *cu_k;
@@ -65,17 +64,17 @@ struct PromptCfg {
     static constexpr int D = D_;
     static constexpr bool BF16 = BF16_;
     static constexpr int NQ = D == 128 ? 2 : 1;  // query tiles per block
-    static constexpr int BN = D == 128 ? 128 : 64;
+    static constexpr int BN = 128;               // keys per tile
+    static constexpr int EN = D / 128;           // ring entries per key or value tile
     static constexpr int CH = D / 64;            // 64-element chunks (128-byte swizzled rows)
-    static constexpr int QB = 128 * D * 2, KB = BN * D * 2;  // bytes of a query / key tile
-    // d = 256: the query tile goes to tensor memory (the score products' shared-memory
-    // traffic, 6 KB per MMA of 32 cycles with both operands there, would bound them)
-    static constexpr bool QT = D == 256;
-    static constexpr int STAGES = QT ? 7 : 5;
+    // bytes of a query tile and of a ring entry: 128 keys x 128 elements, or the
+    // values of 128 / EN keys
+    static constexpr int QB = 128 * D * 2, KB = 128 * 128 * 2, VN = BN / EN;
+    static constexpr int STAGES = 5;
     // how far (log2) a score may lie above the reference before a tile is done again:
     // the probabilities' range, with room for the sums
     static constexpr float AHEAD_LOG2 = BF16 ? 20.f : 14.f;
-    // ring order: AHEAD key tiles, then value tile 0, key tile AHEAD, value tile 1, ...
+    // order of the tiles in the ring: AHEAD key tiles, then value tile 0, key tile AHEAD, value tile 1, ...
     static constexpr int AHEAD = NQ == 2 ? 1 : 2;
     static __host__ __device__ constexpr int key_pos(int j) { return j < AHEAD ? j : 2 * j - AHEAD + 1; }
     static __host__ __device__ constexpr int value_pos(int j, int n) {
@@ -85,12 +84,12 @@ struct PromptCfg {
     static constexpr int SOFT = 128 * NQ;        // softmax threads
     static constexpr int THREADS = SOFT + 128;
     // tensor memory: scores (probabilities in place), then outputs
-    static constexpr int COL_S = 0, COL_O = 2 * BN, COL_Q = COL_O + NQ * D;
-    static constexpr int off_ring = QT ? 0 : NQ * QB;
+    static constexpr int COL_S = 0, COL_O = 2 * BN;
+    static constexpr int off_ring = NQ * QB;
     static constexpr int off_bar = off_ring + STAGES * KB;
     static constexpr int BAR = 320;
     static constexpr int total = off_bar + BAR + 1024;  // + alignment to 1024
-    static_assert(COL_Q + (QT ? D / 2 : 0) <= 512, "tensor memory");
+    static_assert(COL_O + NQ * D <= 512, "tensor memory");
     static_assert(total <= 232448, "shared memory");
 };
 
@@ -293,8 +292,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             mbar_init(empty + 8 * s, NQ);
             mbar_init(vclean + 8 * s, 1);
         }
-        mbar_init(qfull, C::QT ? 4 : 1);
-        mbar_init(qfree, 2);
+        mbar_init(qfull, 1);
+        mbar_init(qfree, NQ);
         for (int t = 0; t < 2; ++t) {
             mbar_init(sfull + 8 * t, 1);
             mbar_init(pready + 8 * t, 4);
@@ -315,7 +314,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     // uses of a score buffer) gives the parities of its waits.
     int ring = 0, use0 = 0, use1 = 0;
     auto advance = [&](const PromptWork& w) {
-        ring += 2 * w.tiles();
+        ring += 2 * C::EN * w.tiles();
         use0 += NQ == 2 ? w.n[0] : (w.tiles() + 1) / 2;
         use1 += NQ == 2 ? w.n[1] : w.tiles() / 2;
     };
@@ -343,34 +342,40 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 if (!w.ok) break;
                 const int n = w.tiles();
                 if (lane == 0 && n > 0 && !dead) {
-                    if constexpr (!C::QT) {
-                        if (q_loads > 0) prompt_wait(qfree, (q_loads - 1) & 1, dead, err);
-                        if (!dead) {
-                            ++q_loads;
-                            // the tokens of both tiles that exist (rows of others come along and are not used)
-                            const int tiles = NQ == 2 && w.n[1] > 0 ? 2 : 1;
-                            mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
-                            for (int t = 0; t < tiles; ++t)
-                                for (int c = 0; c < CH; ++c)
-                                    tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
-                                           w.q0 + w.t0 + t * a.tile_tok, qfull);
-                        }
-                    }
-                    auto load = [&](const CUtensorMap* m, int j) {
-                        const int s = loads % S;
-                        if (loads >= S) prompt_wait(empty + 8 * s, ((loads / S) - 1) & 1, dead, err);
-                        if (!dead) {
-                            mbar_expect_tx(full + 8 * s, C::KB);
+                    if (q_loads > 0) prompt_wait(qfree, (q_loads - 1) & 1, dead, err);
+                    if (!dead) {
+                        ++q_loads;
+                        // the tokens of both tiles that exist (rows of others come along and are not used)
+                        const int tiles = NQ == 2 && w.n[1] > 0 ? 2 : 1;
+                        mbar_expect_tx(qfull, (uint32_t)(tiles * CH * a.tile_tok * a.group * 128));
+                        for (int t = 0; t < tiles; ++t)
                             for (int c = 0; c < CH; ++c)
-                                tma_3d(smem_u32(smem) + C::off_ring + s * C::KB + c * (BN * 128), m, 64 * c, w.row,
-                                       w.k0 + (w.j0 + j) * BN, full + 8 * s);
+                                tma_4d(smem_u32(smem) + t * C::QB + c * (128 * 128), &mq, 64 * c, 0, w.row,
+                                       w.q0 + w.t0 + t * a.tile_tok, qfull);
+                    }
+                    // a key tile goes in by halves of the elements, a value tile by
+                    // halves of the keys (at d = 128 either in one piece)
+                    auto load = [&](bool key, int j) {
+                        for (int h = 0; h < C::EN; ++h) {
+                            const int s = loads % S;
+                            if (loads >= S) prompt_wait(empty + 8 * s, ((loads / S) - 1) & 1, dead, err);
+                            if (dead) return;
+                            const uint32_t dst = smem_u32(smem) + C::off_ring + s * C::KB;
+                            const int k0 = w.k0 + (w.j0 + j) * BN;
+                            mbar_expect_tx(full + 8 * s, C::KB);
+                            if (key)
+                                for (int c = 0; c < 2; ++c)
+                                    tma_3d(dst + c * (BN * 128), &mk, 64 * (2 * h + c), w.row, k0, full + 8 * s);
+                            else
+                                for (int c = 0; c < CH; ++c)
+                                    tma_3d(dst + c * (C::VN * 128), &mv, 64 * c, w.row, k0 + h * C::VN, full + 8 * s);
                             ++loads;
                         }
                     };
-                    for (int j = 0; j < C::AHEAD && j < n; ++j) load(&mk, j);
+                    for (int j = 0; j < C::AHEAD && j < n; ++j) load(true, j);
                     for (int j = 0; j < n; ++j) {
-                        load(&mv, j);
-                        if (j + C::AHEAD < n) load(&mk, j + C::AHEAD);
+                        load(false, j);
+                        if (j + C::AHEAD < n) load(true, j + C::AHEAD);
                     }
                 }
                 __syncwarp();
@@ -379,19 +384,20 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 uint32_t next = 0;
                 if (lane == 0) next = atomicAdd(a.next, 1u);
                 dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
-                ring += 2 * n;
+                ring += 2 * C::EN * n;
                 // zero the value rows behind the sequence's last key: 0 * NaN or inf
-                // of a neighbour's row would be NaN.  The item's last copy has them.
-                if (w.ragged<BN>()) {
-                    const int s = (ring - 1) % S;
-                    prompt_wait(full + 8 * s, ((ring - 1) / S) & 1, dead, err);
-                    uint8_t* v = smem + C::off_ring + s * C::KB;
-                    for (int i = lane; i < CH * BN * 8; i += 32)
-                        if ((i >> 3) % BN >= w.lk % BN) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(vclean + 8 * s);
-                }
+                // of a neighbour's row would be NaN.  The item's last copies have them.
+                if (w.ragged<BN>())
+                    for (int h = 0; h < C::EN; ++h) {
+                        const int r = ring - C::EN + h, s = r % S, keep = w.lk % BN - h * C::VN;
+                        prompt_wait(full + 8 * s, (r / S) & 1, dead, err);
+                        uint8_t* v = smem + C::off_ring + s * C::KB;
+                        for (int i = lane; i < C::KB / 16; i += 32)
+                            if ((i >> 3) % C::VN >= keep) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(vclean + 8 * s);
+                    }
                 dead = __any_sync(0xffffffffu, (int)dead);
                 item = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
             }
@@ -401,7 +407,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     bool d2 = false;
                     for (int i = max(0, loads - S); i < loads; ++i) prompt_wait(full + 8 * (i % S), (i / S) & 1, d2, err);
                     d2 = false;
-                    if (!C::QT && q_loads > 0) prompt_wait(qfull, (q_loads - 1) & 1, d2, err);
+                    if (q_loads > 0) prompt_wait(qfull, (q_loads - 1) & 1, d2, err);
                 }
                 // the last block leaves the counters ready for the next call
                 if (atomicAdd(a.next + 1, 1u) == gridDim.x - 1) a.next[0] = a.next[1] = 0;
@@ -419,38 +425,36 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 const int me = warp - (W0 + 1);
                 const uint64_t q_desc = prompt_desc(smem_u32(smem), 16);
                 const uint64_t k_desc = prompt_desc(smem_u32(smem) + C::off_ring, 16);
-                const uint64_t v_desc = prompt_desc(smem_u32(smem) + C::off_ring, BN * 128);
-                auto take = [&](int pos) {  // ring position `pos` of the item
-                    const int r = ring + pos;
+                const uint64_t v_desc = prompt_desc(smem_u32(smem) + C::off_ring, C::VN * 128);
+                auto take = [&](int pos, int h) {  // entry h of the tile at `pos` of the item's ring order
+                    const int r = ring + C::EN * pos + h;
                     prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
                     return r % S;
                 };
-                // `early` runs before the last three MMAs: what it lets another thread
-                // issue lines up behind them
-                auto scores = [&](int buf, int t, int s, auto early) {
-                    [[maybe_unused]] const uint64_t qd = q_desc + (uint64_t)(t * (C::QB >> 4));
+                // element half h of a key tile.  `early` runs before the last three
+                // MMAs: what it lets another thread issue lines up behind them
+                auto scores = [&](int buf, int t, int s, int h, auto early) {
+                    const uint64_t qd = q_desc + (uint64_t)((t * C::QB + h * 2 * (128 * 128)) >> 4);
                     const uint64_t kd = k_desc + (uint64_t)(s * (C::KB >> 4));
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t b = kd + (uint64_t)(((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4);
-                        if (k == D / 16 - 3) early();
-                        if constexpr (C::QT)
-                            prompt_mma_ts(tmem + C::COL_S + buf * BN, tmem + C::COL_Q + 8 * k, b, id_s, k > 0);
-                        else
-                            prompt_mma_ss(tmem + C::COL_S + buf * BN,
-                                          qd + (uint64_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), b, id_s, k > 0);
+                    for (int k = 0; k < 8; ++k) {
+                        if (k == 8 - 3) early();
+                        prompt_mma_ss(tmem + C::COL_S + buf * BN,
+                                      qd + (uint64_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                      kd + (uint64_t)(((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4), id_s, h > 0 || k > 0);
                     }
-                    tc_commit(sfull + 8 * buf);
+                    if (h == C::EN - 1) tc_commit(sfull + 8 * buf);
                 };
-                auto values = [&](int buf, int t, int s, bool first) {
+                // key half h of a value tile (at d = 256)
+                auto values = [&](int buf, int t, int s, int h, bool first) {
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::KB >> 4));
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < BN / 16; ++k)
-                        prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * k,
-                                      vd + (uint64_t)((k * 2048) >> 4), id_o, !(first && k == 0));
-                    tc_commit(pvdone + 8 * buf);
+                    for (int k = 0; k < C::VN / 16; ++k)
+                        prompt_mma_ts(tmem + C::COL_O + t * D, tmem + C::COL_S + buf * BN + 8 * (h * (C::VN / 16) + k),
+                                      vd + (uint64_t)((k * 2048) >> 4), id_o, !(first && h == 0 && k == 0));
+                    if (h == C::EN - 1) tc_commit(pvdone + 8 * buf);
                 };
                 int q_uses = 0, turns = 0;
                 uint32_t clean = 0;  // parity of each stage's next cleaning
@@ -462,8 +466,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     const int n = w.tiles();
                     if (n == 0) continue;
                     const bool rag = w.ragged<BN>();
-                    auto value_tile = [&](int j) {
-                        const int s = take(C::value_pos(j, n));
+                    auto value_tile = [&](int j, int h) {
+                        const int s = take(C::value_pos(j, n), h);
                         if (rag && j == n - 1) {
                             prompt_wait(vclean + 8 * s, (clean >> s) & 1, dead, err);
                             clean ^= 1u << s;
@@ -483,21 +487,21 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                             if (both) mbar_arrive(turn + 8 * (1 - me));
                         };
                         prompt_wait(qfull, q_uses & 1, dead, err);
-                        int ks = take(C::key_pos(0));
+                        int ks = take(C::key_pos(0), 0);
                         begin();
-                        if (mine > 0) scores(me, me, ks, pass);
+                        if (mine > 0) scores(me, me, ks, 0, pass);
                         else pass();
                         tc_commit(empty + 8 * ks);
                         if (mine <= 1) tc_commit(qfree);
                         for (int j = 0; j < n; ++j) {
-                            const int vs = value_tile(j);
-                            if (j + 1 < n) ks = take(C::key_pos(j + 1));
+                            const int vs = value_tile(j, 0);
+                            if (j + 1 < n) ks = take(C::key_pos(j + 1), 0);
                             begin();
                             if (j < mine) prompt_wait(pready + 8 * me, (use + j) & 1, dead, err);
-                            if (j < mine) values(me, me, vs, j == 0);
+                            if (j < mine) values(me, me, vs, 0, j == 0);
                             // (these scores overwrite the probabilities, whose products this
                             // thread issued before: MMAs of a thread run in order)
-                            if (j + 1 < mine) scores(me, me, ks, pass);
+                            if (j + 1 < mine) scores(me, me, ks, 0, pass);
                             else pass();
                             tc_commit(empty + 8 * vs);
                             if (j + 1 < n) tc_commit(empty + 8 * ks);
@@ -512,17 +516,22 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                             // the buffer's probabilities are used up
                             const int use = (j & 1 ? use1 : use0) + (j >> 1);
                             if (use > 0) prompt_wait(pvdone + 8 * (j & 1), (use - 1) & 1, dead, err);
-                            const int ks = take(C::key_pos(j));
-                            scores(j & 1, 0, ks, [] {});
-                            tc_commit(empty + 8 * ks);
+                            for (int h = 0; h < C::EN; ++h) {
+                                const int ks = take(C::key_pos(j), h);
+                                scores(j & 1, 0, ks, h, [] {});
+                                tc_commit(empty + 8 * ks);
+                            }
                         }
+                        tc_commit(qfree);
                     } else {
                         for (int j = 0; j < n; ++j) {
                             const int use = (j & 1 ? use1 : use0) + (j >> 1);
                             prompt_wait(pready + 8 * (j & 1), use & 1, dead, err);
-                            const int vs = value_tile(j);
-                            values(j & 1, 0, vs, j == 0);
-                            tc_commit(empty + 8 * vs);
+                            for (int h = 0; h < C::EN; ++h) {
+                                const int vs = value_tile(j, h);
+                                values(j & 1, 0, vs, h, j == 0);
+                                tc_commit(empty + 8 * vs);
+                            }
                         }
                     }
                     ++q_uses;
@@ -551,28 +560,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             // key tiles that every row of the tile sees whole
             const int whole = prompt_limit(a, w, min(first, w.lq)) / BN;
             const int64_t row = (int64_t)(w.q0 + tok) * a.q_heads + w.row * a.group + head;
-            if constexpr (C::QT) {
-                // (the last item's scores are done: this thread has seen them)
-                if (nt > 0) {
-                    const uint4* q = reinterpret_cast<const uint4*>(
-                        static_cast<const uint16_t*>(a.q) +
-                        (live ? (int64_t)(w.q0 + tok) * a.q_stride + (int64_t)(w.row * a.group + head) * D : 0));
-#pragma unroll 1
-                    for (int i = 0; i < D / 64; ++i) {
-                        uint32_t x[32];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint4 v = live ? __ldg(q + 8 * i + k) : make_uint4(0u, 0u, 0u, 0u);
-                            x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
-                        }
-                        tmem_st32(tmem + lanes + C::COL_Q + 32 * i, x);
-                    }
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(qfull);
-                }
-            }
             float m = -INFINITY, l = 0.f, mx = -INFINITY;
             for (int j = 0; j < nt; ++j) {
                 const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
@@ -803,7 +790,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 template <class C>
 int prompt_parts(const PromptArgs& a, int64_t items, int sms, int64_t part_rows) {
     const double keys = (double)a.n_k - (a.causal ? 0.5 * std::min(a.n_q, a.n_k) : 0.0);
-    const double tiles = keys / a.batch / C::BN, tile_us = C::D == 128 ? 1.4 : 0.85;
+    const double tiles = keys / a.batch / C::BN, tile_us = 1.7;
     int best = 1;
     double best_us = 0;
     for (int z = 1; z <= kPromptParts; ++z) {
