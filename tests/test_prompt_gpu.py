@@ -179,6 +179,42 @@ def test_neighbours_and_rows_behind_the_last_sequence(d):
         assert (out[180:] == 5).all() and (lse[180:] == 7).all()
 
 
+@pytest.mark.parametrize("d,g,lq,lk", [(128, 1, 300, 300), (128, 4, 150, 150), (128, 8, 40, 700), (256, 2, 200, 200),
+                                       (256, 8, 20, 333)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_values_a_row_does_not_see(d, g, lq, lk, dtype):
+    """Infinities and NaN in keys and values later than a row: no influence; the rows that see them get them."""
+    p, q, k, v, cq, ck = _case(d, g, 2, [lq], [lk], dtype, 18)
+    at = [lk - 1, lk - 3, lk - lq // 2, lk - lq + 2]
+    v[at[0], 0, 5] = float("nan")
+    v[at[1], 1, d - 1] = float("inf")
+    v[at[2], 0, 0] = float("-inf")
+    v[at[2] + 1, 0, 0] = float("inf")  # -inf, then NaN in the rows that see both
+    v[at[3], 1, 77] = float("inf")
+    k[at[1] + 1, 1, 3] = float("nan")  # the last rows of head 1
+    out, lse = _run(p, q, k, v, cq, ck)
+    got = _np(out)
+    kn, vn, qn = _np(k), _np(v), _np(q)
+    limit = np.arange(lq) + 1 + lk - lq
+    clean = np.where(np.isfinite(vn), vn, 0.0)
+    for h in range(2):
+        sl = slice(h * g, (h + 1) * g)
+        hurt = limit > at[1] + 1 if h == 1 else np.zeros(lq, bool)  # rows that see the NaN key
+        ref, _, mag = f8.attention(qn[:, sl], np.nan_to_num(kn[:, h:h + 1]), clean[:, h:h + 1], 1 / np.sqrt(d), limit)
+        tol, _ = _bounds(qn[:, sl], np.nan_to_num(kn[:, h:h + 1]), 1 / np.sqrt(d), mag, ref, q.dtype, lk)
+        want = ref.copy()
+        for key, col in np.argwhere(~np.isfinite(vn[:, h])):
+            with np.errstate(invalid="ignore"):  # -inf + inf
+                want[limit > key, :, col] += vn[key, h, col]
+        want[hurt] = np.nan
+        fin = np.isfinite(want)
+        g_h = got[:, sl]
+        assert np.array_equal(np.isnan(g_h), np.isnan(want)) and np.array_equal(g_h[~fin & ~np.isnan(want)],
+                                                                               want[~fin & ~np.isnan(want)])
+        assert (np.abs(g_h[fin] - want[fin]) <= tol[fin]).all()
+    assert p.device_error() == 0
+
+
 def test_bad_starts_are_reported_and_stay_inside():
     p, q, k, v, cq, ck = _case(128, 2, 1, [40, 50], [40, 50], "bf16", 15)
     for bad_q, bad_k in (([0, 40, 200], [0, 40, 90]), ([0, 60, 40], [0, 40, 90]), ([0, 40, 90], [-5, 40, 90]),

@@ -129,6 +129,8 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
         k_stride = v_stride = q_stride;
     }
     PromptArgs a;
+    a.v = v;
+    a.v_stride = v_stride;
     a.out = out;
     a.lse = lse;
     a.cu_q = cu_q;

@@ -46,6 +46,8 @@
 namespace tq {
 
 struct PromptArgs {
+    const void* v;
+    int64_t v_stride;
     void* out;
     float* lse;
     const int32_t *cu_q, *cu_k;
@@ -87,7 +89,7 @@ struct PromptCfg {
     static constexpr int COL_S = 0, COL_O = 2 * BN;
     static constexpr int off_ring = NQ * QB;
     static constexpr int off_bar = off_ring + STAGES * KB;
-    static constexpr int BAR = 320;
+    static constexpr int BAR = 256;
     static constexpr int total = off_bar + BAR + 1024;  // + alignment to 1024
     static_assert(COL_O + NQ * D <= 512, "tensor memory");
     static_assert(total <= 232448, "shared memory");
@@ -153,6 +155,11 @@ __device__ __forceinline__ uint32_t prompt_pack(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 }
+template <bool BF16>
+__device__ __forceinline__ float2 prompt_values(uint32_t w) {
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 // pairs of fp32 (one instruction for two lanes' worth of work)
 __device__ __forceinline__ uint64_t prompt_pair(float x, float y) {
     uint64_t r;
@@ -185,11 +192,12 @@ struct PromptWork {
     int t0;              // first token of query tile 0
     int row, part;       // KV head, part of the keys
     int j0, n[2];        // first key tile; key tiles of each query tile from there on
+    int seen;            // keys that every row of the item sees; value tiles that reach behind
+                         // them are checked
     __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
-    // the last value tile of the item reaches behind the sequence's last key
     template <int BN>
-    __device__ __forceinline__ bool ragged() const {
-        return tiles() > 0 && lk % BN != 0 && lk / BN == j0 + tiles() - 1;
+    __device__ __forceinline__ bool checked(int j) const {
+        return (j0 + j + 1) * BN > seen;
     }
 };
 
@@ -206,15 +214,16 @@ __device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int64_t i
     const int per = C::NQ * a.tile_tok, sub = a.heads * a.parts;
     PromptWork w;
     w.ok = 0;
-    w.q0 = w.lq = w.k0 = w.lk = w.t0 = w.row = w.part = w.j0 = w.n[0] = w.n[1] = 0;
+    w.q0 = w.lq = w.k0 = w.lk = w.t0 = w.row = w.part = w.j0 = w.n[0] = w.n[1] = w.seen = 0;
+    int have = -1, q0 = 0, q1 = 0, k0 = 0, k1 = 0;  // (up to 32 sequences are read once)
     for (int pass = total < 0 ? 0 : 1; pass < 2; ++pass) {
         int seen = 0;
         const int64_t want = (int64_t)total - 1 - item / sub;
         if (pass == 1 && want < 0) break;
         for (int b0 = 0; b0 < a.batch; b0 += 32) {
             const int b = b0 + lane;
-            int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-            if (b < a.batch) {
+            if (have != b0) q0 = q1 = k0 = k1 = 0;
+            if (have != b0 && b < a.batch) {
                 q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
                 k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
                 if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
@@ -223,6 +232,7 @@ __device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int64_t i
                     k0 = min(max(k0, 0), a.n_k), k1 = min(max(k1, k0), a.n_k);
                 }
             }
+            have = b0;
             const int n = (q1 - q0 + per - 1) / per;
             int incl = n;
 #pragma unroll
@@ -249,6 +259,7 @@ __device__ __forceinline__ PromptWork prompt_find(const PromptArgs& a, int64_t i
         if (pass == 0) total = seen;
     }
     if (w.ok) {
+        w.seen = prompt_limit(a, w, w.t0);
         const int x = (int)(item % sub);
         w.row = x / a.parts;
         w.part = x - w.row * a.parts;
@@ -278,19 +289,20 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::off_bar);
     const uint32_t full = smem_u32(bars), empty = full + 8 * S, qfull = empty + 8 * S, qfree = qfull + 8,
                    sfull = qfree + 8, pready = sfull + 16, pvdone = pready + 16, turn = pvdone + 16, wfull = turn + 16,
-                   wfree = wfull + 16, vclean = wfree + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 3 * S + 14);
-    static_assert((3 * S + 14) * 8 + 4 <= C::BAR, "barriers");
+                   wfree = wfull + 16;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 2 * S + 14);
+    static_assert((2 * S + 14) * 8 + 4 <= C::BAR, "barriers");
     __shared__ PromptWork s_w[2];
+    __shared__ int s_bad[4];  // [it & 3] = it + 1: item it has values that are not finite in its checked rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int W0 = C::SOFT / 32;  // first of the other four warps: copies, MMA
     uint32_t* err = a.err;
 
+    if (tid < 4) s_bad[tid] = 0;
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, NQ);
-            mbar_init(vclean + 8 * s, 1);
         }
         mbar_init(qfull, 1);
         mbar_init(qfree, NQ);
@@ -300,7 +312,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             mbar_init(pvdone + 8 * t, 1);
             mbar_init(turn + 8 * t, 1);
             mbar_init(wfull + 8 * t, 1);
-            mbar_init(wfree + 8 * t, 2 + W0);  // the two issuing threads and the softmax warps
+            mbar_init(wfree + 8 * t, 2 + W0);  // the issuing threads and the softmax warps
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -326,7 +338,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     };
 
     if (warp >= W0) {
-        if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(56));
         if (warp == W0) {
             // ---------------------------------------------------- copies
             int total = -1, loads = 0, q_loads = 0;
@@ -384,21 +396,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 uint32_t next = 0;
                 if (lane == 0) next = atomicAdd(a.next, 1u);
                 dead = __shfl_sync(0xffffffffu, (int)dead, 0) != 0;
-                ring += 2 * C::EN * n;
-                // zero the value rows behind the sequence's last key: 0 * NaN or inf
-                // of a neighbour's row would be NaN.  The item's last copies have them.
-                if (w.ragged<BN>())
-                    for (int h = 0; h < C::EN; ++h) {
-                        const int r = ring - C::EN + h, s = r % S, keep = w.lk % BN - h * C::VN;
-                        prompt_wait(full + 8 * s, (r / S) & 1, dead, err);
-                        uint8_t* v = smem + C::off_ring + s * C::KB;
-                        for (int i = lane; i < C::KB / 16; i += 32)
-                            if ((i >> 3) % C::VN >= keep) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(vclean + 8 * s);
-                    }
-                dead = __any_sync(0xffffffffu, (int)dead);
                 item = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, next, 0);
             }
             if (lane == 0) {
@@ -457,7 +454,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     if (h == C::EN - 1) tc_commit(pvdone + 8 * buf);
                 };
                 int q_uses = 0, turns = 0;
-                uint32_t clean = 0;  // parity of each stage's next cleaning
                 PromptWork w;
                 for (int it = 0;; ++it) {
                     fetch(it, w);
@@ -465,15 +461,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     if (!w.ok) break;
                     const int n = w.tiles();
                     if (n == 0) continue;
-                    const bool rag = w.ragged<BN>();
-                    auto value_tile = [&](int j, int h) {
-                        const int s = take(C::value_pos(j, n), h);
-                        if (rag && j == n - 1) {
-                            prompt_wait(vclean + 8 * s, (clean >> s) & 1, dead, err);
-                            clean ^= 1u << s;
-                        }
-                        return s;
-                    };
+                    auto value_tile = [&](int j, int h) { return take(C::value_pos(j, n), h); };
                     if constexpr (NQ == 2) {
                         // both threads see every ring position and release every stage
                         const int mine = me == 0 ? w.n[0] : w.n[1], use = me == 0 ? use0 : use1;
@@ -541,7 +529,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
     } else {
         // ------------------------------------------------ softmax, output
-        if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(216));
+        if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(224));
         const int t = NQ == 2 ? warp >> 2 : 0;
         const int rt = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -560,10 +548,93 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             // key tiles that every row of the tile sees whole
             const int whole = prompt_limit(a, w, min(first, w.lq)) / BN;
             const int64_t row = (int64_t)(w.q0 + tok) * a.q_heads + w.row * a.group + head;
+            // A probability of zero does not keep a value out of a product: 0 * inf
+            // and 0 * NaN are NaN.  In a value tile with rows that some query row does
+            // not see, the rows behind the sequence's last key (a neighbour's) become
+            // zero, and so do values that are not finite in rows that only some query
+            // rows see; the output adds those to the rows that see them.  Done before
+            // the tile's probabilities are signalled, by the query tile's four warps.
+            // (At d = 128 both query tiles do it; what one has zeroed the other finds
+            // zero, and the flag set before.)
+            auto check = [&](int j) {
+                const uint32_t em = C::BF16 ? 0x7F807F80u : 0x7C007C00u, e1 = C::BF16 ? 0x00800080u : 0x04000400u;
+                if (NQ == 1 && j > 0) {
+                    // (orders the ring's earlier phases before the wait below)
+                    const int pb = (j - 1) & 1;
+                    prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
+                }
+                bool wrote = false;
+#pragma unroll 1
+                for (int h = 0; h < C::EN; ++h) {
+                    const int r = ring + C::EN * C::value_pos(j, w.tiles()) + h, key0 = (w.j0 + j) * BN + h * C::VN;
+                    prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
+                    uint8_t* v = smem + C::off_ring + (r % S) * C::KB;
+                    // rows [r0, r1) to check, [r1, VN) to zero, in CH columns of 128
+                    // bytes; 8 lanes a row, 16 rows at a time
+                    const int r1 = max(0, min(C::VN, w.lk - key0)), r0 = min(r1, max(0, w.seen - key0));
+                    auto at = [&](int c, int rr) { return reinterpret_cast<uint4*>(v + (c * C::VN + rr) * 128 + (rt & 7) * 16); };
+                    auto inf = [&](uint32_t y) { return (y & em) + e1; };  // bits 15, 31: not finite
+                    uint32_t any = 0;
+#pragma unroll 1
+                    for (int rr = r0 + (rt >> 3); rr < r1; rr += 64) {
+                        uint4 x[4][2];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                x[u][c] = rr + 16 * u < r1 ? *at(c, rr + 16 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) any |= inf(x[u][c].x) | inf(x[u][c].y) | inf(x[u][c].z) | inf(x[u][c].w);
+                        if constexpr (CH > 2) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    x[u][c] = rr + 16 * u < r1 ? *at(c + 2, rr + 16 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    any |= inf(x[u][c].x) | inf(x[u][c].y) | inf(x[u][c].z) | inf(x[u][c].w);
+                        }
+                    }
+                    if (any & 0x80008000u) {
+                        s_bad[it & 3] = it + 1;
+                        __threadfence_block();
+                        wrote = true;
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c)
+#pragma unroll 1
+                            for (int rr = r0 + (rt >> 3); rr < r1; rr += 16) {
+                                auto fix = [&](uint32_t y) {
+                                    const uint32_t f = inf(y);
+                                    return y & ~((f & 0x8000u ? 0xFFFFu : 0u) | (f & 0x80000000u ? 0xFFFF0000u : 0u));
+                                };
+                                const uint4 x = *at(c, rr);
+                                *at(c, rr) = make_uint4(fix(x.x), fix(x.y), fix(x.z), fix(x.w));
+                            }
+                    }
+                    if (r1 < C::VN) {
+                        wrote = true;
+#pragma unroll 1
+                        for (int c = 0; c < CH; ++c)
+#pragma unroll 1
+                            for (int rr = r1 + (rt >> 3); rr < C::VN; rr += 16) *at(c, rr) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                // (the other query tile's warps may have written what this one reads)
+                __threadfence_block();
+                if (wrote || s_bad[it & 3] == it + 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            };
             float m = -INFINITY, l = 0.f, mx = -INFINITY;
             for (int j = 0; j < nt; ++j) {
                 const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
                 const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
+                // (while the scores are under way; at d = 256 the wait for the values
+                // needs the scores before it)
+                if (NQ == 2 && w.checked<BN>(j)) check(j);
                 prompt_wait(sfull + 8 * buf, use & 1, dead, err);
                 tc_fence_after();
                 uint32_t s[BN / 32][32];
@@ -662,6 +733,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     again = __any_sync(0xffffffffu, (mx - m) * c > C::AHEAD_LOG2);
                 } while (again);
                 l += lj;
+                if (NQ == 1 && w.checked<BN>(j)) check(j);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -671,6 +743,31 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 const int buf = NQ == 2 ? t : (nt - 1) & 1, use = (buf ? use1 : use0) + (NQ == 2 ? nt - 1 : (nt - 1) >> 1);
                 prompt_wait(pvdone + 8 * buf, use & 1, dead, err);
                 tc_fence_after();
+            }
+            if (nt > 0 && s_bad[it & 3] == it + 1) {
+                // the values that were left out of the products, to the rows that see
+                // them (into the sums in tensor memory; rare, so it may take its time)
+                const int last = min(lim, (w.j0 + nt) * BN);
+#pragma unroll 1
+                for (int i = 0; i < D; i += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(so + i, o);
+                    tc_wait_ld();
+#pragma unroll 1
+                    for (int key = max(w.seen, w.j0 * BN); key < last; ++key) {
+                        const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                            static_cast<const uint16_t*>(a.v) + (int64_t)(w.k0 + key) * a.v_stride + w.row * D + i);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 x = prompt_values<C::BF16>(__ldg(v + k));
+                            if (!isfinite(x.x)) o[2 * k] = __float_as_uint(__uint_as_float(o[2 * k]) + x.x);
+                            if (!isfinite(x.y)) o[2 * k + 1] = __float_as_uint(__uint_as_float(o[2 * k + 1]) + x.y);
+                        }
+                    }
+                    __syncwarp();
+                    tmem_st16(so + i, o);
+                }
+                tc_wait_st();
             }
             if (a.parts > 1) {
                 const int64_t at = (int64_t)w.part * a.n_q * a.q_heads + row;
