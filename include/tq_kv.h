@@ -421,7 +421,7 @@ typedef struct tq_f8_config {
     int32_t num_kv_heads;       /* H_kv >= 1 */
     int32_t num_q_heads;        /* H_q = G * H_kv, any G >= 1; q head h reads KV head h / G */
     int32_t block_size;         /* tokens per cache block; must be 16 */
-    int64_t num_blocks;         /* blocks in the cache pool */
+    int64_t num_blocks;         /* blocks in the cache pool; num_blocks * H_kv < 2^31 */
     int32_t max_batch;          /* sequences per load or decode call */
     int32_t max_blocks_per_seq; /* columns of the block table;
                                    max_batch * max_blocks_per_seq * H_kv * ceil(G / 16) < 2^31 */

@@ -14,8 +14,11 @@
 // its segments (the pages of one (sequence, KV head) each) step by step and add
 // up in shared memory at a segment's end; or, with many short sequences, one run
 // per warp, and no warp waits for another.  A step is 256/d pages.  Each warp
-// keeps a ring of steps in flight with cp.async, across segments; the copies put
-// the rows where the tensor-core operands read them without bank conflicts.  Products per 16 tokens:
+// keeps a ring of steps in flight, across segments: one tensor copy per page,
+// whose 128-byte swizzle lays the rows out so that the operand reads below meet no
+// bank conflict, and one small copy of its scales.  (16-byte cp.async in a swizzle
+// of our own moved as much, but issuing it took a warp 1255 cycles of the 4240 of
+// a step.)  Products per 16 tokens:
 //   S^T[tokens x heads] = K Q^T     mma.m16n8k16, A = codes as fp16 (exact)
 //   O^T[d x heads] += V^T P^T       A = pairs of value codes, B = the weights
 // so a KV head's query heads (8 or 16 columns) share every page, and tokens and
@@ -30,6 +33,7 @@
 #include <algorithm>
 
 #include "tq_f8.cuh"
+#include "tq_tma.h"
 
 namespace tq {
 
@@ -80,27 +84,39 @@ __device__ __forceinline__ uint32_t f8_pack_rest(float x, float y, uint32_t hi) 
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     return f8_pack_f16(x - f.x, y - f.y);
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// a page's 32 code rows: box {128 bytes, 32 rows, d/128 halves, 1 page}
+__device__ __forceinline__ void f8_page_copy(uint32_t dst, const CUtensorMap* m, int page, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(0), "r"(page), "r"(bar)
+        : "memory");
 }
+// Token of row g (and, 8 further, of row g + 8) of the score product.  The swizzle
+// puts 16-byte chunk x of row t at x ^ (t & 7); with this order the rows a quarter
+// warp reads together differ in bit 2 (keys: rows 2i, 2i + 1, chunks c) and in
+// bits 1..2 (values: rows 2c, chunks g), so that its 8 lanes hit 8 chunk places.
+__device__ __forceinline__ int f8_token(int g) { return (g & 6) ^ ((g & 1) ? 5 : 0); }
 
 template <int D, int NT, bool PREC>
 struct F8Cfg {
     static constexpr int PP = 256 / D;                 // pages per step
-    static constexpr int PAGE = f8_page_bytes(D);
-    static constexpr int STEP = PP * PAGE;             // bytes of a ring stage
+    static constexpr int CODES = 32 * D;               // bytes of a page's codes in the ring
+    static constexpr int STEP = PP * CODES;            // bytes of a ring stage
     static constexpr int HEADS = 8 * NT;
     static constexpr int QF = (D / 16) * NT * 32 * 8 * (PREC ? 2 : 1);  // query operands of a warp
-    // blocks per SM (three where two pages per warp and the registers allow it, else two), and as
-    // deep a ring as fits then, of at most four stages
-    static constexpr int per_cta(int n) { return 233472 / n - 1024 - 1280; }
-    static constexpr int fit(int n) { return (per_cta(n) / kF8Warps - QF - 64) / STEP; }
+    // blocks per SM (three where two stages per warp and the registers allow it,
+    // else two), and as deep a ring as fits then
+    static constexpr int EXTRA = PP * (32 + 4) + 8;    // scales, valid tokens and barrier of a stage
+    static constexpr int per_cta(int n) { return 233472 / n - 1024 - 1280 - 1024; }
+    static constexpr int fit(int n) { return (per_cta(n) / kF8Warps - QF) / (STEP + EXTRA); }
     static constexpr int CTAS = fit(3) >= 2 && NT == 1 && D == 128 ? 3 : fit(2) >= 2 ? 2 : 1;
     static constexpr int STAGES = fit(CTAS) < 6 ? fit(CTAS) : 6;
     static_assert(STAGES >= 2, "ring");
     static constexpr int off_q = kF8Warps * STAGES * STEP;
-    static constexpr int off_info = off_q + kF8Warps * QF;         // [warps][STAGES][PP] valid tokens
-    static constexpr int total = off_info + kF8Warps * STAGES * PP * 4;
+    static constexpr int off_ex = off_q + kF8Warps * QF;                   // [warps][STAGES][PP][32]
+    static constexpr int off_bar = off_ex + kF8Warps * STAGES * PP * 32;   // [warps][STAGES]
+    static constexpr int off_info = off_bar + kF8Warps * STAGES * 8;       // [warps][STAGES][PP] valid tokens
+    static constexpr int total = off_info + kF8Warps * STAGES * PP * 4 + 1024;  // + alignment to 1024
     static constexpr int ITEMS = D / 16 * NT * 32;     // float4 per partial sum
     // two sums fit the four warps' query operands, whose place they take at a segment's end
     static_assert(2 * ITEMS * 16 <= kF8Warps * QF, "merge buffers");
@@ -159,11 +175,12 @@ struct F8JoinSmem {
 static_assert(kF8MaxSms * kF8Ctas / kF8Join + 1 <= 32, "groups of a join");
 
 template <int D, int NT, bool PREC>
-__global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decode_kernel(F8DecodeArgs a) {
+__global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decode_kernel(const __grid_constant__ F8DecodeArgs a, const __grid_constant__ CUtensorMap pages) {
     using C = F8Cfg<D, NT, PREC>;
     constexpr int S = C::STAGES, PP = C::PP, W = kF8Warps, HEADS = C::HEADS;
     static_assert(sizeof(F8JoinSmem) <= C::total, "the join reuses the rings");
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     __shared__ int s_last;
     __shared__ float4 s_ref[W][HEADS];
     __shared__ F8Seg s_part[W][2];  // segments whose sums are in the workspace (b < 0: none)
@@ -171,7 +188,16 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     const int nj = a.heads * a.nhg;
     uint8_t* ring = smem + warp * (S * C::STEP);
     uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q + warp * C::QF);
+    const uint8_t* exps = smem + C::off_ex + warp * S * PP * 32;
+    const uint32_t bars = smem_u32(smem + C::off_bar) + warp * S * 8;
     int* info = reinterpret_cast<int*>(smem + C::off_info) + warp * S * PP;
+    const int tok = f8_token(g);
+    bool dead = false;
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
 
     if (lane < 2) s_part[warp][lane].b = -1;
     pdl_wait();
@@ -248,6 +274,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         // ---- producer: this warp's steps, segment after segment
         F8Seg ps = f8_next(a, prod, nj);
         int pst = sw;
+        int made = 0, used = 0;  // steps copied, steps taken
         int ids = -1, ids_at = 0, ids_n = 0;  // block ids of ids_n pages: this warp's steps from ids_at on
         auto produce = [&](int stage) {
             while (ps.p0 + pst * PP >= ps.p1) {
@@ -267,36 +294,25 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 }
             }
             const int h = a.nhg == 1 ? ps.j : ps.j / a.nhg;
-#pragma unroll
-            for (int pp = 0; pp < PP; ++pp) {
-                const int blk = __shfl_sync(0xffffffffu, ids, ids_at + pp);
-                const int p = ps.p0 + pst * PP + pp;
-                // (a page behind the segment's last has block id -1 too)
-                if (lane == 0) info[stage * PP + pp] = blk < 0 ? 0 : min(16, ps.len - 16 * p);
-                if (blk < 0) continue;
-                const uint8_t* src = a.cache + ((int64_t)blk * a.heads + h) * C::PAGE;
-                const uint32_t dst = smem_u32(ring + stage * C::STEP + pp * C::PAGE);
-                // 32 rows (16 keys, 16 values) of CPR 16-byte chunks; chunk ch of
-                // row r goes to ch ^ 4 (r & 1) for keys and ch ^ (r & 6) for values,
-                // which the operand reads below hit without bank conflicts
-                constexpr int CPR = D / 16, RPI = 32 / CPR;  // rows per warp-wide copy
-                const int r0 = lane / CPR, ch = lane % CPR;
-#pragma unroll
-                for (int i = 0; i < CPR; ++i) {
-                    const int x = i < CPR / 2 ? (r0 & 1) << 2 : (r0 & 6 & (RPI - 1)) ^ (RPI * i & 6);
-                    cp_async16(dst + r0 * D + ((ch ^ x) << 4) + 512 * i, src + 16 * lane + 512 * i);
-                }
-                if (lane < 2) cp_async16(dst + 32 * D + 16 * lane, src + 32 * D + 16 * lane);
+            // lane pp: page pp of the step (one behind the segment's last has block id -1 too)
+            const int blk = __shfl_sync(0xffffffffu, ids, ids_at + (lane < PP ? lane : 0));
+            const bool there = lane < PP && blk >= 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+            if (lane == 0) mbar_expect_tx(bars + 8 * stage, n * f8_page_bytes(D));
+            if (lane < PP) info[stage * PP + lane] = there ? min(16, ps.len - 16 * (ps.p0 + pst * PP + lane)) : 0;
+            __syncwarp();
+            if (there) {
+                const int page = blk * a.heads + h;
+                f8_page_copy(smem_u32(ring) + stage * C::STEP + lane * C::CODES, &pages, page, bars + 8 * stage);
+                bulk_copy(smem_u32(exps) + (stage * PP + lane) * 32, a.cache + (int64_t)page * f8_page_bytes(D) + C::CODES, 32,
+                          bars + 8 * stage);
             }
             pst += sn;
             ids_at += PP;
+            ++made;
         };
-        auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s) {
-            produce(s);
-            commit();
-        }
+        for (int s = 0; s < S - 1; ++s) produce(s);
         int stage = 0;
 
         while (cons.left > 0) {
@@ -390,10 +406,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 for (int e = 0; e < 2; ++e) r[n][e] = rv[n][e] = kF8None, l[n][e] = 0.f;
 
             for (int p = sg.p0 + sw * PP; p < sg.p1; p += sn * PP) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-                __syncwarp();  // the step has landed for every lane; the last step's stage (and qf) is settled
-                produce(stage == 0 ? S - 1 : stage - 1);
-                commit();
+                __syncwarp();  // the last step's stage (and qf) is settled
+                if (!dead) produce(stage == 0 ? S - 1 : stage - 1);
+                if (!dead) dead = !mbar_wait(bars + 8 * stage, (used / S) & 1, a.err);
+                dead = __any_sync(0xffffffffu, dead);
+                ++used;
                 const uint8_t* sp = ring + stage * C::STEP;
                 // ---- scores
                 float s[PP][NT][4];
@@ -408,8 +425,8 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                     for (int pp = 0; pp < PP; ++pp)
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
-                            ka[pp][u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + (g + 8 * u) * D +
-                                                                        (((4 * h + c) ^ ((g & 1) << 2)) << 4));
+                            ka[pp][u] = *reinterpret_cast<const uint4*>(
+                                sp + pp * C::CODES + (h >> 1) * 4096 + (tok + 8 * u) * 128 + (((4 * (h & 1) + c) ^ tok) << 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -439,12 +456,12 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 for (int pp = 0; pp < PP; ++pp) {
                     nv[pp] = info[stage * PP + pp];
                     full &= nv[pp] == 16;
-                    const uint8_t* ex = sp + pp * C::PAGE + 32 * D;
+                    const uint8_t* ex = exps + (stage * PP + pp) * 32;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         // a vector stored as NaN has zero codes and E = 255: 0 * inf here
-                        ck[pp][u] = __uint_as_float((uint32_t)ex[g + 8 * u] << 23);
-                        const uint32_t eb = ex[16 + g + 8 * u];
+                        ck[pp][u] = __uint_as_float((uint32_t)ex[tok + 8 * u] << 23);
+                        const uint32_t eb = ex[16 + tok + 8 * u];
                         ev[pp][u] = eb == 255u ? __uint_as_float(0x7FC00000u)
                                                : __uint_as_float(0x4B000000u | eb) - (8388608.f + 127.f);
                     }
@@ -469,7 +486,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    if (g + 8 * (i >> 1) >= nv[pp]) pw[pp][n][i] = w[pp][n][i] = 0.f;
+                                    if (tok + 8 * (i >> 1) >= nv[pp]) pw[pp][n][i] = w[pp][n][i] = 0.f;
                     }
                 };
                 weights();
@@ -490,7 +507,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             for (int pp = 0; pp < PP; ++pp)
 #pragma unroll
                                 for (int u = 0; u < 2; ++u)
-                                    if (g + 8 * u < nv[pp]) {
+                                    if (tok + 8 * u < nv[pp]) {
                                         const float x = s[pp][n][2 * u + e] * (ck[pp][u] * cqr[n][e]);
                                         m = fmaxf(m, x);
                                         mv = fmaxf(mv, x + ev[pp][u]);
@@ -525,16 +542,17 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                                                    f8_transpose(f8_pack_rest(x[2], x[3], h1)));
                     }
 
-                // ---- values: token pairs (2c, 2c + 1) and (2c + 8, 2c + 9) of 16 coordinates
+                // ---- values: the token pairs of rows (2c, 2c + 1) and (2c + 8, 2c + 9), 16 coordinates
                 if (!full) {
                     // rows behind the last token may hold anything, NaN codes too
 #pragma unroll 1
-                    for (int idx = lane; idx < PP * 16 * (D / 16); idx += 32) {
-                        const int pp = idx / D, t = idx / (D / 16) % 16;
+                    for (int idx = lane; idx < PP * D; idx += 32) {
+                        const int pp = idx / D, x = idx % D, t = x / 8 % 16;  // 16-byte piece x of the page's value rows
                         if (t >= info[stage * PP + pp])
-                            *reinterpret_cast<uint4*>(ring + stage * C::STEP + pp * C::PAGE + 16 * D + (idx % D) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(ring + stage * C::STEP + pp * C::CODES + (x / 128) * 4096 + 2048 +
+                                                      (x % 128) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
                     __syncwarp();
                 }
 #pragma unroll
@@ -545,9 +563,9 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                         uint4 v[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const int t = 2 * c + (u & 1) + 8 * (u >> 1);
-                            v[u] = *reinterpret_cast<const uint4*>(sp + pp * C::PAGE + 16 * D + t * D +
-                                                                   (((8 * h + g) ^ (t & 6)) << 4));
+                            const int t = f8_token(2 * c + (u & 1));
+                            v[u] = *reinterpret_cast<const uint4*>(sp + pp * C::CODES + h * 4096 + 2048 +
+                                                                   (t + 8 * (u >> 1)) * 128 + ((g ^ t) << 4));
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -680,7 +698,10 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             }
             __syncwarp();  // qf is free
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        // after a wait that gave up: copies still in flight land before the ring is reused
+        if (dead)
+            for (bool d2 = false; used < made; ++used)
+                if (!d2) d2 = !mbar_wait(bars + 8 * (used % S), (used / S) & 1, a.err);
     }
 
     // ---- joins
@@ -799,6 +820,25 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     }
 }
 
+// the code rows of the cache: {128 bytes, 32 rows, d/128 halves of a row, pages}
+static tq_status f8_page_map(CUtensorMap* m, const void* cache, int d, int64_t pages) {
+    char why[200] = "";
+    auto enc = tensor_map_encoder(why, sizeof why);
+    if (!enc) return driver_failure("%s", why);
+    const tq_status bs = bind_device_context();
+    if (bs != TQ_OK) return bs;
+    const cuuint64_t dims[4] = {128, 32, (cuuint64_t)(d / 128), (cuuint64_t)pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)d, 128, (cuuint64_t)f8_page_bytes(d)};
+    const cuuint32_t box[4] = {128, 32, (cuuint32_t)(d / 128), 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return driver_failure("cuTensorMapEncodeTiled failed (CUresult %d) for %lld pages at %p", (int)r,
+                              (long long)pages, cache);
+    return TQ_OK;
+}
+
 template <int D, int NT, bool PREC>
 static tq_status launch_f8_decode(const F8DecodeArgs& a, cudaStream_t s) {
     using C = F8Cfg<D, NT, PREC>;
@@ -809,9 +849,12 @@ static tq_status launch_f8_decode(const F8DecodeArgs& a, cudaStream_t s) {
     if (st != TQ_OK) return st;
     // one wave of resident blocks
     const int grid = C::CTAS * std::min(sms, kF8MaxSms);
+    CUtensorMap pages;
+    st = f8_page_map(&pages, a.cache, D, a.num_blocks * a.heads);
+    if (st != TQ_OK) return st;
     // launched programmatically: the launch overlaps the previous kernel's end,
     // and the kernel waits for it before its first read
-    return cuda_status(launch_pdl(true, f8_decode_kernel<D, NT, PREC>, dim3(grid), dim3(kF8Threads), C::total, s, a));
+    return cuda_status(launch_pdl(true, f8_decode_kernel<D, NT, PREC>, dim3(grid), dim3(kF8Threads), C::total, s, a, pages));
 }
 
 template <int D>
