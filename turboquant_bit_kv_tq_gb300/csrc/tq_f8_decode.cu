@@ -9,11 +9,11 @@
 // own, so no weight over- or underflows whatever the scales are.
 //
 // Bound by memory (2 d + 2 bytes per token and KV head).  All pages of all
-// sequences, in the order (sequence, KV head, page), are dealt out evenly in
-// runs to a fixed grid of resident blocks: one run per block, whose warps share
-// its segments (the pages of one (sequence, KV head) each) step by step and add
-// up in shared memory at a segment's end; or, with many short sequences, one run
-// per warp, and no warp waits for another.  A step is 256/d pages.  Each warp
+// sequences, in the order (sequence, KV head, page), are dealt out in runs to a
+// fixed grid of resident blocks: evenly, one run per block, whose warps share its
+// segments (the pages of one (sequence, KV head) each) step by step and add up in
+// shared memory at a segment's end; or, with many short sequences, whole (sequence,
+// KV head)s to warps, and no warp waits for another.  A step is 256/d pages.  Each warp
 // keeps a ring of steps in flight, across segments: one tensor copy per page,
 // whose 128-byte swizzle lays the rows out so that the operand reads below meet no
 // bank conflict, and one small copy of its scales.  (16-byte cp.async in a swizzle
@@ -26,9 +26,8 @@
 // would want 128 rows of operands in shared memory, written back after the
 // conversion; mma.sync takes the converted codes from registers.)
 // A segment that is a whole (sequence, KV head) is written out at once.  The
-// sums of the others go to the workspace and are joined in run order: those of
-// one block when its warps are through, then those of 16 blocks by the last of
-// them to arrive, then the groups' by the last group.
+// sums of the others go to the workspace and are joined in run order: those of 16
+// blocks by the last of them to arrive, then the groups' by the last group.
 
 #include <algorithm>
 
@@ -166,7 +165,7 @@ struct F8Runs {
 // 2^(r' - r) / l of a head's sums; no token: 0
 __device__ __forceinline__ float f8_norm(float R, float Rv, float L) { return L == 0.f ? 0.f : exp2f(Rv - R) / L; }
 
-constexpr int kF8SoloPages = 32;  // pages per unit on average below which warps go alone
+constexpr int kF8SoloPages = 16;  // a warp takes units of up to this many pages alone, whatever its share
 constexpr int kF8Join = 16;  // blocks a group joins; at most kF8MaxSms * kF8Ctas / kF8Join + 1 groups
 struct F8JoinSmem {
     float fac[32][16];
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     __shared__ int s_last;
     __shared__ float4 s_ref[W][HEADS];
-    __shared__ F8Seg s_part[W][2];  // segments whose sums are in the workspace (b < 0: none)
+    __shared__ F8Seg s_part[2];  // segments whose sums are in the workspace (b < 0: none)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int nj = a.heads * a.nhg;
     uint8_t* ring = smem + warp * (S * C::STEP);
@@ -199,12 +198,12 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     }
     __syncwarp();
 
-    if (lane < 2) s_part[warp][lane].b = -1;
+    if (tid < 2) s_part[tid].b = -1;  // (warp 0 alone writes them, and all read after a barrier)
     pdl_wait();
     // ---- totals: lane i of every warp counts the sequences [i per, (i + 1) per)
     const int per = (a.batch + 31) >> 5;
     const int bt0 = min(a.batch, lane * per), bt1 = min(a.batch, bt0 + per);
-    int mine = 0, some = 0;
+    int mine = 0, some = 0, most = 0;
 #pragma unroll 4
     for (int b = bt0; b < bt1; ++b) {
         const int len = __ldg(a.lens + b);
@@ -212,6 +211,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         const int np = f8_pages(a, len);
         mine += np;
         some += np > 0;
+        most = max(most, np);
     }
     int incl = mine;
 #pragma unroll
@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     const int before = (incl - mine) * nj;
     const int total = __shfl_sync(0xffffffffu, incl, 31) * nj;
     const int units = (int)__reduce_add_sync(0xffffffffu, (unsigned)some) * nj;
+    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
     // sequences without a token: their rows are zero
     if (units < a.batch * nj)
         for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -231,44 +232,55 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         }
     if (total == 0) return;
     // One run per block, of at least 16 pages on average (two steps for each
-    // warp), or, with more units than blocks and those short, one per warp, of at
-    // least 8 pages.
-    const bool solo = units > (int)gridDim.x && (long long)total < (long long)kF8SoloPages * units;
-    const int rpb = solo ? W : 1;  // runs per block
+    // warp); or, with more units than blocks and none much longer than a warp's
+    // share, a run of whole units per warp.
+    const int warps = (int)gridDim.x * W;
+    const bool solo = units > (int)gridDim.x && most <= max(kF8SoloPages, 2 * (total / warps));
     F8Runs runs;
-    {
-        const int per_run = solo ? 8 : 16;
-        const long long want = (long long)units * max(1, total / units / per_run);
-        runs.n = (uint32_t)min((long long)gridDim.x * rpb, want);
-        runs.q = (uint32_t)total / runs.n;
-        runs.r = (uint32_t)total - runs.q * runs.n;
-    }
-    const uint32_t run0 = blockIdx.x * rpb, run = solo ? run0 + warp : run0;
-    if (run0 >= runs.n) return;
+    runs.n = solo ? (uint32_t)min(warps, total)
+                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, total / units / 16));
+    runs.q = (uint32_t)total / runs.n;
+    runs.r = (uint32_t)total - runs.q * runs.n;
+    const uint32_t run = solo ? blockIdx.x * W + warp : blockIdx.x;
 
     if (run < runs.n) {
-        const int u0 = (int)runs.start(run), u1 = (int)runs.start(run + 1);
         const int sw = solo ? 0 : warp, sn = solo ? 1 : W;  // this warp takes the steps sw, sw + sn, ... of a segment
-        F8Walk cons;
-        {
-            // the sequence u0 lies in: one lane has it among its own
+        // page u of the order: one lane has its sequence among its own
+        auto locate = [&](int u) {
             int at = before, b = bt0, len = 0;
-            const bool here = u0 >= before && u0 < before + mine * nj;
+            const bool here = u >= before && u < before + mine * nj;
             if (here)
                 for (;; ++b) {
                     len = __ldg(a.lens + b);
                     const int n = f8_pages(a, len) * nj;
-                    if (u0 < at + n) break;
+                    if (u < at + n) break;
                     at += n;
                 }
             const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-            cons.b = __shfl_sync(0xffffffffu, b, src);
-            cons.len = f8_clamp(a, __shfl_sync(0xffffffffu, len, src));
-            const int rel = u0 - __shfl_sync(0xffffffffu, at, src), np = (cons.len + 15) >> 4;
-            cons.j = rel / np;
-            cons.p = rel - cons.j * np;
+            F8Walk w;
+            w.b = __shfl_sync(0xffffffffu, b, src);
+            w.len = f8_clamp(a, __shfl_sync(0xffffffffu, len, src));
+            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = (w.len + 15) >> 4;
+            w.j = rel / np;
+            w.p = rel - w.j * np;
+            w.left = total - u;
+            return w;
+        };
+        int u0 = (int)runs.start(run), u1 = (int)runs.start(run + 1);
+        F8Walk cons = locate(u0);
+        if (solo) {
+            // the units that start in [u0, u1)
+            if (u1 < total) {
+                const F8Walk w = locate(u1);
+                if (w.p > 0) u1 += ((w.len + 15) >> 4) - w.p;
+            }
+            if (cons.p > 0) {
+                u0 += ((cons.len + 15) >> 4) - cons.p;
+                f8_next(a, cons, nj);
+            }
         }
         cons.left = u1 - u0;
+        if (cons.left <= 0) return;  // (solo: no unit starts here)
         F8Walk prod = cons;
 
         // ---- producer: this warp's steps, segment after segment
@@ -694,7 +706,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             a.meta[slot * HEADS + 8 * n + 2 * c + e] = make_float4(r[n][e], rv[n][e], l[n][e], 0.f);
-                if (lane == 0) s_part[warp][which] = sg;
+                if (lane == 0) s_part[which] = sg;
             }
             __syncwarp();  // qf is free
         }
@@ -704,9 +716,10 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 if (!d2) d2 = !mbar_wait(bars + 8 * (used % S), (used / S) & 1, a.err);
     }
 
+    if (solo) return;
+
     // ---- joins
-    __threadfence();
-    __syncthreads();  // the rings are free, the block's partial sums visible
+    __syncthreads();  // the rings are free, the block's sums written
     F8JoinSmem& js = *reinterpret_cast<F8JoinSmem*>(smem);
     // the sums of `count` <= 32 slots (s0, then s1 + st, s1 + 2 st, ...) into slot s0, or out
     auto join = [&](int count, int s0, int s1, int st, bool fin, const F8Seg& sg) {
@@ -751,71 +764,37 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                               a.out_dtype);
             }
         }
-        if (!fin) {
-            if (tid < HEADS) a.meta[s0 * HEADS + tid] = js.tot[tid];
-            __threadfence();
-        }
+        if (!fin && tid < HEADS) a.meta[s0 * HEADS + tid] = js.tot[tid];
         __syncthreads();
     };
     // one more of `all` has arrived at *cnt: is it the last?  (leaves the counter ready for the next call)
     auto arrive = [&](uint32_t* cnt, int all) {
         if (tid == 0) {
+            __threadfence();  // after a barrier: the block's writes
             s_last = atomicAdd(cnt, 1u) == (uint32_t)(all - 1);
             if (s_last) *cnt = 0;
+            __threadfence();
         }
         __syncthreads();
-        const bool last = s_last != 0;
-        __threadfence();
-        __syncthreads();
-        return last;
+        return s_last != 0;
     };
-    for (int x = 0; x < 2 * W;) {
-        const F8Seg sg = s_part[x >> 1][x & 1];
-        if (sg.b < 0) {
-            ++x;
-            continue;
-        }
-        // the segments of this unit in this block (x0, and the first ones of the next warps)
-        const int x0 = x;
-        int count = 1, p1 = sg.p1;
-        for (++x; x < 2 * W; ++x) {
-            const F8Seg& nx = s_part[x >> 1][x & 1];
-            if (nx.b < 0) continue;
-            if (nx.b != sg.b || nx.j != sg.j) break;
-            p1 = nx.p1;
-            ++count;
-        }
-        // the blocks of this unit, from the one that holds its first page on
-        const int w0 = x0 >> 1;
-        const uint32_t i = run0 + w0;
-        const int v0 = (x0 & 1) ? (int)runs.start(i + 1) - sg.p1 : (int)runs.start(i) - sg.p0, v1 = v0 + sg.np();
-        const int i0 = (int)runs.owner(v0), i1 = (int)runs.owner(v1 - 1);
-        const int c0 = i0 / rpb, c1 = i1 / rpb, n = c1 - c0 + 1, st = 2 * rpb;  // st: slots of a block
-        const int first = 2 * i0 + ((int)runs.start(i0) >= v0 ? 0 : 1);         // slot of block c0
-        const int gi = ((int)blockIdx.x - c0) / kF8Join, g0 = c0 + gi * kF8Join;
-        // this block's sums, then those of its group of blocks (where there are
-        // more than one group), then those of all blocks or groups
-        int jn = count, j0 = 2 * (int)run0 + x0, j1 = 2 * (int)(run0 + w0), jst = 2;
-        bool fin = sg.p0 == 0 && p1 == sg.np();
-        for (bool grouped = n <= kF8Join;; grouped = true) {
-            if (jn > 1 || fin) join(jn, j0, j1, jst, fin, sg);
-            if (fin) break;
-            uint32_t* cnt;
-            if (!grouped) {
-                jn = min(kF8Join, c1 - g0 + 1);
-                j0 = gi == 0 ? first : st * g0;
-                j1 = st * g0;
-                jst = st;
-                cnt = a.gcnt + j0;
-            } else {
-                fin = true;
-                jn = n <= kF8Join ? n : (n + kF8Join - 1) / kF8Join;
-                j0 = first;
-                j1 = st * c0;
-                jst = n <= kF8Join ? st : st * kF8Join;
-                cnt = a.cnt + (int64_t)sg.b * nj + sg.j;
-            }
+    for (int x = 0; x < 2; ++x) {
+        const F8Seg sg = s_part[x];
+        if (sg.b < 0) continue;
+        // the runs (= blocks) of this unit, from the one that holds its first page on
+        const int v0 = (int)(x ? runs.start(run + 1) - sg.p1 : runs.start(run) - sg.p0);
+        const int c0 = (int)runs.owner(v0), c1 = (int)runs.owner(v0 + sg.np() - 1), n = c1 - c0 + 1;
+        const int first = 2 * c0 + ((int)runs.start(c0) >= v0 ? 0 : 1);  // slot of block c0; the others': 2 c
+        const int gi = ((int)run - c0) / kF8Join, g0 = c0 + gi * kF8Join;
+        // those of its group of blocks (where there are more than one group), then
+        // those of all blocks or groups
+        for (bool fin = n <= kF8Join;; fin = true) {
+            const int jn = !fin ? min(kF8Join, c1 - g0 + 1) : n <= kF8Join ? n : (n + kF8Join - 1) / kF8Join;
+            const int j0 = fin || gi == 0 ? first : 2 * g0, j1 = fin ? 2 * c0 : 2 * g0;
+            uint32_t* cnt = fin ? a.cnt + (int64_t)sg.b * nj + sg.j : a.gcnt + j0;
             if (!arrive(cnt, jn)) break;
+            if (jn > 1) join(jn, j0, j1, fin && n > kF8Join ? 2 * kF8Join : 2, fin, sg);
+            if (fin) break;
         }
     }
 }
