@@ -10,10 +10,13 @@ namespace tq {
 // ------------------------------------------------------------------- store
 // One vector per group of d/8 lanes, 8 elements per lane.  Maximum over the
 // lanes, exact scaling by a power of two, one conversion to e4m3.  Bound by
-// memory: 2 (or 4) bytes in and 1 out per element.
+// memory: 2 (or 4) bytes in and 1 out per element.  A block takes consecutive
+// tokens of one KV head, whose rows lie side by side in a page; neighbouring
+// blocks take the other heads of the same tokens.  The vectors are loaded before
+// their slot is known, so that a block waits for memory once.
 struct F8StoreArgs {
     const void *k, *v;
-    int64_t k_stride, v_stride, n_vec;  // strides in elements; vectors per tensor
+    int64_t k_stride, v_stride, n_tokens;  // strides in elements
     const int64_t* slots;
     uint8_t* cache;
     int64_t num_slots;
@@ -21,49 +24,65 @@ struct F8StoreArgs {
     uint32_t* err;
 };
 
-constexpr int kF8StoreThreads = 256;
+constexpr int kF8StoreThreads = 128;
 
+// 8 elements, as they lie in memory
 template <int DT>
-__device__ __forceinline__ void f8_load8(const void* base, int64_t off, float (&x)[8]) {
-    if constexpr (DT == TQ_DTYPE_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct F8Raw {
+    uint4 w[DT == TQ_DTYPE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, int64_t off) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off * (DT == TQ_DTYPE_F32 ? 4 : 2));
+        w[0] = __ldg(p);
+        if constexpr (DT == TQ_DTYPE_F32) w[1] = __ldg(p + 1);
+    }
+    // largest magnitude: as a number's bits without the sign they are ordered like
+    // integers, inf and NaN above every number.  16-bit types: two maxima, packed
+    __device__ __forceinline__ uint32_t top() const {
+        if constexpr (DT == TQ_DTYPE_F32) {
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = DT == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(u[i]) : F8Elem::from_f16x2(u[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+            for (int i = 0; i < 2; ++i)
+                m = max(max(m, max(w[i].x & 0x7FFFFFFFu, w[i].y & 0x7FFFFFFFu)),
+                        max(w[i].z & 0x7FFFFFFFu, w[i].w & 0x7FFFFFFFu));
+            return m;
+        } else {
+            return __vmaxu2(__vmaxu2(w[0].x & 0x7FFF7FFFu, w[0].y & 0x7FFF7FFFu),
+                            __vmaxu2(w[0].z & 0x7FFF7FFFu, w[0].w & 0x7FFF7FFFu));
         }
     }
-}
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[DT == TQ_DTYPE_F32].x, w[DT == TQ_DTYPE_F32].y,
+                               w[DT == TQ_DTYPE_F32].z, w[DT == TQ_DTYPE_F32].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (DT == TQ_DTYPE_F32) {
+                x[i] = __uint_as_float(u[i]);
+            } else {
+                const float2 f = DT == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(u[i >> 1]) : F8Elem::from_f16x2(u[i >> 1]);
+                x[i] = i & 1 ? f.y : f.x;
+            }
+        }
+    }
+};
 
-// 8 elements of a vector spread over LPV lanes -> 8 codes and the exponent byte
-template <int LPV>
-__device__ __forceinline__ uint2 f8_encode8(const float (&x)[8], uint32_t& ebyte) {
-    uint32_t top = 0;  // |x| as bits: integer order, and inf / NaN sort above every number
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = LPV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+// codes and exponent byte of 8 elements, from the vector's largest magnitude (fp32 bits)
+template <int DT>
+__device__ __forceinline__ uint2 f8_encode8(const F8Raw<DT>& raw, uint32_t top, uint32_t& ebyte) {
     const bool bad = top >= 0x7F800000u;
     // smallest e with top <= 448 * 2^e = 1.75 * 2^(e + 8); at most 120, so no upper clamp
-    const int e = max((int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), 1);
+    const int e = max((int)((top + 0x1FFFFFu) >> 23) - 8, 1);
     ebyte = bad ? 255u : (uint32_t)e;
-    const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e)
+    const float inv = __uint_as_float((uint32_t)(254 - min(e, 254)) << 23);  // 2^(127 - e)
+    float x[8];
+    raw.values(x);
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (inf and NaN times 0 is NaN, which must not reach the codes)
-        const float lo = bad ? 0.f : x[2 * i] * inv, hi = bad ? 0.f : x[2 * i + 1] * inv;
         uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
         c[i] = r;
     }
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    return bad ? make_uint2(0u, 0u) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 template <int D, int DT>
@@ -71,23 +90,37 @@ __global__ void __launch_bounds__(kF8StoreThreads) f8_store_kernel(F8StoreArgs a
     constexpr int LPV = D / 8;  // lanes per vector
     constexpr int PAGE = f8_page_bytes(D);
     const int sub = threadIdx.x % LPV;
-    const int64_t vec = (int64_t)blockIdx.x * (kF8StoreThreads / LPV) + threadIdx.x / LPV;
+    const int group = blockIdx.x / (unsigned)a.heads, h = blockIdx.x - (unsigned)group * a.heads;
+    const int64_t t = (int64_t)group * (kF8StoreThreads / LPV) + threadIdx.x / LPV;
     // whole warps stay for the shuffles; lanes of a vector share every decision
-    const bool in = vec < a.n_vec;
-    const int64_t t = in ? vec / a.heads : 0;
-    const int h = in ? (int)(vec - t * a.heads) : 0;
-    int64_t slot = in ? __ldg(a.slots + t) : -1;
+    F8Raw<DT> k = {}, v = {};
+    int64_t slot = -1;
+    if (t < a.n_tokens) {
+        slot = __ldg(a.slots + t);
+        k.load(a.k, t * a.k_stride + (int64_t)h * D + 8 * sub);
+        v.load(a.v, t * a.v_stride + (int64_t)h * D + 8 * sub);
+    }
     if (slot >= a.num_slots || slot < -1) {
         if (sub == 0) set_error(a.err, TQ_DEVERR_SLOT);
         slot = -1;
     }
-    float xk[8] = {}, xv[8] = {};
-    if (slot >= 0) {
-        f8_load8<DT>(a.k, t * a.k_stride + (int64_t)h * D + 8 * sub, xk);
-        f8_load8<DT>(a.v, t * a.v_stride + (int64_t)h * D + 8 * sub, xv);
+    uint32_t tk = k.top(), tv = v.top();
+    if constexpr (DT == TQ_DTYPE_F32) {
+#pragma unroll
+        for (int o = LPV / 2; o > 0; o >>= 1) {
+            tk = max(tk, __shfl_xor_sync(0xffffffffu, tk, o));
+            tv = max(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+        }
+    } else {
+        // both vectors' maxima in one word: one exchange for the two
+        uint32_t m = __vmaxu2(__byte_perm(tk, tv, 0x5410), __byte_perm(tk, tv, 0x7632));
+#pragma unroll
+        for (int o = LPV / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float2 f = DT == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(m) : F8Elem::from_f16x2(m);
+        tk = __float_as_uint(f.x), tv = __float_as_uint(f.y);
     }
     uint32_t ek, ev;
-    const uint2 ck = f8_encode8<LPV>(xk, ek), cv = f8_encode8<LPV>(xv, ev);
+    const uint2 ck = f8_encode8<DT>(k, tk, ek), cv = f8_encode8<DT>(v, tv, ev);
     if (slot < 0) return;
     uint8_t* page = a.cache + ((slot >> 4) * a.heads + h) * PAGE;
     const int row = (int)(slot & 15);
@@ -102,7 +135,7 @@ __global__ void __launch_bounds__(kF8StoreThreads) f8_store_kernel(F8StoreArgs a
 template <int D, int DT>
 static tq_status launch_f8_store(const F8StoreArgs& a, cudaStream_t s) {
     constexpr int VPB = kF8StoreThreads / (D / 8);
-    const int64_t blocks = (a.n_vec + VPB - 1) / VPB;
+    const int64_t blocks = (a.n_tokens + VPB - 1) / VPB * a.heads;
     if (blocks > 0x7FFFFFFF) return TQ_ERR_INVALID_ARG;
     f8_store_kernel<D, DT><<<(unsigned)blocks, kF8StoreThreads, 0, s>>>(a);
     return cuda_status(cudaGetLastError());
@@ -303,7 +336,7 @@ tq_status tq_f8_store(const tq_f8_cache* c, const void* k, const void* v, int in
     a.v = v;
     a.k_stride = k_stride;
     a.v_stride = v_stride;
-    a.n_vec = num_tokens * c->cfg.num_kv_heads;
+    a.n_tokens = num_tokens;
     a.slots = slot_mapping;
     a.cache = static_cast<uint8_t*>(cache_buf);
     a.num_slots = c->cfg.num_blocks * kBlock;
