@@ -411,8 +411,9 @@ tq_status tq_decode_attention_noalloc(const tq_cache* cache, const void* q, int 
  *   K codes   16 x d   e4m3
  *   V codes   16 x d   e4m3
  *   K scales  16 x u8  exponent byte E: the vector's scale is 2^(E - 127)
- *   V scales  16 x u8  (E = 255: the vector is NaN)
- * page_bytes = 32 d + 32.  A stored element stands for code * 2^(E - 127).
+ *   V scales  16 x u8  (E = 255, with zero codes: the vector is NaN)
+ * page_bytes = 32 d + 32.  A stored element stands for code * 2^(E - 127); the
+ * store writes E = 1 .. 247 and 255, and no NaN code.
  * The scale is a power of two, so that scaling is exact and a stored element
  * carries one rounding, that to e4m3 (4 significant bits, ties to even).
  * ------------------------------------------------------------------------ */
@@ -555,7 +556,8 @@ tq_status tq_prompt_destroy(tq_prompt* p);
  *              the sequences concerned are unspecified)
  *   scale      <= 0 means 1/sqrt(d)
  *   out        device [n_q][H_q][d], 16-byte aligned; lse device fp32
- *              [n_q][H_q] or NULL.  Rows no sequence names are left as they were
+ *              [n_q][H_q] or NULL.  Rows no sequence names are left as they
+ *              were.  Neither may overlap an input
  * Products and sums in fp32, the probabilities rounded to dtype for the value
  * product (their sum is of the unrounded ones).  n_q == 0 is a no-op.
  */

@@ -430,3 +430,5 @@ def test_refusals():
     assert e.value.status == -5
     with pytest.raises(ValueError):
         tq.TQF8Cache(head_dim=128, num_kv_heads=2, num_q_heads=8, num_blocks=4, max_blocks_per_seq=2, cache=c.cache[:-1])
+    with pytest.raises(ValueError):
+        tq.tq_f8_decode_attention(c.handle, c.cfg, q, c.cache[:-1], t, n, q.clone())

@@ -129,6 +129,55 @@ def test_long_prompt_and_many_short_ones():
         _check(q, k, v, lq, lq, True, out, lse)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,g,h,lq,lk,dtype", [
+    (128, 4, 1, [5, 0, 40], [3000, 100, 2500], "bf16"),
+    (128, 8, 2, [70], [4100], "f16"),
+    (256, 8, 1, [17, 1], [2900, 3], "bf16"),
+    (256, 1, 2, [33], [5000], "f16"),
+    (128, 1, 1, [300], [2900], "bf16"),
+    (128, 4, 1, [6], [0], "bf16"),
+])
+def test_few_rows_over_many_keys(d, g, h, lq, lk, dtype, causal):
+    """The keys are cut into parts that other blocks take, and joined; rows behind the last sequence stay."""
+    p, q, k, v, cq, ck = _case(d, g, h, lq, lk, dtype, 19)
+    n, pad = sum(lq), 3
+    q2 = torch.cat([q, torch.zeros((pad,) + q.shape[1:], device="cuda", dtype=q.dtype)])
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=h, num_q_heads=g * h, dtype=DT[dtype], max_batch=3, max_tokens=n + pad)
+    out = torch.full(q2.shape, 5.0, device="cuda", dtype=q.dtype)
+    lse = torch.full(q2.shape[:2], 7.0, device="cuda")
+    p.attention(q2, k, v, cq, ck, out=out, lse=lse, causal=causal)
+    assert p.device_error() == 0
+    _check(q, k, v, lq, lk, causal, out[:n], lse[:n])
+    assert (out[n:] == 5).all() and (lse[n:] == 7).all()
+    again = out.clone()
+    p.attention(q2, k, v, cq, ck, out=out, lse=lse, causal=causal)
+    assert torch.equal(out, again)
+
+
+def test_parts_with_values_a_row_does_not_see():
+    lq, lk = 20, 4000
+    p, q, k, v, cq, ck = _case(128, 4, 1, [lq], [lk], "bf16", 20)
+    v[lk - 1, 0, 3] = float("inf")
+    v[lk - 10, 0, 9] = float("nan")
+    v[100, 0, 50] = float("-inf")  # seen by all
+    out, _ = _run(p, q, k, v, cq, ck)
+    got = _np(out)
+    limit = np.arange(lq) + 1 + lk - lq
+    clean = v.clone()
+    for i, c in ((lk - 1, 3), (lk - 10, 9), (100, 50)):
+        clean[i, 0, c] = 0
+    ref, _, mag = f8.attention(_np(q), _np(k), _np(clean), 1 / np.sqrt(128), limit)
+    tol, _ = _bounds(_np(q), _np(k), 1 / np.sqrt(128), mag, ref, q.dtype, lk)
+    want = ref.copy()
+    want[:, :, 50] = -np.inf
+    want[limit > lk - 1, :, 3] = np.inf
+    want[limit > lk - 10, :, 9] = np.nan
+    fin = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
+    assert np.array_equal(np.isneginf(got), np.isneginf(want)) and (np.abs(got[fin] - want[fin]) <= tol[fin]).all()
+
+
 def test_peaked_scores_and_a_given_scale():
     # references move in nearly every tile: keys grow along the sequence
     lq = [600]
@@ -154,6 +203,11 @@ def test_rows_of_a_projection(d, h):
     cu = _gpu(_starts(lq))
     out, lse = _run(p, q, k, v, cu, cu)
     _check(q, k, v, lq, lq, True, out, lse)
+    # a single row, whose stride says nothing
+    one = torch.randn((1, 5 * h * d + 3), device="cuda").to(torch.bfloat16)[:, :h * d].view(1, h, d)
+    cu = _gpu(_starts([1]))
+    out, lse = _run(p, q[:1], one, one, cu, cu)
+    _check(q[:1], one, one, [1], [1], True, out, lse)
 
 
 @pytest.mark.parametrize("d", [128, 256])

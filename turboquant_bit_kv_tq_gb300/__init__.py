@@ -522,13 +522,15 @@ def _rows(t, name, heads, d, dev):
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be [rows, {heads}, {d}], got {tuple(shape)}")
+    if shape[0] == 0:
+        return t.data_ptr(), heads * d
     row, head, el = t.stride()
     if el != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the [{heads}, {d}] part of a row must be contiguous")
-    if row < heads * d:
-        if shape[0] > 1:
-            raise ValueError(f"{name}: rows overlap (row stride {row})")
-        row = heads * d
+    if shape[0] == 1:
+        row = heads * d  # the stride of a single row says nothing
+    elif row < heads * d:
+        raise ValueError(f"{name}: rows overlap (row stride {row})")
     return t.data_ptr(), row
 
 
@@ -552,6 +554,14 @@ def _index(t, name, dtype, least, dev):
     if t.numel() < least or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with at least {least} entries, got {list(t.shape)}")
     return t.data_ptr()
+
+
+def _pages(cache, cfg):
+    """Pointer of an 8-bit cache's pages."""
+    need = cfg.num_blocks * cfg.num_kv_heads * (32 * cfg.head_dim + 32)
+    if cache is None or not cache.is_cuda or not cache.is_contiguous() or cache.nbytes < need:
+        raise ValueError(f"cache must be a contiguous CUDA tensor of at least {need} bytes")
+    return cache.data_ptr()
 
 
 def _table(t, batch, columns, dev):
@@ -601,7 +611,7 @@ def tq_f8_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
     vp, vs = _rows(v, "v", heads, d, dev)
     n = k.shape[0]
     st = load_library().tq_f8_store(handle, kp, vp, dt, ks, vs, n,
-                                    _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _dev(cache, "cache"),
+                                    _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _pages(cache, cfg),
                                     _launch_stream(stream, dev))
     if st:
         raise TQError(st, "tq_f8_store")
@@ -618,7 +628,7 @@ def tq_f8_load(handle, cfg, cache, block_table, seq_lens, cu_out, k_out, v_out, 
     b, n, i32 = seq_lens.shape[0], k_out.shape[0], _TORCH.int32
     shape = (n, cfg.num_kv_heads, cfg.head_dim)
     st = load_library().tq_f8_load(
-        handle, _dev(cache, "cache"), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        handle, _pages(cache, cfg), _table(block_table, b, cfg.max_blocks_per_seq, dev),
         _index(seq_lens, "seq_lens", i32, b, dev), _index(cu_out, "cu_out", i32, b, dev), b, n,
         _plain(k_out, "k_out", shape, None, dev), _plain(v_out, "v_out", shape, None, dev), dt,
         _launch_stream(stream, dev))
@@ -635,7 +645,7 @@ def tq_f8_decode_attention(handle, cfg, q, cache, block_table, seq_lens, out, sc
     qp, qs = _rows(q, "q", heads, d, dev)
     b = q.shape[0]
     st = load_library().tq_f8_decode_attention(
-        handle, qp, qt, qs, _dev(cache, "cache"), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        handle, qp, qt, qs, _pages(cache, cfg), _table(block_table, b, cfg.max_blocks_per_seq, dev),
         _index(seq_lens, "seq_lens", _TORCH.int32, b, dev), scale, b, _plain(out, "out", (b, heads, d), None, dev), ot,
         _launch_stream(stream, dev))
     if st:
