@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     static_assert(sizeof(F8JoinSmem) <= C::total, "the join reuses the rings");
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    __shared__ int s_last;
+    __shared__ int s_last[2][2];  // [unit][level]: each written once, so that no read of one is overtaken
     __shared__ float4 s_ref[W][HEADS];
     __shared__ F8Seg s_part[2];  // segments whose sums are in the workspace (b < 0: none)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -735,67 +735,111 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         }
         const int kvh = sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
         const int nh = min(a.hp, a.group - hg * a.hp), qh0 = kvh * a.group + hg * a.hp;
+        // two items of a thread at a time, all their loads before the first sum
+        static_assert(C::ITEMS % (2 * kF8Threads) == 0, "items of a thread");
+        __syncthreads();  // the factors
 #pragma unroll 1
-        for (int it = tid; it < C::ITEMS; it += kF8Threads) {
-            const int ln = it & 31, n = (it >> 5) % NT, i = (it >> 5) / NT, h = 8 * n + 2 * (ln & 3);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int it0 = tid; it0 < C::ITEMS; it0 += 2 * kF8Threads) {
+            float4 v[2] = {};
 #pragma unroll 1
-            for (int k0 = 0; k0 < count; k0 += 16) {
-                float4 x[16];
+            for (int k0 = 0; k0 < count; k0 += 8) {
+                float4 x[8][2];
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    x[k] = k0 + k < count ? __ldcg(a.part + slot(k0 + k) * C::ITEMS + it) : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (it == tid && k0 == 0) __syncthreads();  // the factors (every thread has a first item)
+                for (int k = 0; k < 8; ++k)
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k0 + k < count) {
-                        const float2 f = *reinterpret_cast<const float2*>(&js.fac[k0 + k][h]);
-                        v.x += x[k].x * f.x, v.y += x[k].y * f.y, v.z += x[k].z * f.x, v.w += x[k].w * f.y;
-                    }
+                    for (int y = 0; y < 2; ++y)
+                        x[k][y] = k0 + k < count ? __ldcg(a.part + slot(k0 + k) * C::ITEMS + it0 + y * kF8Threads)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + k < count)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int it = it0 + y * kF8Threads, h = 8 * ((it >> 5) % NT) + 2 * (it & 3);
+                            const float2 f = *reinterpret_cast<const float2*>(&js.fac[k0 + k][h]);
+                            v[y].x += x[k][y].x * f.x, v[y].y += x[k][y].y * f.y, v[y].z += x[k][y].z * f.x,
+                                v[y].w += x[k][y].w * f.y;
+                        }
             }
-            if (!fin) {
-                a.part[(int64_t)s0 * C::ITEMS + it] = v;
-            } else if (h < nh) {
-                const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
-                const int64_t at = ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
-                f8_store2(a.out, at, t0.z == 0.f ? 0.f : v.x * t0.w, t0.z == 0.f ? 0.f : v.z * t0.w, a.out_dtype);
-                if (h + 1 < nh)
-                    f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v.y * t1.w, t1.z == 0.f ? 0.f : v.w * t1.w,
-                              a.out_dtype);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int it = it0 + y * kF8Threads;
+                const int ln = it & 31, n = (it >> 5) % NT, i = (it >> 5) / NT, h = 8 * n + 2 * (ln & 3);
+                if (!fin) {
+                    a.part[(int64_t)s0 * C::ITEMS + it] = v[y];
+                } else if (h < nh) {
+                    const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
+                    const int64_t at =
+                        ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
+                    f8_store2(a.out, at, t0.z == 0.f ? 0.f : v[y].x * t0.w, t0.z == 0.f ? 0.f : v[y].z * t0.w, a.out_dtype);
+                    if (h + 1 < nh)
+                        f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v[y].y * t1.w, t1.z == 0.f ? 0.f : v[y].w * t1.w,
+                                  a.out_dtype);
+                }
             }
         }
         if (!fin && tid < HEADS) a.meta[s0 * HEADS + tid] = js.tot[tid];
         __syncthreads();
     };
-    // one more of `all` has arrived at *cnt: is it the last?  (leaves the counter ready for the next call)
+    // one more of `all` has arrived at *cnt, seen by one thread after a barrier: is it
+    // the last?  (leaves the counter ready for the next call)
     auto arrive = [&](uint32_t* cnt, int all) {
-        if (tid == 0) {
-            __threadfence();  // after a barrier: the block's writes
-            s_last = atomicAdd(cnt, 1u) == (uint32_t)(all - 1);
-            if (s_last) *cnt = 0;
-            __threadfence();
-        }
-        __syncthreads();
-        return s_last != 0;
+        __threadfence();  // the block's writes
+        const bool last = atomicAdd(cnt, 1u) == (uint32_t)(all - 1);
+        if (last) *cnt = 0;
+        __threadfence();
+        return last;
     };
-    for (int x = 0; x < 2; ++x) {
-        const F8Seg sg = s_part[x];
-        if (sg.b < 0) continue;
-        // the runs (= blocks) of this unit, from the one that holds its first page on
+    // What a block's part of a unit is joined with: the runs (= blocks) of the unit,
+    // c0 .. c1, from the one that holds its first page on; with more than kF8Join of
+    // them in groups first.
+    struct Step {
+        int jn, j0, j1, st;  // sums to join: slots j0, then j1 + st, j1 + 2 st, ...
+        uint32_t* cnt;
+    };
+    auto step = [&](const F8Seg& sg, int x, bool fin, bool& single) {
         const int v0 = (int)(x ? runs.start(run + 1) - sg.p1 : runs.start(run) - sg.p0);
         const int c0 = (int)runs.owner(v0), c1 = (int)runs.owner(v0 + sg.np() - 1), n = c1 - c0 + 1;
         const int first = 2 * c0 + ((int)runs.start(c0) >= v0 ? 0 : 1);  // slot of block c0; the others': 2 c
         const int gi = ((int)run - c0) / kF8Join, g0 = c0 + gi * kF8Join;
-        // those of its group of blocks (where there are more than one group), then
-        // those of all blocks or groups
-        for (bool fin = n <= kF8Join;; fin = true) {
-            const int jn = !fin ? min(kF8Join, c1 - g0 + 1) : n <= kF8Join ? n : (n + kF8Join - 1) / kF8Join;
-            const int j0 = fin || gi == 0 ? first : 2 * g0, j1 = fin ? 2 * c0 : 2 * g0;
-            uint32_t* cnt = fin ? a.cnt + (int64_t)sg.b * nj + sg.j : a.gcnt + j0;
-            if (!arrive(cnt, jn)) break;
-            if (jn > 1) join(jn, j0, j1, fin && n > kF8Join ? 2 * kF8Join : 2, fin, sg);
-            if (fin) break;
+        single = n <= kF8Join;
+        Step s;
+        if (single || fin) {
+            s.jn = single ? n : (n + kF8Join - 1) / kF8Join;
+            s.j0 = first;
+            s.j1 = 2 * c0;
+            s.st = single ? 2 : 2 * kF8Join;
+            s.cnt = a.cnt + (int64_t)sg.b * nj + sg.j;
+        } else {
+            s.jn = min(kF8Join, c1 - g0 + 1);
+            s.j0 = gi == 0 ? first : 2 * g0;
+            s.j1 = 2 * g0;
+            s.st = 2;
+            s.cnt = a.gcnt + s.j0;
         }
+        return s;
+    };
+    // a block may hold the end of one unit and the beginning of another: both arrive at once
+    if (lane == 0 && warp < 2) {
+        bool single;
+        s_last[warp][0] = 0;
+        if (s_part[warp].b >= 0) {
+            const Step s = step(s_part[warp], warp, false, single);
+            s_last[warp][0] = arrive(s.cnt, s.jn);
+        }
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x) {
+        if (!s_last[x][0]) continue;
+        const F8Seg sg = s_part[x];
+        bool single;
+        Step s = step(sg, x, false, single);
+        if (s.jn > 1) join(s.jn, s.j0, s.j1, s.st, single, sg);
+        if (single) continue;
+        s = step(sg, x, true, single);
+        if (tid == 0) s_last[x][1] = arrive(s.cnt, s.jn);
+        __syncthreads();
+        if (s_last[x][1]) join(s.jn, s.j0, s.j1, s.st, true, sg);
     }
 }
 
