@@ -271,6 +271,30 @@ def test_decode_value_scales_far_apart(d, g, ot):
         _check_decode(c, q, table, lens, ot, got)
 
 
+@pytest.mark.parametrize("x", [-121, 118])
+@pytest.mark.parametrize("d,lens", [(128, [9000, 40]), (256, [700, 3000])])
+def test_decode_values_at_the_ends_of_the_range(d, lens, x):
+    """Values near 2^x, all positive: the power of two of the output and the row
+    sum meet at its end only.  In units of 2^x, beside the bound above one
+    rounding of an fp32 number that may be subnormal: 2^-150."""
+    rng = _rng(13, d, x & 255)
+    g, n = 4, sum(lens)
+    table, blocks = _table(rng, lens)
+    c = _cache(d, 1, g, blocks, len(lens), table.shape[1])
+    k, v = 0.05 * rng.standard_normal((n, 1, d)), rng.uniform(0.5, 4, (n, 1, d)) * 2.0 ** x
+    c.store(_gpu(k, torch.float32), _gpu(v, torch.float32), _gpu(_slots(table, lens)))
+    q = rng.standard_normal((len(lens), g, d)).astype(np.float32)
+    got = c.decode(_gpu(q), _gpu(table), _gpu(np.array(lens, np.int32)))
+    pages, sc = c.pages().cpu().numpy(), 1 / np.sqrt(d)
+    for b, m in enumerate(lens):
+        kb, vb = f8.rows(pages, table[b], m, d)
+        vb = vb * 2.0 ** -x
+        ref, _, mag = f8.attention(q[b:b + 1].astype(np.float64), kb, vb, sc)
+        tol = _bound(q[b:b + 1].astype(np.float64), kb, vb, sc, mag, ref, True, got.dtype)[0] + 2.0 ** (-150 - x)
+        err = np.abs(_np(got)[b] * 2.0 ** -x - ref[0])
+        assert (err <= tol).all(), (b, m, err.max(), (err / tol).max())
+
+
 def test_decode_queries_far_from_one_and_a_given_scale():
     for qt, gain in (("f32", 2.0 ** 90), ("f32", 2.0 ** -90), ("bf16", 2.0 ** 100), ("f16", 2.0 ** -14)):
         lens = [333]

@@ -56,15 +56,6 @@ struct F8Elem {
     }
 };
 
-// four consecutive elements at p (16-bit: 8-byte aligned, fp32: 16-byte)
-__device__ __forceinline__ float4 f8_load4(const void* p, int dtype) {
-    if (dtype == TQ_DTYPE_F32) return __ldg(static_cast<const float4*>(p));
-    const uint2 w = __ldg(static_cast<const uint2*>(p));
-    const float2 a = dtype == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(w.x) : F8Elem::from_f16x2(w.x);
-    const float2 b = dtype == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(w.y) : F8Elem::from_f16x2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
 __device__ __forceinline__ uint32_t f8_pack16(float x, float y, int dtype) {
     if (dtype == TQ_DTYPE_BF16) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);

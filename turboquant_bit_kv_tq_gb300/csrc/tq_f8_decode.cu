@@ -162,14 +162,18 @@ struct F8Runs {
     }
 };
 
-// 2^(r' - r) / l of a head's sums; no token: 0
-__device__ __forceinline__ float f8_norm(float R, float Rv, float L) { return L == 0.f ? 0.f : exp2f(Rv - R) / L; }
+// 2^(r' - r) / l of a head's sums, as two factors: the power alone is subnormal
+// where the value scales are the smallest.  No token: 0
+__device__ __forceinline__ float2 f8_norm(float R, float Rv, float L) {
+    const float half = exp2f(0.5f * (Rv - R));
+    return L == 0.f ? make_float2(0.f, 0.f) : make_float2(half / L, half);
+}
 
 constexpr int kF8SoloPages = 16;  // a warp takes units of up to this many pages alone, whatever its share
 constexpr int kF8Join = 16;  // blocks a group joins; at most kF8MaxSms * kF8Ctas / kF8Join + 1 groups
 struct F8JoinSmem {
     float fac[32][16];
-    float4 tot[16];
+    float4 tot[16];  // {r, r', l, -} for another join, {f8_norm's factors, l, -} for the output
 };
 static_assert(kF8MaxSms * kF8Ctas / kF8Join + 1 <= 32, "groups of a join");
 
@@ -677,15 +681,15 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int h = 8 * n + 2 * c + e;
-                        const float f = f8_norm(r[n][e], rv[n][e], l[n][e]);
+                        const float2 f = f8_norm(r[n][e], rv[n][e], l[n][e]);
                         if (h < nh)
 #pragma unroll
                             for (int i0 = 0; i0 < D / 16; i0 += 8) {
                                 float v[16];
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    v[2 * i] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][e] * f;
-                                    v[2 * i + 1] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][2 + e] * f;
+                                    v[2 * i] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][e] * f.x * f.y;
+                                    v[2 * i + 1] = l[n][e] == 0.f ? 0.f : o[i0 + i][n][2 + e] * f.x * f.y;
                                 }
                                 f8_store16(a.out, ((int64_t)sg.b * a.q_heads + qh0 + h) * D + 16 * i0 + 16 * g, v,
                                            a.out_dtype);
@@ -731,7 +735,8 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             const float R = warp_max(m.x), Rv = warp_max(m.y);
             const float L = warp_sum(m.z * f8_exp2(m.x - R));
             js.fac[lane][h] = f8_exp2(m.y - Rv);
-            if (lane == 0) js.tot[h] = make_float4(R, Rv, L, f8_norm(R, Rv, L));
+            const float2 f = f8_norm(R, Rv, L);
+            if (lane == 0) js.tot[h] = fin ? make_float4(f.x, f.y, L, 0.f) : make_float4(R, Rv, L, 0.f);
         }
         const int kvh = sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
         const int nh = min(a.hp, a.group - hg * a.hp), qh0 = kvh * a.group + hg * a.hp;
@@ -771,10 +776,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                     const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
                     const int64_t at =
                         ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
-                    f8_store2(a.out, at, t0.z == 0.f ? 0.f : v[y].x * t0.w, t0.z == 0.f ? 0.f : v[y].z * t0.w, a.out_dtype);
+                    f8_store2(a.out, at, t0.z == 0.f ? 0.f : v[y].x * t0.x * t0.y,
+                              t0.z == 0.f ? 0.f : v[y].z * t0.x * t0.y, a.out_dtype);
                     if (h + 1 < nh)
-                        f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v[y].y * t1.w, t1.z == 0.f ? 0.f : v[y].w * t1.w,
-                                  a.out_dtype);
+                        f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v[y].y * t1.x * t1.y,
+                                  t1.z == 0.f ? 0.f : v[y].w * t1.x * t1.y, a.out_dtype);
                 }
             }
         }
