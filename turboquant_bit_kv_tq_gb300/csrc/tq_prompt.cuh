@@ -769,31 +769,50 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 }
                 tc_wait_st();
             }
+            // 4 x 4 transposition over a quad of lanes: swap pieces with lane ^ 1, then with
+            // lane ^ 2; lane u of a quad ends up with 16-byte piece u of the quad's four rows
+            const int u = lane & 3;
+            auto quad = [&](uint32_t (&p)[4][4]) {
+#pragma unroll
+                for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (!(q & b))
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t send = u & b ? p[q][x] : p[q | b][x];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, b);
+                                if (u & b) p[q][x] = got;
+                                else p[q | b][x] = got;
+                            }
+            };
+            // four lanes write 64 bytes of one row side by side (a lane alone would touch
+            // 32 lines with every store)
+            int64_t rows[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(0xffffffffu, live ? row : -1, (lane & ~3) + r);
             if (a.parts > 1) {
-                const int64_t at = (int64_t)w.part * a.n_q * a.q_heads + row;
+                const int64_t part = (int64_t)w.part * a.n_q * a.q_heads;
                 if (nt > 0) {
 #pragma unroll 1
-                    for (int i = 0; i < D; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(so + i, o);
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(so + i, o);
                         tc_wait_ld();
-                        if (live) {
-                            uint4* dst = reinterpret_cast<uint4*>(a.part + at * D + i);
+                        uint32_t p[4][4];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        }
+                        for (int k = 0; k < 16; ++k) p[k >> 2][k & 3] = o[k];
+                        quad(p);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (rows[r] >= 0)
+                                *reinterpret_cast<uint4*>(a.part + (part + rows[r]) * D + i + 4 * u) =
+                                    make_uint4(p[r][0], p[r][1], p[r][2], p[r][3]);
                     }
                 }
-                if (live) a.meta[at] = make_float2(m, l);
+                if (live) a.meta[part + row] = make_float2(m, l);
             } else {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                // four lanes write 64 bytes of one row side by side (a lane alone
-                // would touch 32 lines with every store): lane u of a quad ends up
-                // with 16-byte piece u of the quad's four rows
-                const int u = lane & 3;
-                int64_t rows[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(0xffffffffu, live ? row : -1, (lane & ~3) + r);
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
@@ -807,19 +826,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         p[k >> 2][k & 3] = l == 0.f ? 0u
                                                     : prompt_pack<C::BF16>(__uint_as_float(o[2 * k]) * inv,
                                                                            __uint_as_float(o[2 * k + 1]) * inv);
-                    // 4 x 4 transposition over the quad: swap pieces with lane ^ 1, then with lane ^ 2
-#pragma unroll
-                    for (int b = 1; b < 4; b <<= 1)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (!(q & b))
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const uint32_t send = u & b ? p[q][x] : p[q | b][x];
-                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, send, b);
-                                    if (u & b) p[q][x] = got;
-                                    else p[q | b][x] = got;
-                                }
+                    quad(p);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (rows[r] >= 0)
@@ -839,46 +846,54 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Add the parts of every row up.  One block per query row, one warp per head at a
-// time; a part without a key of the row has l = 0 and no sums.
+// Add the parts of every row up, one warp per row and head; a part without a key of
+// the row has l = 0 and no sums.  Eight parts' loads are under way at a time.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)a.n_q * a.q_heads, row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     pdl_wait();
+    if (row >= rows) return;
     // rows no sequence names are left as they were
+    const int tok = (int)(row / a.q_heads);
     bool mine = false;
     for (int b = lane; b < a.batch; b += 32) mine |= __ldg(a.cu_q + b) <= tok && tok < __ldg(a.cu_q + b + 1);
+    // lane z: part z
+    const float2 ml = lane < a.parts ? __ldcg(a.meta + lane * rows + row) : make_float2(-INFINITY, 0.f);
     if (!__any_sync(0xffffffffu, mine)) return;
-    const int64_t rows = (int64_t)a.n_q * a.q_heads;
-    for (int h = warp; h < a.q_heads; h += 8) {
-        const int64_t row = (int64_t)tok * a.q_heads + h;
-        // lane z: part z
-        const float2 ml = lane < a.parts ? __ldcg(a.meta + lane * rows + row) : make_float2(-INFINITY, 0.f);
-        const float M = warp_max(ml.x);
-        const float f = ml.y == 0.f ? 0.f : M == -INFINITY ? 1.f : prompt_exp2((ml.x - M) * a.scale_log2);
-        const float l = warp_sum(ml.y == 0.f ? 0.f : ml.y * f);
-        float o[D / 32];
+    const float M = warp_max(ml.x);
+    const float f = ml.y == 0.f ? 0.f : M == -INFINITY ? 1.f : prompt_exp2((ml.x - M) * a.scale_log2);
+    const float l = warp_sum(ml.y == 0.f ? 0.f : ml.y * f);
+    const uint32_t there = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    float o[D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-        for (int z = 0; z < a.parts; ++z) {
-            const float fz = __shfl_sync(0xffffffffu, f, z);
-            if (__shfl_sync(0xffffffffu, ml.y, z) == 0.f) continue;
-            const float4* p = reinterpret_cast<const float4*>(a.part + (z * rows + row) * D) + lane;
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    for (int z0 = 0; z0 < a.parts; z0 += 8) {
+        float4 x[8][D / 128];
 #pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                const float4 x = __ldcg(p + 32 * i);
-                o[4 * i] = fmaf(x.x, fz, o[4 * i]), o[4 * i + 1] = fmaf(x.y, fz, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(x.z, fz, o[4 * i + 2]), o[4 * i + 3] = fmaf(x.w, fz, o[4 * i + 3]);
-            }
+        for (int z = 0; z < 8; ++z)
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i)
+                if (there >> (z0 + z) & 1)
+                    x[z][i] = __ldcg(reinterpret_cast<const float4*>(a.part + ((z0 + z) * rows + row) * D) + lane + 32 * i);
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            const float fz = __shfl_sync(0xffffffffu, f, z0 + z);
+            if (there >> (z0 + z) & 1)
+#pragma unroll
+                for (int i = 0; i < D / 128; ++i) {
+                    o[4 * i] = fmaf(x[z][i].x, fz, o[4 * i]), o[4 * i + 1] = fmaf(x[z][i].y, fz, o[4 * i + 1]);
+                    o[4 * i + 2] = fmaf(x[z][i].z, fz, o[4 * i + 2]), o[4 * i + 3] = fmaf(x[z][i].w, fz, o[4 * i + 3]);
+                }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int i = 0; i < D / 128; ++i)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 128 * i + 4 * lane) =
-                make_uint2(prompt_pack<BF16>(o[4 * i] * inv, o[4 * i + 1] * inv),
-                           prompt_pack<BF16>(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
-        if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : M * a.scale + logf(l);
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < D / 128; ++i)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 128 * i + 4 * lane) =
+            make_uint2(prompt_pack<BF16>(o[4 * i] * inv, o[4 * i + 1] * inv),
+                       prompt_pack<BF16>(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
+    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : M * a.scale + logf(l);
 }
 
 // Parts of the keys: as many as shorten the longest run of a block, the join
@@ -914,7 +929,7 @@ tq_status launch_prompt(PromptArgs a, int64_t part_rows, const CUtensorMap& mq, 
     prompt_kernel<C><<<grid, C::THREADS, C::total, s>>>(a, mq, mk, mv);
     st = cuda_status(cudaGetLastError());
     if (st == TQ_OK && a.parts > 1)
-        st = cuda_status(launch_pdl(true, prompt_join_kernel<C::D, C::BF16>, dim3(a.n_q), dim3(256), 0, s, a));
+        st = cuda_status(launch_pdl(true, prompt_join_kernel<C::D, C::BF16>, dim3((unsigned)(((int64_t)a.n_q * a.q_heads + 7) / 8)), dim3(256), 0, s, a));
     return st;
 }
 
