@@ -316,6 +316,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // launched programmatically: what is above overlaps the previous kernel's end (not
+    // the allocation, which could take tensor memory that kernel still asks for)
+    pdl_wait();
     if (warp == 0) tmem_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
@@ -926,8 +929,7 @@ tq_status launch_prompt(PromptArgs a, int64_t part_rows, const CUtensorMap& mq, 
     const int64_t items = ((int64_t)a.n_q + (int64_t)a.batch * (per - 1)) / per * a.heads;
     a.parts = prompt_parts<C>(a, items, sms, part_rows);
     const int grid = (int)std::min<int64_t>(items * a.parts, sms);
-    prompt_kernel<C><<<grid, C::THREADS, C::total, s>>>(a, mq, mk, mv);
-    st = cuda_status(cudaGetLastError());
+    st = cuda_status(launch_pdl(true, prompt_kernel<C>, dim3(grid), dim3(C::THREADS), C::total, s, a, mq, mk, mv));
     if (st == TQ_OK && a.parts > 1)
         st = cuda_status(launch_pdl(true, prompt_join_kernel<C::D, C::BF16>, dim3((unsigned)(((int64_t)a.n_q * a.q_heads + 7) / 8)), dim3(256), 0, s, a));
     return st;
