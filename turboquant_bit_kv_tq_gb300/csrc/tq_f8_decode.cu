@@ -429,11 +429,17 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 ++used;
                 const uint8_t* sp = ring + stage * C::STEP;
                 // ---- scores
-                float s[PP][NT][4];
+                // chains of dependent products: one per page and n-tile, two more where
+                // that is only one, and the queries' second parts in their own
+                constexpr int CH = PP * NT == 1 ? 2 : 1, ACC = CH * (PREC ? 2 : 1);
+                float acc[ACC][PP][NT][4];
 #pragma unroll
-                for (int pp = 0; pp < PP; ++pp)
+                for (int x = 0; x < ACC; ++x)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) s[pp][n][0] = s[pp][n][1] = s[pp][n][2] = s[pp][n][3] = 0.f;
+                    for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            acc[x][pp][n][0] = acc[x][pp][n][1] = acc[x][pp][n][2] = acc[x][pp][n][3] = 0.f;
 #pragma unroll
                 for (int h = 0; h < D / 64; ++h) {
                     uint4 ka[PP][2];
@@ -457,12 +463,23 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                                 const uint32_t w1 = k == 0 ? ka[pp][1].x : k == 1 ? ka[pp][1].y : k == 2 ? ka[pp][1].z : ka[pp][1].w;
                                 const uint32_t a0 = f8_to_f16x2(w0), a1 = f8_to_f16x2(w1), a2 = f8_to_f16x2_hi(w0),
                                                a3 = f8_to_f16x2_hi(w1);
-                                f8_mma(s[pp][n], a0, a1, a2, a3, b);
-                                if constexpr (PREC) f8_mma(s[pp][n], a0, a1, a2, a3, bl);
+                                f8_mma(acc[k % CH][pp][n], a0, a1, a2, a3, b);
+                                if constexpr (PREC) f8_mma(acc[CH + k % CH][pp][n], a0, a1, a2, a3, bl);
                             }
                         }
                     }
                 }
+                float s[PP][NT][4];
+#pragma unroll
+                for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[pp][n][i] = acc[ACC - 1][pp][n][i];
+#pragma unroll
+                            for (int x = ACC - 2; x >= 0; --x) s[pp][n][i] += acc[x][pp][n][i];
+                        }
 
                 // ---- weights.  p = 2^(x - r), w = 2^(x + ev - r') with x = score * ck
                 float ck[PP][2], ev[PP][2], pw[PP][NT][4], w[PP][NT][4], top = 0.f;
@@ -591,18 +608,22 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             const uint32_t t3 = k == 0 ? v[3].x : k == 1 ? v[3].y : k == 2 ? v[3].z : v[3].w;
                             const uint32_t x0 = __byte_perm(t0, t1, 0x5140), x1 = __byte_perm(t0, t1, 0x7362);
                             const uint32_t y0 = __byte_perm(t2, t3, 0x5140), y1 = __byte_perm(t2, t3, 0x7362);
+                            uint32_t va[2][4];
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
                                 const uint32_t x = m ? x1 : x0, y = m ? y1 : y0;
-                                const uint32_t a0 = f8_to_f16x2(x), a1 = f8_to_f16x2_hi(x), a2 = f8_to_f16x2(y),
-                                               a3 = f8_to_f16x2_hi(y);
-                                const int i = 8 * h + 2 * k + m;
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    f8_mma(o[i][n], a0, a1, a2, a3, pb[pp][n]);
-                                    if constexpr (PREC) f8_mma(o[i][n], a0, a1, a2, a3, pl[pp][n]);
-                                }
+                                va[m][0] = f8_to_f16x2(x), va[m][1] = f8_to_f16x2_hi(x);
+                                va[m][2] = f8_to_f16x2(y), va[m][3] = f8_to_f16x2_hi(y);
                             }
+                            // (the weights' second parts after both m: not behind their own first)
+#pragma unroll
+                            for (int part = 0; part < (PREC ? 2 : 1); ++part)
+#pragma unroll
+                                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+                                        f8_mma(o[8 * h + 2 * k + m][n], va[m][0], va[m][1], va[m][2], va[m][3],
+                                               part ? pl[pp][n] : pb[pp][n]);
                         }
                     }
                 }
