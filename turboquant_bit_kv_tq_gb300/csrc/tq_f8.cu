@@ -262,7 +262,7 @@ static tq_status f8_check(const tq_f8_config& c) {
     // q rows and the pages of all block-table entries, KV heads and head groups within int32
     const F8Geom g = f8_geom(c);
     if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF ||
-        (double)c.max_batch * c.max_blocks_per_seq * c.num_kv_heads * g.nhg > 2147483647.0 ||
+        (double)c.max_batch * (c.max_blocks_per_seq + kF8UnitCost) * c.num_kv_heads * g.nhg > 2147483647.0 ||
         (double)c.num_blocks * c.num_kv_heads > 2147483647.0)
         return TQ_ERR_INVALID_ARG;
     return TQ_OK;

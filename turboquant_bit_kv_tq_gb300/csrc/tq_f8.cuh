@@ -9,6 +9,7 @@ namespace tq {
 // kF8MaxSms SMs; the workspace holds two partial sums for each block.
 constexpr int kF8Warps = 4, kF8Ctas = 3, kF8MaxSms = 160;
 constexpr int kF8Slots = 2 * kF8Ctas * kF8MaxSms;
+constexpr int kF8UnitCost = 8;  // places of the order that is dealt out a unit takes beside its pages
 
 // Query heads of one KV head that one work unit serves (nhg units per KV head
 // share its pages through L2 when G > 16), in n-tiles of 8 heads.

@@ -117,6 +117,10 @@ struct F8Cfg {
     static constexpr int off_info = off_bar + kF8Warps * STAGES * 8;       // [warps][STAGES][PP] valid tokens
     static constexpr int total = off_info + kF8Warps * STAGES * PP * 4 + 1024;  // + alignment to 1024
     static constexpr int ITEMS = D / 16 * NT * 32;     // float4 per partial sum
+    // the join's factors, then partial sums, in place of rings and query operands
+    static constexpr int JOIN_AT = 4096;
+    static constexpr int JOIN_FIT = (off_ex - JOIN_AT) / (ITEMS * 16), JOIN_CAP = JOIN_FIT < 32 ? JOIN_FIT : 32;
+    static_assert(JOIN_CAP >= 1, "place for a join");
     // two sums fit the four warps' query operands, whose place they take at a segment's end
     static_assert(2 * ITEMS * 16 <= kF8Warps * QF, "merge buffers");
 };
@@ -125,24 +129,30 @@ static_assert(kF8Ctas >= F8Cfg<128, 1, false>::CTAS, "workspace slots");
 __device__ __forceinline__ int f8_clamp(const F8DecodeArgs& a, int len) { return max(0, min(len, a.max_blocks * 16)); }
 __device__ __forceinline__ int f8_pages(const F8DecodeArgs& a, int len) { return (f8_clamp(a, len) + 15) >> 4; }
 
+// A unit (a sequence's KV head and head group) costs more than its pages (its query,
+// its sums): in the order that is dealt out kF8UnitCost empty places follow its last.
+__device__ __forceinline__ int f8_places(int np) { return np > 0 ? np + kF8UnitCost : 0; }
+
 // A position in the order (sequence, KV head and head group, page) and the
-// pages left of a warp's run.
+// places left of a run.
 struct F8Walk {
-    int b, j, p, len, left;
+    int b, j, p, len, left, at;
 };
 struct F8Seg {
-    int b, j, p0, p1, len;
+    int b, j, p0, p1, len, v0;  // pages [p0, p1), none if the run has only empty places of the unit; v0: place of page 0
     __device__ __forceinline__ int np() const { return (len + 15) >> 4; }
 };
 __device__ __forceinline__ F8Seg f8_next(const F8DecodeArgs& a, F8Walk& w, int nj) {
     F8Seg s;
     s.b = w.b;
     s.j = w.j;
-    s.p0 = w.p;
     s.len = w.len;
-    const int n = min(s.np() - w.p, w.left);
-    s.p1 = w.p + n;
+    s.v0 = w.at - w.p;
+    const int np = s.np(), n = min(f8_places(np) - w.p, w.left);
+    s.p0 = min(w.p, np);
+    s.p1 = min(w.p + n, np);
     w.left -= n;
+    w.at += n;
     w.p = 0;
     if (++w.j == nj) {
         w.j = 0;
@@ -170,22 +180,27 @@ __device__ __forceinline__ float2 f8_norm(float R, float Rv, float L) {
 }
 
 constexpr int kF8SoloPages = 16;  // a warp takes units of up to this many pages alone, whatever its share
-constexpr int kF8Join = 16;  // blocks a group joins; at most kF8MaxSms * kF8Ctas / kF8Join + 1 groups
+// The parts of up to kF8Join blocks are joined by the last of them; of more, by the
+// last of each kF8Group, and the groups' by the last group (one KV head, 32768 tokens
+// = 128 blocks: 21 us in groups of 16, 25 in groups of 32; 8 x up to 32768 with at most
+// 18 blocks a unit: 70 us in one step).
+constexpr int kF8Join = 32, kF8Group = 16;
 struct F8JoinSmem {
-    float fac[32][16];
+    float fac[kF8Join][16];
     float4 tot[16];  // {r, r', l, -} for another join, {f8_norm's factors, l, -} for the output
 };
-static_assert(kF8MaxSms * kF8Ctas / kF8Join + 1 <= 32, "groups of a join");
+static_assert(kF8Join <= 32 && kF8MaxSms * kF8Ctas / kF8Group + 1 <= kF8Join, "groups of a join");
 
 template <int D, int NT, bool PREC>
 __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decode_kernel(const __grid_constant__ F8DecodeArgs a, const __grid_constant__ CUtensorMap pages) {
     using C = F8Cfg<D, NT, PREC>;
     constexpr int S = C::STAGES, PP = C::PP, W = kF8Warps, HEADS = C::HEADS;
-    static_assert(sizeof(F8JoinSmem) <= C::total, "the join reuses the rings");
+    static_assert(sizeof(F8JoinSmem) <= C::JOIN_AT, "the join reuses the rings");
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     __shared__ int s_last[2][2];  // [unit][level]: each written once, so that no read of one is overtaken
     __shared__ float4 s_ref[W][HEADS];
+    __shared__ uint64_t s_jbar;  // the joins' copies
     __shared__ F8Seg s_part[2];  // segments whose sums are in the workspace (b < 0: none)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int nj = a.heads * a.nhg;
@@ -196,6 +211,8 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     int* info = reinterpret_cast<int*>(smem + C::off_info) + warp * S * PP;
     const int tok = f8_token(g);
     bool dead = false;
+    const uint32_t jbar = smem_u32(&s_jbar);
+    if (tid == 0) mbar_init(jbar, 1);
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -213,7 +230,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         const int len = __ldg(a.lens + b);
         if (len < 0 || len > a.max_blocks * 16) set_error(a.err, TQ_DEVERR_SEQLEN);
         const int np = f8_pages(a, len);
-        mine += np;
+        mine += f8_places(np);
         some += np > 0;
         most = max(most, np);
     }
@@ -242,7 +259,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     const bool solo = units > (int)gridDim.x && most <= max(kF8SoloPages, 2 * (total / warps));
     F8Runs runs;
     runs.n = solo ? (uint32_t)min(warps, total)
-                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, total / units / 16));
+                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, (total / units - kF8UnitCost) / 16));
     runs.q = (uint32_t)total / runs.n;
     runs.r = (uint32_t)total - runs.q * runs.n;
     const uint32_t run = solo ? blockIdx.x * W + warp : blockIdx.x;
@@ -256,7 +273,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             if (here)
                 for (;; ++b) {
                     len = __ldg(a.lens + b);
-                    const int n = f8_pages(a, len) * nj;
+                    const int n = f8_places(f8_pages(a, len)) * nj;
                     if (u < at + n) break;
                     at += n;
                 }
@@ -264,10 +281,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             F8Walk w;
             w.b = __shfl_sync(0xffffffffu, b, src);
             w.len = f8_clamp(a, __shfl_sync(0xffffffffu, len, src));
-            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = (w.len + 15) >> 4;
+            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = f8_places((w.len + 15) >> 4);
             w.j = rel / np;
             w.p = rel - w.j * np;
             w.left = total - u;
+            w.at = u;
             return w;
         };
         int u0 = (int)runs.start(run), u1 = (int)runs.start(run + 1);
@@ -276,10 +294,10 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             // the units that start in [u0, u1)
             if (u1 < total) {
                 const F8Walk w = locate(u1);
-                if (w.p > 0) u1 += ((w.len + 15) >> 4) - w.p;
+                if (w.p > 0) u1 += f8_places((w.len + 15) >> 4) - w.p;
             }
             if (cons.p > 0) {
-                u0 += ((cons.len + 15) >> 4) - cons.p;
+                u0 += f8_places((cons.len + 15) >> 4) - cons.p;
                 f8_next(a, cons, nj);
             }
         }
@@ -333,6 +351,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 
         while (cons.left > 0) {
             const F8Seg sg = f8_next(a, cons, nj);
+            if (sg.p0 == sg.p1) continue;
             const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
             const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
             const int qh0 = kvh * a.group + hg * a.hp;
@@ -717,7 +736,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             }
                     }
             } else {
-                const int which = u0 >= u1 - cons.left - sg.p1 ? 0 : 1;  // 0: the run starts in this unit
+                const int which = u0 >= sg.v0 ? 0 : 1;  // 0: the run starts in this unit
                 const int slot = 2 * (int)run + which;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
@@ -746,63 +765,73 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
     // ---- joins
     __syncthreads();  // the rings are free, the block's sums written
     F8JoinSmem& js = *reinterpret_cast<F8JoinSmem*>(smem);
+    int joined = 0;
     // the sums of `count` <= 32 slots (s0, then s1 + st, s1 + 2 st, ...) into slot s0, or out
     auto join = [&](int count, int s0, int s1, int st, bool fin, const F8Seg& sg) {
         auto slot = [&](int k) { return (int64_t)(k == 0 ? s0 : s1 + k * st); };
-        // lane k: slot k
-        for (int h = warp; h < HEADS; h += W) {
-            float4 m = make_float4(kF8None, kF8None, 0.f, 0.f);
-            if (lane < count) m = __ldcg(a.meta + slot(lane) * HEADS + h);
-            const float R = warp_max(m.x), Rv = warp_max(m.y);
-            const float L = warp_sum(m.z * f8_exp2(m.x - R));
-            js.fac[lane][h] = f8_exp2(m.y - Rv);
-            const float2 f = f8_norm(R, Rv, L);
-            if (lane == 0) js.tot[h] = fin ? make_float4(f.x, f.y, L, 0.f) : make_float4(R, Rv, L, 0.f);
+        constexpr int IPT = C::ITEMS / kF8Threads;
+        static_assert(C::ITEMS % kF8Threads == 0, "items of a thread");
+        float4 v[IPT];
+#pragma unroll
+        for (int y = 0; y < IPT; ++y) v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = 0; k0 < count; k0 += C::JOIN_CAP) {
+            const int n = min(C::JOIN_CAP, count - k0);
+            // the sums come by bulk copies, all under way at once; lane k: slot k0 + k
+            if (warp == 0) {
+                if (lane == 0) mbar_expect_tx(jbar, n * (C::ITEMS * 16));
+                __syncwarp();
+                if (lane < n) {
+                    // other blocks' plain writes, and this block's last use of the place, before the copy
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    bulk_copy(smem_u32(smem) + C::JOIN_AT + lane * (C::ITEMS * 16), a.part + slot(k0 + lane) * C::ITEMS,
+                              C::ITEMS * 16, jbar);
+                }
+            }
+            if (k0 == 0) {
+                // lane k: slot k
+                for (int h = warp; h < HEADS; h += W) {
+                    float4 m = make_float4(kF8None, kF8None, 0.f, 0.f);
+                    if (lane < count) m = __ldcg(a.meta + slot(lane) * HEADS + h);
+                    const float R = warp_max(m.x), Rv = warp_max(m.y);
+                    const float L = warp_sum(m.z * f8_exp2(m.x - R));
+                    js.fac[lane][h] = f8_exp2(m.y - Rv);
+                    const float2 f = f8_norm(R, Rv, L);
+                    if (lane == 0) js.tot[h] = fin ? make_float4(f.x, f.y, L, 0.f) : make_float4(R, Rv, L, 0.f);
+                }
+                __syncthreads();  // the factors
+            }
+            if (!mbar_wait(jbar, joined & 1, a.err)) mbar_wait(jbar, joined & 1, a.err);
+            ++joined;
+            const float4* x = reinterpret_cast<const float4*>(smem + C::JOIN_AT) + tid;
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+#pragma unroll
+                for (int y = 0; y < IPT; ++y) {
+                    const int it = tid + y * kF8Threads, h = 8 * ((it >> 5) % NT) + 2 * (it & 3);
+                    const float4 z = x[k * C::ITEMS + y * kF8Threads];
+                    const float2 f = *reinterpret_cast<const float2*>(&js.fac[k0 + k][h]);
+                    v[y].x += z.x * f.x, v[y].y += z.y * f.y, v[y].z += z.z * f.x, v[y].w += z.w * f.y;
+                }
+            }
+            __syncthreads();  // the place is free
         }
         const int kvh = sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
         const int nh = min(a.hp, a.group - hg * a.hp), qh0 = kvh * a.group + hg * a.hp;
-        // two items of a thread at a time, all their loads before the first sum
-        static_assert(C::ITEMS % (2 * kF8Threads) == 0, "items of a thread");
-        __syncthreads();  // the factors
-#pragma unroll 1
-        for (int it0 = tid; it0 < C::ITEMS; it0 += 2 * kF8Threads) {
-            float4 v[2] = {};
-#pragma unroll 1
-            for (int k0 = 0; k0 < count; k0 += 8) {
-                float4 x[8][2];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        x[k][y] = k0 + k < count ? __ldcg(a.part + slot(k0 + k) * C::ITEMS + it0 + y * kF8Threads)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k0 + k < count)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int it = it0 + y * kF8Threads, h = 8 * ((it >> 5) % NT) + 2 * (it & 3);
-                            const float2 f = *reinterpret_cast<const float2*>(&js.fac[k0 + k][h]);
-                            v[y].x += x[k][y].x * f.x, v[y].y += x[k][y].y * f.y, v[y].z += x[k][y].z * f.x,
-                                v[y].w += x[k][y].w * f.y;
-                        }
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int it = it0 + y * kF8Threads;
-                const int ln = it & 31, n = (it >> 5) % NT, i = (it >> 5) / NT, h = 8 * n + 2 * (ln & 3);
-                if (!fin) {
-                    a.part[(int64_t)s0 * C::ITEMS + it] = v[y];
-                } else if (h < nh) {
-                    const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
-                    const int64_t at =
-                        ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
-                    f8_store2(a.out, at, t0.z == 0.f ? 0.f : v[y].x * t0.x * t0.y,
-                              t0.z == 0.f ? 0.f : v[y].z * t0.x * t0.y, a.out_dtype);
-                    if (h + 1 < nh)
-                        f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v[y].y * t1.x * t1.y,
-                                  t1.z == 0.f ? 0.f : v[y].w * t1.x * t1.y, a.out_dtype);
-                }
+        for (int y = 0; y < IPT; ++y) {
+            const int it = tid + y * kF8Threads;
+            const int ln = it & 31, n = (it >> 5) % NT, i = (it >> 5) / NT, h = 8 * n + 2 * (ln & 3);
+            if (!fin) {
+                a.part[(int64_t)s0 * C::ITEMS + it] = v[y];
+            } else if (h < nh) {
+                const float4 t0 = js.tot[h], t1 = js.tot[h + 1];
+                const int64_t at = ((int64_t)sg.b * a.q_heads + qh0 + h) * D + (i >> 3) * 128 + 16 * (ln >> 2) + 2 * (i & 7);
+                f8_store2(a.out, at, t0.z == 0.f ? 0.f : v[y].x * t0.x * t0.y, t0.z == 0.f ? 0.f : v[y].z * t0.x * t0.y,
+                          a.out_dtype);
+                if (h + 1 < nh)
+                    f8_store2(a.out, at + D, t1.z == 0.f ? 0.f : v[y].y * t1.x * t1.y,
+                              t1.z == 0.f ? 0.f : v[y].w * t1.x * t1.y, a.out_dtype);
             }
         }
         if (!fin && tid < HEADS) a.meta[s0 * HEADS + tid] = js.tot[tid];
@@ -824,21 +853,20 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         int jn, j0, j1, st;  // sums to join: slots j0, then j1 + st, j1 + 2 st, ...
         uint32_t* cnt;
     };
-    auto step = [&](const F8Seg& sg, int x, bool fin, bool& single) {
-        const int v0 = (int)(x ? runs.start(run + 1) - sg.p1 : runs.start(run) - sg.p0);
-        const int c0 = (int)runs.owner(v0), c1 = (int)runs.owner(v0 + sg.np() - 1), n = c1 - c0 + 1;
-        const int first = 2 * c0 + ((int)runs.start(c0) >= v0 ? 0 : 1);  // slot of block c0; the others': 2 c
-        const int gi = ((int)run - c0) / kF8Join, g0 = c0 + gi * kF8Join;
+    auto step = [&](const F8Seg& sg, bool fin, bool& single) {
+        const int c0 = (int)runs.owner(sg.v0), c1 = (int)runs.owner(sg.v0 + sg.np() - 1), n = c1 - c0 + 1;
+        const int first = 2 * c0 + ((int)runs.start(c0) >= sg.v0 ? 0 : 1);  // slot of block c0; the others': 2 c
+        const int gi = ((int)run - c0) / kF8Group, g0 = c0 + gi * kF8Group;
         single = n <= kF8Join;
         Step s;
         if (single || fin) {
-            s.jn = single ? n : (n + kF8Join - 1) / kF8Join;
+            s.jn = single ? n : (n + kF8Group - 1) / kF8Group;
             s.j0 = first;
             s.j1 = 2 * c0;
-            s.st = single ? 2 : 2 * kF8Join;
+            s.st = single ? 2 : 2 * kF8Group;
             s.cnt = a.cnt + (int64_t)sg.b * nj + sg.j;
         } else {
-            s.jn = min(kF8Join, c1 - g0 + 1);
+            s.jn = min(kF8Group, c1 - g0 + 1);
             s.j0 = gi == 0 ? first : 2 * g0;
             s.j1 = 2 * g0;
             s.st = 2;
@@ -851,7 +879,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         bool single;
         s_last[warp][0] = 0;
         if (s_part[warp].b >= 0) {
-            const Step s = step(s_part[warp], warp, false, single);
+            const Step s = step(s_part[warp], false, single);
             s_last[warp][0] = arrive(s.cnt, s.jn);
         }
     }
@@ -860,10 +888,10 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         if (!s_last[x][0]) continue;
         const F8Seg sg = s_part[x];
         bool single;
-        Step s = step(sg, x, false, single);
+        Step s = step(sg, false, single);
         if (s.jn > 1) join(s.jn, s.j0, s.j1, s.st, single, sg);
         if (single) continue;
-        s = step(sg, x, true, single);
+        s = step(sg, true, single);
         if (tid == 0) s_last[x][1] = arrive(s.cnt, s.jn);
         __syncthreads();
         if (s_last[x][1]) join(s.jn, s.j0, s.j1, s.st, true, sg);
