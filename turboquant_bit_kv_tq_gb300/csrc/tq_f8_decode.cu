@@ -790,9 +790,15 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             }
             if (k0 == 0) {
                 // lane k: slot k
-                for (int h = warp; h < HEADS; h += W) {
-                    float4 m = make_float4(kF8None, kF8None, 0.f, 0.f);
-                    if (lane < count) m = __ldcg(a.meta + slot(lane) * HEADS + h);
+                float4 ms[HEADS / W];
+#pragma unroll
+                for (int y = 0; y < HEADS / W; ++y)
+                    ms[y] = lane < count ? __ldcg(a.meta + slot(lane) * HEADS + warp + y * W)
+                                         : make_float4(kF8None, kF8None, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < HEADS / W; ++y) {
+                    const int h = warp + y * W;
+                    const float4 m = ms[y];
                     const float R = warp_max(m.x), Rv = warp_max(m.y);
                     const float L = warp_sum(m.z * f8_exp2(m.x - R));
                     js.fac[lane][h] = f8_exp2(m.y - Rv);
