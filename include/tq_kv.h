@@ -425,7 +425,7 @@ typedef struct tq_f8_config {
     int64_t num_blocks;         /* blocks in the cache pool; num_blocks * H_kv < 2^31 */
     int32_t max_batch;          /* sequences per load or decode call */
     int32_t max_blocks_per_seq; /* columns of the block table;
-                                   max_batch * (max_blocks_per_seq + 8) * H_kv * ceil(G / 16) < 2^31 */
+                                   max_batch * (max_blocks_per_seq + 24) * H_kv * ceil(G / 16) < 2^31 */
 } tq_f8_config;
 
 typedef struct tq_f8_cache tq_f8_cache;

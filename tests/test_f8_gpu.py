@@ -252,6 +252,20 @@ def test_decode(d, hkv, g, lens, qt, ot):
     assert c.device_error() == 0
 
 
+@pytest.mark.parametrize("d,hkv,g,lens,qt,ot", [
+    (128, 1, 12, [20000, 3], "f32", "f32"),              # parts joined in groups
+    (256, 1, 16, [12000], "bf16", "bf16"),               # more parts than fit at a time
+    (256, 1, 4, [31, 6000, 1, 300], "f16", "f32"),
+    (128, 8, 4, [4000, 40, 0, 90, 17, 700, 64, 3000], "bf16", "bf16"),  # several units in a run
+    (128, 4, 2, [257] * 130, "bf16", "bf16"),            # more units than blocks, too long for a warp
+])
+def test_decode_many_parts_and_units(d, hkv, g, lens, qt, ot):
+    c, q, table = _decode_case(d, hkv, g, lens, qt, ot, 3 * d + hkv + g)
+    got = c.decode(q.cuda(), _gpu(table), _gpu(np.array(lens, np.int32)), out_dtype=DT[ot])
+    _check_decode(c, q, table, lens, ot, got)
+    assert c.device_error() == 0
+
+
 def test_decode_more_sequences_than_blocks():
     rng = _rng(6)
     lens = [int(x) for x in rng.integers(0, 90, 700)]

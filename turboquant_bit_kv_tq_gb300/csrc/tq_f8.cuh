@@ -9,7 +9,11 @@ namespace tq {
 // kF8MaxSms SMs; the workspace holds two partial sums for each block.
 constexpr int kF8Warps = 4, kF8Ctas = 3, kF8MaxSms = 160;
 constexpr int kF8Slots = 2 * kF8Ctas * kF8MaxSms;
-constexpr int kF8UnitCost = 8;  // places of the order that is dealt out a unit takes beside its pages
+// Places a unit takes beside its pages where pages are dealt out, at most: its start
+// and its sums take a block about as long as 8 (d = 128) to 16 (d = 256) pages.  With
+// 0, 4, 8, 16, 24, 32: 8 x up to 32768 tokens, d = 256: 81, 73, 68, 60, 59, 58 us;
+// 64 x up to 2000, d = 128: 56, 48, 37, 35, 34, 35 us.
+constexpr int kF8UnitCost = 24;
 
 // Query heads of one KV head that one work unit serves (nhg units per KV head
 // share its pages through L2 when G > 16), in n-tiles of 8 heads.

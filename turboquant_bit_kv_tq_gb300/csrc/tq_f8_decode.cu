@@ -130,8 +130,8 @@ __device__ __forceinline__ int f8_clamp(const F8DecodeArgs& a, int len) { return
 __device__ __forceinline__ int f8_pages(const F8DecodeArgs& a, int len) { return (f8_clamp(a, len) + 15) >> 4; }
 
 // A unit (a sequence's KV head and head group) costs more than its pages (its query,
-// its sums): in the order that is dealt out kF8UnitCost empty places follow its last.
-__device__ __forceinline__ int f8_places(int np) { return np > 0 ? np + kF8UnitCost : 0; }
+// its sums): in the order that is dealt out `cost` empty places follow its last.
+__device__ __forceinline__ int f8_places(int np, int cost) { return np > 0 ? np + cost : 0; }
 
 // A position in the order (sequence, KV head and head group, page) and the
 // places left of a run.
@@ -142,13 +142,13 @@ struct F8Seg {
     int b, j, p0, p1, len, v0;  // pages [p0, p1), none if the run has only empty places of the unit; v0: place of page 0
     __device__ __forceinline__ int np() const { return (len + 15) >> 4; }
 };
-__device__ __forceinline__ F8Seg f8_next(const F8DecodeArgs& a, F8Walk& w, int nj) {
+__device__ __forceinline__ F8Seg f8_next(const F8DecodeArgs& a, F8Walk& w, int nj, int cost) {
     F8Seg s;
     s.b = w.b;
     s.j = w.j;
     s.len = w.len;
     s.v0 = w.at - w.p;
-    const int np = s.np(), n = min(f8_places(np) - w.p, w.left);
+    const int np = s.np(), n = min(f8_places(np, cost) - w.p, w.left);
     s.p0 = min(w.p, np);
     s.p1 = min(w.p + n, np);
     w.left -= n;
@@ -230,20 +230,29 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         const int len = __ldg(a.lens + b);
         if (len < 0 || len > a.max_blocks * 16) set_error(a.err, TQ_DEVERR_SEQLEN);
         const int np = f8_pages(a, len);
-        mine += f8_places(np);
+        mine += np;
         some += np > 0;
         most = max(most, np);
     }
+    const int units = (int)__reduce_add_sync(0xffffffffu, (unsigned)some) * nj;
+    const int all_pages = (int)__reduce_add_sync(0xffffffffu, (unsigned)mine) * nj;
+    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+    // One run per block, of at least 16 pages on average (two steps for each
+    // warp); or, with more units than blocks and none much longer than a warp's
+    // share, a run of whole units per warp.
+    const int warps = (int)gridDim.x * W, share = all_pages / warps;
+    const bool solo = units > (int)gridDim.x && most <= max(kF8SoloPages, 2 * share);
+    // (a fixed cost, of less weight where the runs are short: the last of several runs
+    // of a unit would be left with few pages)
+    const int cost = min(kF8UnitCost, share);
+    mine += cost * some;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    const int before = (incl - mine) * nj;
-    const int total = __shfl_sync(0xffffffffu, incl, 31) * nj;
-    const int units = (int)__reduce_add_sync(0xffffffffu, (unsigned)some) * nj;
-    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+    const int before = (incl - mine) * nj, total = all_pages + cost * units;
     // sequences without a token: their rows are zero
     if (units < a.batch * nj)
         for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -252,14 +261,9 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                 f8_store2(a.out, (int64_t)b * a.q_heads * D + 2 * i, 0.f, 0.f, a.out_dtype);
         }
     if (total == 0) return;
-    // One run per block, of at least 16 pages on average (two steps for each
-    // warp); or, with more units than blocks and none much longer than a warp's
-    // share, a run of whole units per warp.
-    const int warps = (int)gridDim.x * W;
-    const bool solo = units > (int)gridDim.x && most <= max(kF8SoloPages, 2 * (total / warps));
     F8Runs runs;
     runs.n = solo ? (uint32_t)min(warps, total)
-                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, (total / units - kF8UnitCost) / 16));
+                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, all_pages / units / 16));
     runs.q = (uint32_t)total / runs.n;
     runs.r = (uint32_t)total - runs.q * runs.n;
     const uint32_t run = solo ? blockIdx.x * W + warp : blockIdx.x;
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             if (here)
                 for (;; ++b) {
                     len = __ldg(a.lens + b);
-                    const int n = f8_places(f8_pages(a, len)) * nj;
+                    const int n = f8_places(f8_pages(a, len), cost) * nj;
                     if (u < at + n) break;
                     at += n;
                 }
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             F8Walk w;
             w.b = __shfl_sync(0xffffffffu, b, src);
             w.len = f8_clamp(a, __shfl_sync(0xffffffffu, len, src));
-            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = f8_places((w.len + 15) >> 4);
+            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = f8_places((w.len + 15) >> 4, cost);
             w.j = rel / np;
             w.p = rel - w.j * np;
             w.left = total - u;
@@ -294,11 +298,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             // the units that start in [u0, u1)
             if (u1 < total) {
                 const F8Walk w = locate(u1);
-                if (w.p > 0) u1 += f8_places((w.len + 15) >> 4) - w.p;
+                if (w.p > 0) u1 += f8_places((w.len + 15) >> 4, cost) - w.p;
             }
             if (cons.p > 0) {
-                u0 += f8_places((cons.len + 15) >> 4) - cons.p;
-                f8_next(a, cons, nj);
+                u0 += f8_places((cons.len + 15) >> 4, cost) - cons.p;
+                f8_next(a, cons, nj, cost);
             }
         }
         cons.left = u1 - u0;
@@ -306,14 +310,14 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         F8Walk prod = cons;
 
         // ---- producer: this warp's steps, segment after segment
-        F8Seg ps = f8_next(a, prod, nj);
+        F8Seg ps = f8_next(a, prod, nj, cost);
         int pst = sw;
         int made = 0, used = 0;  // steps copied, steps taken
         int ids = -1, ids_at = 0, ids_n = 0;  // block ids of ids_n pages: this warp's steps from ids_at on
         auto produce = [&](int stage) {
             while (ps.p0 + pst * PP >= ps.p1) {
                 if (prod.left <= 0) return;
-                ps = f8_next(a, prod, nj);
+                ps = f8_next(a, prod, nj, cost);
                 pst = sw;
                 ids_n = 0;
             }
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
         int stage = 0;
 
         while (cons.left > 0) {
-            const F8Seg sg = f8_next(a, cons, nj);
+            const F8Seg sg = f8_next(a, cons, nj, cost);
             if (sg.p0 == sg.p1) continue;
             const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
             const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
