@@ -13,7 +13,9 @@ namespace tq {
 // memory: 2 (or 4) bytes in and 1 out per element.  A block takes consecutive
 // tokens of one KV head, whose rows lie side by side in a page; neighbouring
 // blocks take the other heads of the same tokens.  The vectors are loaded before
-// their slot is known, so that a block waits for memory once.
+// their slot is known, so that a block waits for memory once.  65536 tokens x 8 heads,
+// d = 128, bf16: 65 us, 6235 GB/s (92% of a plain copy's 6786); with the slot
+// loaded first and a block's warps on different heads it took 77.
 struct F8StoreArgs {
     const void *k, *v;
     int64_t k_stride, v_stride, n_tokens;  // strides in elements
@@ -144,7 +146,8 @@ static tq_status launch_f8_store(const F8StoreArgs& a, cudaStream_t s) {
 // -------------------------------------------------------------------- load
 // The pages of all sequences, in the order (sequence, page, KV head), are
 // dealt out to the warps of a fixed grid; a warp reads one page and writes its
-// 16 rows of keys and of values.  Bound by memory.
+// 16 rows of keys and of values.  Bound by memory: 16 sequences of up to 16384 tokens,
+// 8 heads, d = 128, to bf16: 135 us, 6118 GB/s (90% of a plain copy).
 struct F8LoadArgs {
     const uint8_t* cache;
     const int32_t *table, *lens, *cu;

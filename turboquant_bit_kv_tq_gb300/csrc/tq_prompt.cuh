@@ -32,6 +32,12 @@
 // an item covers a part of the keys only (`parts` of them); its unnormalised
 // output goes to the workspace and prompt_join_kernel adds the parts up.
 //
+// Measured (32/8 heads, causal, bf16; 2 d multiply-adds per visible pair): 1 x 8192,
+// d = 128: 375 us, 1467 TFLOP/s (cuBLAS: 1931 in a burst); 1 x 16384: 1549; 1 x 8192,
+// 32/4 heads, d = 256: 1530 to 1600; 16 prompts of up to 2048, d = 128: 219 us, 994 (an
+// item costs about 4.6 us beside its key tiles, whose masked halves do not count);
+// 96 rows after 16384 keys, d = 256: 49 us, 1060.
+//
 // Warps: 0-3 (and 4-7 at d = 128) softmax and output of query tile 0 (1), then
 // one for the copies (TMA), two that issue MMAs and an idle one that completes
 // the warpgroup of the register split.
@@ -900,7 +906,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 }
 
 // Parts of the keys: as many as shorten the longest run of a block, the join
-// (about 5 us) counted in.  The lengths are on the device; what the host knows is
+// (about 5 us) counted in (96 rows after 16384 keys, 24 items: 271 us in one part, 49
+// in six; 8192 rows are not cut).  The lengths are on the device; what the host knows is
 // the row counts.
 template <class C>
 int prompt_parts(const PromptArgs& a, int64_t items, int sms, int64_t part_rows) {
