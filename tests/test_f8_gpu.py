@@ -390,6 +390,26 @@ def test_decode_strided_queries_streams_and_graphs():
         _check_decode(c, wide[:, 5:13], table, n, "bf16", got)
 
 
+def test_decode_allocates_its_output_on_the_given_stream():
+    """A block that the current stream still writes to is not handed to a call on another stream."""
+    lens = [70, 33] * 60
+    c, q, table = _decode_case(128, 2, 4, lens, "bf16", "bf16", 41)
+    args = (q.cuda(), _gpu(table), _gpu(np.array(lens, np.int32)))
+    want = c.decode(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty_like(want) for _ in range(200)]  # every free block of this size
+    at = {x.data_ptr() for x in old}
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for x in old:
+        x.fill_(3)
+    del old, x
+    got = c.decode(*args, stream=side)
+    assert got.data_ptr() not in at
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_two_handles_on_two_streams():
     lens = [3000, 40]
     made = [_decode_case(128, 1, 4, lens, "bf16", "bf16", 20 + i) for i in range(2)]

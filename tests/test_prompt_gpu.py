@@ -302,6 +302,21 @@ def test_streams_graphs_and_no_lse():
         _check(q, k, v, lens, lens, True, out, None)
 
 
+def test_output_is_allocated_on_the_given_stream():
+    p, q, k, v, cq, ck = _case(128, 4, 2, [90, 30], [90, 30], "bf16", 17)
+    want = p.attention(q, k, v, cq, ck)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty_like(want) for _ in range(200)]  # every free block of this size
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for x in old:
+        x.fill_(3)
+    del old, x
+    got = p.attention(q, k, v, cq, ck, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("d,g", [(128, 4), (256, 8)])
 def test_chunked_prompt_through_the_cache_then_decode(d, g):
     """Two prompts in chunks: read the prefix back, attend, store the chunk; then decode steps."""

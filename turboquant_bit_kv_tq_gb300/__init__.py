@@ -582,6 +582,15 @@ def _launch_stream(stream, dev):
     return stream.cuda_stream
 
 
+def _output(q, dtype, stream):
+    """A tensor of q's shape for a call on `stream`, whose memory belongs to that
+    stream: of another's, an earlier use might still be under way there."""
+    if stream is None:
+        return _TORCH.empty(q.shape, dtype=dtype, device=q.device)
+    with _TORCH.cuda.stream(stream):
+        return _TORCH.empty(q.shape, dtype=dtype, device=q.device)
+
+
 def tq_f8_cache_sizes(cfg):
     vals = [ctypes.c_size_t() for _ in range(3)]
     _check(load_library().tq_f8_cache_sizes(ctypes.byref(cfg), *[ctypes.byref(v) for v in vals]), "tq_f8_cache_sizes")
@@ -703,7 +712,7 @@ class TQF8Cache:
 
     def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
         if out is None:
-            out = _TORCH.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+            out = _output(q, out_dtype or q.dtype, stream)
         tq_f8_decode_attention(self.handle, self.cfg, q, self.cache, block_table, seq_lens, out, scale, stream)
         return out
 
@@ -792,7 +801,7 @@ class TQPrompt:
         if q.get_device() != self.device.index:
             raise _wrong_device(q, "q", self.device.index)
         if out is None:
-            out = _TORCH.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _output(q, q.dtype, stream)
         tq_prompt_attention(self.handle, self.cfg, q, k, v, cu_q, cu_k, out, lse, causal, scale, stream)
         return out
 
