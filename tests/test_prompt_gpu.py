@@ -269,6 +269,33 @@ def test_values_a_row_does_not_see(d, g, lq, lk, dtype):
     assert p.device_error() == 0
 
 
+@pytest.mark.parametrize("d,g,h,lens,causal", [(128, 4, 4, [3000, 70, 1500], True), (256, 8, 3, [1300, 5, 900], True),
+                                               (128, 2, 8, [700, 33, 300, 1000], False), (128, 1, 16, [2500], True)])
+def test_rows_keep_their_bits_beside_values_that_are_not_finite(d, g, h, lens, causal):
+    """Several items per block; some have such values, at their end, in the middle, in the
+    last item of all: a row that sees none of its head is the same bit for bit, one that
+    sees one has it in its column and the same bits in the others."""
+    p, q, k, v, cq, ck = _case(d, g, h, lens, lens, "bf16", 19 + d + h)
+    ref, _ = _run(p, q, k, v, cq, ck, causal=causal)
+    rng = np.random.default_rng(d + h)
+    n = sum(lens)
+    bad = torch.zeros((n, h, d), dtype=torch.bool)
+    for key in [0, n // 3, n // 2 + 1, n - 2, n - 1] if not causal else [n // 3, n // 2 + 1, n - 200, n - 2, n - 1]:
+        bad[key, int(rng.integers(h)), int(rng.integers(d))] = True
+    bad = bad.cuda()
+    v2 = torch.where(bad, torch.tensor(float("inf"), dtype=v.dtype, device="cuda"), v)
+    out, _ = _run(p, q, k, v2, cq, ck, causal=causal)
+    sees = torch.zeros((n, h, d), dtype=torch.bool, device="cuda")  # [query row, KV head, column]
+    at = 0
+    for m in lens:
+        part = bad[at:at + m]
+        sees[at:at + m] = part.cumsum(0) > 0 if causal else part.any(0, keepdim=True)
+        at += m
+    sees = sees.repeat_interleave(g, 1)
+    assert torch.equal(out[~sees], ref[~sees])
+    assert not torch.isfinite(out[sees]).any() and sees.any()
+
+
 def test_bad_starts_are_reported_and_stay_inside():
     p, q, k, v, cq, ck = _case(128, 2, 1, [40, 50], [40, 50], "bf16", 15)
     for bad_q, bad_k in (([0, 40, 200], [0, 40, 90]), ([0, 60, 40], [0, 40, 90]), ([0, 40, 90], [-5, 40, 90]),
