@@ -1,4 +1,4 @@
-// The driver's tensor-map encoder, shared by the calls that use bulk tensor copies.
+// The CUDA driver's tensor-map encoder, shared by the calls that use bulk tensor copies.
 #pragma once
 
 #include <cuda.h>
