@@ -14,7 +14,7 @@ namespace tq {
 // tokens of one KV head, whose rows lie side by side in a page; neighbouring
 // blocks take the other heads of the same tokens.  The vectors are loaded before
 // their slot is known, so that a block waits for memory once.  65536 tokens x 8 heads,
-// d = 128, bf16: 65 us, 6235 GB/s (92% of a plain copy's 6786); with the slot
+// d = 128, bf16: 64 us, 6290 GB/s (93% of a plain copy's 6786); with the slot
 // loaded first and a block's warps on different heads it took 77.
 struct F8StoreArgs {
     const void *k, *v;
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kF8StoreThreads) f8_store_kernel(F8StoreArgs a
     const int sub = threadIdx.x % LPV;
     const int group = blockIdx.x / (unsigned)a.heads, h = blockIdx.x - (unsigned)group * a.heads;
     const int64_t t = (int64_t)group * (kF8StoreThreads / LPV) + threadIdx.x / LPV;
+    pdl_wait();  // (the launch overlaps the previous kernel's end)
     // whole warps stay for the shuffles; lanes of a vector share every decision
     F8Raw<DT> k = {}, v = {};
     int64_t slot = -1;
@@ -139,15 +140,14 @@ static tq_status launch_f8_store(const F8StoreArgs& a, cudaStream_t s) {
     constexpr int VPB = kF8StoreThreads / (D / 8);
     const int64_t blocks = (a.n_tokens + VPB - 1) / VPB * a.heads;
     if (blocks > 0x7FFFFFFF) return TQ_ERR_INVALID_ARG;
-    f8_store_kernel<D, DT><<<(unsigned)blocks, kF8StoreThreads, 0, s>>>(a);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(true, f8_store_kernel<D, DT>, dim3((unsigned)blocks), dim3(kF8StoreThreads), 0, s, a));
 }
 
 // -------------------------------------------------------------------- load
 // The pages of all sequences, in the order (sequence, page, KV head), are
 // dealt out to the warps of a fixed grid; a warp reads one page and writes its
 // 16 rows of keys and of values.  Bound by memory: 16 sequences of up to 16384 tokens,
-// 8 heads, d = 128, to bf16: 135 us, 6118 GB/s (90% of a plain copy).
+// 8 heads, d = 128, to bf16: 133 us, 6230 GB/s (92% of a plain copy).
 struct F8LoadArgs {
     const uint8_t* cache;
     const int32_t *table, *lens, *cu;
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kF8LoadThreads) f8_load_kernel(F8LoadArgs a) {
     const int64_t warps = (int64_t)gridDim.x * (kF8LoadThreads / 32);
     const int64_t w0 = (int64_t)blockIdx.x * (kF8LoadThreads / 32) + (threadIdx.x >> 5);
     const int cap = a.max_blocks * 16;
+    pdl_wait();  // (the launch overlaps the previous kernel's end)
     // the walk over the sequences is the same for every warp: warp w takes the
     // units w, w + warps, ... of the running count
     int64_t done = 0;  // units before sequence b
@@ -248,8 +249,7 @@ static tq_status launch_f8_load(const F8LoadArgs& a, cudaStream_t s) {
     if (st != TQ_OK) return st;
     const int64_t most = (int64_t)a.batch * a.max_blocks * a.heads;
     const int64_t blocks = std::min<int64_t>((most + 7) / 8, (int64_t)sms * 8);
-    f8_load_kernel<D, OT><<<(unsigned)blocks, kF8LoadThreads, 0, s>>>(a);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(true, f8_load_kernel<D, OT>, dim3((unsigned)blocks), dim3(kF8LoadThreads), 0, s, a));
 }
 
 static bool f8_dtype_ok(int t) { return t == TQ_DTYPE_F32 || t == TQ_DTYPE_BF16 || t == TQ_DTYPE_F16; }
