@@ -576,6 +576,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll 1
                 for (int h = 0; h < C::EN; ++h) {
                     const int r = ring + C::EN * C::value_pos(j, w.tiles()) + h, key0 = (w.j0 + j) * BN + h * C::VN;
+                    // A wait on `full` tells this load from the stage's last one only when
+                    // that one is known to be there.  The tile before this one, or the last
+                    // item's, says so; at d = 128 a query tile without keys in the last item
+                    // has waited for nothing in it.  What made the stage free for this load
+                    // does: both issuing threads had taken the load before.
+                    if (NQ == 2 && j == 0 && r >= S) prompt_wait(empty + 8 * (r % S), (r / S - 1) & 1, dead, err);
                     prompt_wait(full + 8 * (r % S), (r / S) & 1, dead, err);
                     uint8_t* v = smem + C::off_ring + (r % S) * C::KB;
                     // rows [r0, r1) to check, [r1, VN) to zero, in CH columns of 128
