@@ -49,3 +49,32 @@ def test_short_chunks_over_keys_between_short_prompts(g, causal):
             _check(q, k, v, lq, lk, causal, out, lse, skip=hurt)
             ref = out, lse
         assert torch.equal(out.nan_to_num(9.0, 9.0, 9.0), ref[0].nan_to_num(9.0, 9.0, 9.0)) and torch.equal(lse, ref[1])
+
+
+def _steps(d, g, dtype, rows, levels, seed):
+    """Rows over key tiles of 128 whose scores (scale 1) are levels[j] in tile j: one
+    element of q and k carries them."""
+    rng = np.random.default_rng((33, d, g, seed))
+    m = 128 * len(levels)
+    q = np.zeros((rows, g, d))
+    k = np.zeros((m, 1, d))
+    q[..., 0] = 1
+    k[..., 0] = np.repeat(levels, 128)[:, None]
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=g, dtype=DT[dtype], max_batch=1, max_tokens=rows)
+    return p, _gpu(q, DT[dtype]), _gpu(k, DT[dtype]), rng, _gpu(_starts([rows])), _gpu(_starts([m]))
+
+
+@pytest.mark.parametrize("d,g,rows", [(128, 4, 20), (128, 1, 200), (256, 4, 20), (256, 8, 50)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_reference_moves_twice_in_one_tile(d, g, rows, dtype):
+    """Tile 1 lies 12 (or 9) log2 units above tile 0: the reference follows in tile 2.
+    That one lies so far above that it is done again, and the reference moves a second
+    time.  Only tile 0 has values, so a lost factor shows whole."""
+    levels = [0, 8.5, 8.5 + 17] if dtype == "bf16" else [0, 6.25, 6.25 + 11]
+    p, q, k, rng, cq, ck = _steps(d, g, dtype, rows, levels, rows)
+    v = np.zeros((k.shape[0], 1, d))
+    v[:128] = rng.uniform(1, 2, (128, 1, d)) * 2.0 ** 14
+    v = _gpu(v, DT[dtype])
+    out, lse = _run(p, q, k, v, cq, ck, causal=False, scale=1.0)
+    assert p.device_error() == 0
+    _check(q, k, v, [rows], [k.shape[0]], False, out, lse, scale=1.0)

@@ -680,6 +680,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 float lj;
                 bool again = false;
                 do {
+                    // the first time's rescaled output and probabilities are there before the
+                    // output is read once more
+                    if (again) tc_wait_st();
                     // mx: the maximum up to the last tile (the first time), or up to this one
                     const bool move = (mx - m) * c > 8.f;  // also from -inf to the first score
                     if (__any_sync(0xffffffffu, move)) {
