@@ -78,3 +78,55 @@ def test_reference_moves_twice_in_one_tile(d, g, rows, dtype):
     out, lse = _run(p, q, k, v, cq, ck, causal=False, scale=1.0)
     assert p.device_error() == 0
     _check(q, k, v, [rows], [k.shape[0]], False, out, lse, scale=1.0)
+
+
+def _fill_shared_memory(d, x):
+    """Query tiles on every SM whose rows are x in element 0: what a later block finds in
+    rows of shared memory that it does not load."""
+    n = 256 * 152 * 2
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=1, max_batch=1, max_tokens=n)
+    q = torch.zeros((n, 1, d), device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = x
+    one = torch.zeros((1, 1, d), device="cuda", dtype=torch.bfloat16)
+    p.attention(q, one, one, _gpu(_starts([n])), _gpu(_starts([1])), causal=False)
+
+
+@pytest.mark.parametrize("d,g", [(128, 3), (128, 5), (128, 40), (256, 3), (256, 40)])
+def test_rows_that_no_token_has_do_not_steer_others(d, g):
+    """128 % g rows of a query tile are not loaded.  Every tile's scores lie about 10 log2
+    units above the last one's: a reference moves one tile late in every row, unless
+    another row of the warp asks for more."""
+    levels = [7.0 * j for j in range(6)]
+    rows = 128 // g
+    p, q, k, rng, cq, ck = _steps(d, g, "bf16", rows, levels, 34)
+    k[..., 1:] = _gpu(0.25 * rng.standard_normal((k.shape[0], 1, d - 1)), k.dtype)
+    q[..., 1:] = _gpu(0.25 * rng.standard_normal((rows, g, d - 1)), q.dtype)
+    v = _gpu(rng.standard_normal(k.shape), k.dtype)
+    outs = []
+    for x in (0.0, 5.0, -3.0, 20.0):
+        _fill_shared_memory(d, x)
+        outs.append(_run(p, q, k, v, cq, ck, causal=False, scale=1.0))
+    _check(q, k, v, [rows], [k.shape[0]], False, *outs[0], scale=1.0)
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("d,g", [(128, 4), (256, 2)])
+def test_queries_of_the_next_sequence_do_not_steer_a_row(d, g):
+    """The rows behind a sequence's last are the next one's queries."""
+    levels = [7.0 * j for j in range(6)]
+    rows, m = 70 // g, 768
+    p, q, k, rng, _, _ = _steps(d, g, "bf16", rows + 40, levels, 35)
+    k[..., 1:] = _gpu(0.25 * rng.standard_normal((m, 1, d - 1)), k.dtype)
+    q[:rows, :, 1:] = _gpu(0.25 * rng.standard_normal((rows, g, d - 1)), q.dtype)
+    k = torch.cat([k, k[:5]])
+    v = _gpu(rng.standard_normal(k.shape), k.dtype)
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=g, max_batch=2, max_tokens=rows + 40)
+    cq, ck = _gpu(_starts([rows, 40])), _gpu(_starts([m, 5]))
+    outs = []
+    for x in (0.0, 5.0, 20.0):
+        q[rows:, :, 0] = x
+        outs.append(_run(p, q, k, v, cq, ck, causal=False, scale=1.0))
+    _check(q, k, v, [rows, 40], [m, 5], False, *outs[-1], scale=1.0)
+    for out, lse in outs[1:]:
+        assert torch.equal(out[:rows], outs[0][0][:rows]) and torch.equal(lse[:rows], outs[0][1][:rows])

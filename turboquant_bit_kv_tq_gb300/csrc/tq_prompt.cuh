@@ -672,10 +672,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         xb = prompt_max3(xb, __uint_as_float(s[i][k + 2]), __uint_as_float(s[i][k + 3]));
                     }
                 };
+                // a tile row that no token of the sequence has (its queries are a neighbour's, or
+                // what shared memory held) has no say in what its warp does
+                auto row_max = [&]() { return live ? prompt_max3(mx, xa, xb) : -INFINITY; };
                 if (j == 0) {
 #pragma unroll
                     for (int i = 0; i < BN / 32; ++i) chunk_max(i);
-                    mx = fmaxf(xa, xb);
+                    mx = row_max();
                 }
                 float lj;
                 bool again = false;
@@ -747,7 +750,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     prompt_unpair(prompt_add2(la, lb), x0, x1);
                     lj = x0 + x1;
                     if (again) break;
-                    mx = prompt_max3(mx, xa, xb);
+                    mx = row_max();
                     again = __any_sync(0xffffffffu, (mx - m) * c > C::AHEAD_LOG2);
                 } while (again);
                 l += lj;
