@@ -554,7 +554,9 @@ tq_status tq_prompt_destroy(tq_prompt* p);
  *   cu_q/cu_k  device int32 [batch + 1], non-decreasing, within [0, n_q] and
  *              [0, n_k] (otherwise clamped, TQ_DEVERR_CHUNK, and the outputs of
  *              the sequences concerned are unspecified)
- *   scale      <= 0 means 1/sqrt(d)
+ *   scale      <= 0 means 1/sqrt(d).  <q, k> and scale <q, k> log2(e) lie within
+ *              fp32's range; however large within it, the weights are those
+ *              of the differences
  *   out        device [n_q][H_q][d], 16-byte aligned; lse device fp32
  *              [n_q][H_q] or NULL.  Rows no sequence names are left as they
  *              were.  Neither may overlap an input

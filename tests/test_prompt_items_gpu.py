@@ -130,3 +130,64 @@ def test_queries_of_the_next_sequence_do_not_steer_a_row(d, g):
     _check(q, k, v, [rows, 40], [m, 5], False, *outs[-1], scale=1.0)
     for out, lse in outs[1:]:
         assert torch.equal(out[:rows], outs[0][0][:rows]) and torch.equal(lse[:rows], outs[0][1][:rows])
+
+
+@pytest.mark.parametrize("d,g", [(128, 4), (256, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_scores_far_from_zero(d, g, dtype):
+    """Scores 2^20 .. 2^21 plus a few halves, all exact in fp32: the softmax is that of
+    the few halves.  Four tiles of small ones, then one key that weighs as much as they
+    do together, so that what the references leave behind counts."""
+    rows, m = 60, 768
+    rng = np.random.default_rng((36, d))
+    big = 2.0 ** 10 * (1 + rng.integers(0, 128, (rows, g)) / 128)
+    x = 0.5 * rng.integers(-2, 3, m)
+    x[530], x[700] = 6.5, 8.0
+    q, k = np.zeros((rows, g, d)), np.zeros((m, 1, d))
+    q[..., 1] = 1
+    k[:, 0, 1] = x
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=g, dtype=DT[dtype], max_batch=1, max_tokens=rows)
+    v = _gpu(rng.standard_normal(k.shape), DT[dtype])
+    near = _gpu(q, DT[dtype]), _gpu(k, DT[dtype])
+    q[..., 0] = big
+    k[..., 0] = 2.0 ** 10
+    for sign in (1, -1):
+        out, lse = _run(p, _gpu(sign * q, DT[dtype]), _gpu(sign * k if sign > 0 else np.where(np.arange(d) == 1, -k, k),
+                                                         DT[dtype]), v, _gpu(_starts([rows])), _gpu(_starts([m])),
+                        causal=False, scale=1.0)
+        assert p.device_error() == 0
+        _check(*near, v, [rows], [m], False, out, None, scale=1.0)
+        # lse: the large part and ln of a sum, one rounding of the size of the large part each
+        z = sign * big * 2.0 ** 10 + np.log(np.exp(x).sum())
+        assert (np.abs(lse.double().cpu().numpy() - z) <= 3 * 2.0 ** -23 * 2 ** 21).all()
+    # the first 300 keys far below: the references cross zero, then follow the few halves
+    k[:300, 0, 0] *= -1
+    out, _ = _run(p, _gpu(q, DT[dtype]), _gpu(k, DT[dtype]), v, _gpu(_starts([rows])), _gpu(_starts([m])), causal=False,
+                  scale=1.0)
+    _check(near[0], near[1][300:], v[300:], [rows], [m - 300], False, out, None, scale=1.0)
+
+
+@pytest.mark.parametrize("d,g,lq,causal", [(128, 4, 60, False), (256, 2, 60, False), (128, 1, 300, True), (256, 1, 300, True)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 2.0 ** 17), ("bf16", 2.0 ** 40), ("f16", 2.0 ** 13), ("f16", 2.0 ** 15)])
+def test_one_score_above_all_others(d, g, lq, causal, dtype, size):
+    """Scores of about size^2 (not a power of two), 0 and their negative: a row's output is
+    the mean of the values of its largest; a row that sees one key gets its value."""
+    rng = np.random.default_rng((37, d, lq))
+    m = 600 if not causal else lq
+    kind = rng.choice([-1.0, -1.0, 0.0, 1.0], m)
+    kind[:256] = np.minimum(kind[:256], 0)
+    kind[:3] = -1
+    q, k = np.zeros((lq, g, d)), np.zeros((m, 1, d))
+    q[..., 3] = size * 141 / 128
+    k[:, 0, 3] = kind * size * 159 / 128
+    v = _gpu(rng.standard_normal(k.shape), DT[dtype])
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=g, dtype=DT[dtype], max_batch=1, max_tokens=lq)
+    out, lse = _run(p, _gpu(q, DT[dtype]), _gpu(k, DT[dtype]), v, _gpu(_starts([lq])), _gpu(_starts([m])), causal=causal,
+                    scale=1.0)
+    assert p.device_error() == 0
+    # the same order with steps of 60: e^-60 is nothing beside the largest
+    q[..., 3], k[:, 0, 3] = 1, kind * 60
+    _check(_gpu(q, DT[dtype]), _gpu(k, DT[dtype]), v, [lq], [m], causal, out, None, scale=1.0)
+    top = np.array([kind[:i + 1].max() for i in range(lq)]) if causal else np.full(lq, kind.max())
+    z = top[:, None] * size * size * (141 / 128) * (159 / 128)
+    assert (np.abs(lse.double().cpu().numpy() - z) <= 2.0 ** -22 * np.abs(z) + 8).all()

@@ -24,7 +24,9 @@
 // rarely, and it moves a tile late: a tile's exponentials do not wait for its
 // maximum, unless that lies so far ahead that they might overflow (2^14 for fp16
 // probabilities, 2^20 for bf16), when they are done again.  That is exact, the
-// final quotient does not depend on m.
+// final quotient does not depend on m.  The argument is one fma, c s - (c m), with
+// c m rounded once per reference; where c m is so large that its rounding would
+// count (2^12, no trained model's scores), m is subtracted from the scores first.
 //
 // One block per SM takes items until none is left (the first by its index, the
 // next from a counter), longest first, so that the copies and score products of
@@ -82,6 +84,9 @@ struct PromptCfg {
     // how far (log2) a score may lie above the reference before a tile is done again:
     // the probabilities' range, with room for the sums
     static constexpr float AHEAD_LOG2 = BF16 ? 20.f : 14.f;
+    // from here on (log2) the rounding of c m would count: half a unit is 2^-13 here,
+    // against 2^-9 and 2^-12 of a probability's
+    static constexpr float FAR_LOG2 = 4096.f;
     // order of the tiles in the ring: AHEAD key tiles, then value tile 0, key tile AHEAD, value tile 1, ...
     static constexpr int AHEAD = NQ == 2 ? 1 : 2;
     static __host__ __device__ constexpr int key_pos(int j) { return j < AHEAD ? j : 2 * j - AHEAD + 1; }
@@ -643,8 +648,28 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                 __threadfence_block();
                 if (wrote || s_bad[it & 3] == it + 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
+            auto rescale = [&](int j, float f) {  // the output's sums, before tile j's
+                if (j == 0) return;
+                if constexpr (NQ == 1) {
+                    // the products of the tile before, of the other buffer
+                    const int pb = (j - 1) & 1;
+                    prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
+                    tc_fence_after();
+                }
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(so + i, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                    tmem_st32(so + i, o);
+                }
+            };
             float m = -INFINITY, l = 0.f, mx = -INFINITY;
-            for (int j = 0; j < nt; ++j) {
+            bool far = false;  // a row of the warp has a reference beyond FAR_LOG2
+            int j = 0;
+            for (; j < nt; ++j) {
                 const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
                 const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
                 // (while the scores are under way; at d = 256 the wait for the values
@@ -680,7 +705,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     for (int i = 0; i < BN / 32; ++i) chunk_max(i);
                     mx = row_max();
                 }
-                float lj;
+                float lj = 0.f;
                 bool again = false;
                 do {
                     // the first time's rescaled output and probabilities are there before the
@@ -692,23 +717,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                         const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
                         if (move) m = mx;
                         l *= f;
-                        if (j > 0) {
-                            if constexpr (NQ == 1) {
-                                // the products of the tile before, of the other buffer
-                                const int pb = (j - 1) & 1;
-                                prompt_wait(pvdone + 8 * pb, ((pb ? use1 : use0) + ((j - 1) >> 1)) & 1, dead, err);
-                                tc_fence_after();
-                            }
-#pragma unroll 1
-                            for (int i = 0; i < D; i += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(so + i, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                tmem_st32(so + i, o);
-                            }
-                        }
+                        rescale(j, f);
+                        far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m) * c > C::FAR_LOG2);
+                        if (far) break;
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
                     const uint64_t c2 = prompt_pair(c, c), mc2 = prompt_pair(-mc, -mc);
@@ -753,8 +764,65 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                     mx = row_max();
                     again = __any_sync(0xffffffffu, (mx - m) * c > C::AHEAD_LOG2);
                 } while (again);
+                if (far) {
+                    // the loop below takes over; it reads the scores once more
+                    if (again) {
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) tmem_st32(ss + 32 * i, s[i]);
+                    }
+                    tc_wait_st();
+                    break;
+                }
                 l += lj;
                 if (NQ == 1 && w.checked<BN>(j)) check(j);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready + 8 * buf);
+            }
+            // Scores this large: the reference is subtracted before they are scaled.  From the
+            // tile on in which the first such reference was taken, without the head start on
+            // the maximum and without haste: two passes over the scores in tensor memory.
+#pragma unroll 1
+            for (; j < nt; ++j) {
+                const int buf = NQ == 2 ? t : j & 1, use = (buf ? use1 : use0) + (NQ == 2 ? j : j >> 1);
+                const uint32_t ss = tmem + lanes + C::COL_S + buf * BN;
+                prompt_wait(sfull + 8 * buf, use & 1, dead, err);
+                tc_fence_after();
+                if (w.checked<BN>(j)) check(j);
+                const int cut = live ? lim - (w.j0 + j) * BN : 0;
+                uint32_t y[32], p[16];
+#pragma unroll 1
+                for (int i = 0; i < BN; i += 32) {
+                    tmem_ld32(ss + i, y);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (i + k < cut) mx = fmaxf(mx, __uint_as_float(y[k]));
+                }
+                const bool move = (mx - m) * c > 8.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = !move ? 1.f : m == -INFINITY ? 0.f : prompt_exp2((m - mx) * c);
+                    if (move) m = mx;
+                    l *= f;
+                    rescale(j, f);
+                }
+                const float by = m == -INFINITY ? 0.f : m;
+                float lj = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < BN; i += 32) {
+                    tmem_ld32(ss + i, y);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const float e0 = i + k < cut ? prompt_exp2((__uint_as_float(y[k]) - by) * c) : 0.f;
+                        const float e1 = i + k + 1 < cut ? prompt_exp2((__uint_as_float(y[k + 1]) - by) * c) : 0.f;
+                        lj += e0 + e1;
+                        p[k / 2] = prompt_pack<C::BF16>(e0, e1);
+                    }
+                    tmem_st16(ss + i / 2, p);
+                }
+                l += lj;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
