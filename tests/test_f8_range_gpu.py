@@ -1,0 +1,54 @@
+"""Decode over the 8-bit cache with scores far from zero, against the fp64 oracle."""
+
+import numpy as np
+import pytest
+
+from oracle import f8
+from test_f8_gpu import DT, _bound, _cache, _gpu, _np, _rng, _slots, _table
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _ranked(d, g, lens, kinds, size, qt, ot, seed, v_scales=(-12, 13)):
+    """Decode with scores kind * about size^2 (not a power of two; scale 1) and value
+    vectors of scales far apart: the mean of the values of a sequence's highest kind.
+    The oracle's scores are 60 times the kind: e^-60 is nothing beside the largest."""
+    rng = _rng(51, d, g, seed)
+    table, blocks = _table(rng, lens)
+    c = _cache(d, 1, g, blocks, len(lens), table.shape[1])
+    n = sum(lens)
+    kind = rng.choice(kinds, n)
+    q, k = np.zeros((len(lens), g, d)), np.zeros((n, 1, d))
+    q[..., 5] = size * 141 / 128
+    k[:, 0, 5] = kind * size * 1.25
+    v = rng.standard_normal((n, 1, d)) * 2.0 ** rng.integers(*v_scales, (n, 1, 1))
+    c.store(_gpu(k, torch.float32), _gpu(v, torch.float32), _gpu(_slots(table, lens)))
+    got = c.decode(_gpu(q, DT[qt]), _gpu(table), _gpu(np.array(lens, np.int32)), scale=1.0, out_dtype=DT[ot])
+    assert c.device_error() == 0
+    pages, gn = c.pages().cpu().numpy(), _np(got)
+    q[..., 5], k[:, 0, 5] = 1, kind * 60
+    at = 0
+    for b, m in enumerate(lens):
+        if m == 0:
+            assert not gn[b].any()
+            continue
+        _, vb = f8.rows(pages, table[b], m, d)
+        ref, _, mag = f8.attention(q[b:b + 1], k[at:at + m], vb, 1.0)
+        tol = _bound(q[b:b + 1], k[at:at + m], vb, 1.0, mag, ref, "f32" in (qt, ot), got.dtype)[0]
+        err = np.abs(gn[b] - ref[0])
+        assert (err <= tol).all(), (b, m, err.max(), (err / tol).max())
+        at += m
+
+
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 11, 2.0 ** 13, 2.0 ** 17, 2.0 ** 45])
+@pytest.mark.parametrize("d,g,lens,qt,ot", [
+    (128, 4, [1, 40, 300, 0, 17], "bf16", "bf16"),
+    (128, 8, [9000, 3], "f32", "f32"),
+    (256, 5, [2500, 33], "bf16", "f32"),
+    (256, 16, [200, 700], "bf16", "bf16"),
+    (128, 2, [60] * 700, "bf16", "bf16"),     # whole units to warps
+])
+def test_value_scales_beside_large_scores(d, g, lens, qt, ot, size):
+    for i, kinds in enumerate(([1.0], [-1.0], [-1, -1, -1, 0, 1.0])):
+        _ranked(d, g, lens, kinds, size, qt, ot, i)

@@ -32,7 +32,7 @@ inline F8Geom f8_geom(const tq_f8_config& c) {
 struct F8Workspace {
     // err: the error word; cnt: one counter per (sequence, KV head, head group);
     // gcnt: one per slot; part: [kF8Slots][d/16][nt][32][4] fp32 sums in
-    // fragment order; meta: [kF8Slots][8 nt] {r, r', l, -}
+    // fragment order; meta: [kF8Slots][8 nt] {r, x, l, -}
     size_t err, cnt, gcnt, zeroed, part, meta, total;
 };
 inline F8Workspace f8_workspace(const tq_f8_config& c) {

@@ -1,12 +1,14 @@
 // Decode attention over the 8-bit cache.
 //
 // With k8, v8 the codes, 2^ek, 2^ev the vectors' scales and c = scale * log2(e):
-//   s_t = c <q, k8_t> 2^ek_t             (log2 units)
-//   l   = sum_t 2^(s_t - r)              r, r': references of the sums, moved
-//   o   = sum_t 2^(s_t + ev_t - r') v8_t  when a score passes them by 2^12
-//   out = o / l * 2^(r' - r)
+//   s_t = c <q, k8_t> 2^ek_t                    (log2 units)
+//   l   = sum_t 2^(s_t - r)                     r, r + x: references of the sums, moved
+//   o   = sum_t 2^((s_t - r) + (ev_t - x)) v8_t  when a weight passes 2^12
+//   out = o / l * 2^x
 // The value scale goes into the exponent of the weight, with a reference of its
-// own, so no weight over- or underflows whatever the scales are.
+// own, so no weight over- or underflows whatever the scales are.  That one is held
+// by its distance x from r: both sums see the same difference s_t - r, exact near r
+// however large the scores are, and ev_t - x keeps every digit beside it.
 //
 // Bound by memory (2 d + 2 bytes per token and KV head).  All pages of all
 // sequences, in the order (sequence, KV head, page), are dealt out in runs to a
@@ -178,10 +180,10 @@ struct F8Runs {
     }
 };
 
-// 2^(r' - r) / l of a head's sums, as two factors: the power alone is subnormal
-// where the value scales are the smallest.  No token: 0
-__device__ __forceinline__ float2 f8_norm(float R, float Rv, float L) {
-    const float half = exp2f(0.5f * (Rv - R));
+// 2^x / l of a head's sums, as two factors: the power alone is subnormal where the
+// value scales are the smallest.  No token: 0
+__device__ __forceinline__ float2 f8_norm(float X, float L) {
+    const float half = exp2f(0.5f * X);
     return L == 0.f ? make_float2(0.f, 0.f) : make_float2(half / L, half);
 }
 
@@ -193,7 +195,7 @@ constexpr int kF8SoloPages = 16;  // a warp takes units of up to this many pages
 constexpr int kF8Join = 32, kF8Group = 16;
 struct F8JoinSmem {
     float fac[kF8Join][16];
-    float4 tot[16];  // {r, r', l, -} for another join, {f8_norm's factors, l, -} for the output
+    float4 tot[16];  // {r, x, l, -} for another join, {f8_norm's factors, l, -} for the output
 };
 static_assert(kF8Join <= 32 && kF8MaxSms * kF8Ctas / kF8Group + 1 <= kF8Join, "groups of a join");
 
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             }
 
             float o[D / 16][NT][4];
-            float r[NT][2], rv[NT][2], l[NT][2];
+            float r[NT][2], xv[NT][2], l[NT][2];
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) r[n][e] = rv[n][e] = kF8None, l[n][e] = 0.f;
+                for (int e = 0; e < 2; ++e) r[n][e] = kF8None, xv[n][e] = l[n][e] = 0.f;
 
             for (int p = sg.p0 + sw * PP; p < sg.p1; p += sn * PP) {
                 __syncwarp();  // the last step's stage (and qf) is settled
@@ -511,8 +513,8 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             for (int x = ACC - 2; x >= 0; --x) s[pp][n][i] += acc[x][pp][n][i];
                         }
 
-                // ---- weights.  p = 2^(x - r), w = 2^(x + ev - r') with x = score * ck
-                float ck[PP][2], ev[PP][2], pw[PP][NT][4], w[PP][NT][4], top = 0.f;
+                // ---- weights.  p = 2^(s - r), w = 2^((s - r) + (ev - x))
+                float ev[PP][2], pw[PP][NT][4], w[PP][NT][4], top = 0.f;
                 int nv[PP];
                 bool full = true;
 #pragma unroll
@@ -523,7 +525,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         // a vector stored as NaN has zero codes and E = 255: 0 * inf here
-                        ck[pp][u] = __uint_as_float((uint32_t)ex[tok + 8 * u] << 23);
+                        const float ck = __uint_as_float((uint32_t)ex[tok + 8 * u] << 23);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) s[pp][n][2 * u + e] = __fmul_rn(s[pp][n][2 * u + e], ck * cqr[n][e]);
                         const uint32_t eb = ex[16 + tok + 8 * u];
                         ev[pp][u] = eb == 255u ? __uint_as_float(0x7FC00000u)
                                                : __uint_as_float(0x4B000000u | eb) - (8388608.f + 127.f);
@@ -538,9 +544,11 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const float x = s[pp][n][2 * u + e], f = ck[pp][u] * cqr[n][e];
-                                    pw[pp][n][2 * u + e] = f8_exp2(fmaf(x, f, -r[n][e]));
-                                    w[pp][n][2 * u + e] = f8_exp2(fmaf(x, f, ev[pp][u] - rv[n][e]));
+                                    // (a product and a difference, not one fma: the largest
+                                    // score is 0 away from itself)
+                                    const float x = __fsub_rn(s[pp][n][2 * u + e], r[n][e]);
+                                    pw[pp][n][2 * u + e] = f8_exp2(x);
+                                    w[pp][n][2 * u + e] = f8_exp2(x + (ev[pp][u] - xv[n][e]));
                                 }
                     if (!full) {
 #pragma unroll
@@ -565,26 +573,29 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float m = r[n][e], mv = rv[n][e] + kF8Head;
+                            float m = r[n][e];
 #pragma unroll
                             for (int pp = 0; pp < PP; ++pp)
 #pragma unroll
                                 for (int u = 0; u < 2; ++u)
-                                    if (tok + 8 * u < nv[pp]) {
-                                        const float x = s[pp][n][2 * u + e] * (ck[pp][u] * cqr[n][e]);
-                                        m = fmaxf(m, x);
-                                        mv = fmaxf(mv, x + ev[pp][u]);
-                                    }
+                                    if (tok + 8 * u < nv[pp]) m = fmaxf(m, s[pp][n][2 * u + e]);
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 4));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 8));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            const float was = (r[n][e] - m) + xv[n][e];  // the old r + x, from m
+                            float mv = was + kF8Head;
+#pragma unroll
+                            for (int pp = 0; pp < PP; ++pp)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u)
+                                    if (tok + 8 * u < nv[pp]) mv = fmaxf(mv, (s[pp][n][2 * u + e] - m) + ev[pp][u]);
+                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 4));
+                            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 8));
                             mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 16)) - kF8Head;
-                            const float fv = f8_exp2(rv[n][e] - mv);
+                            const float fv = f8_exp2(was - mv);
                             l[n][e] *= f8_exp2(r[n][e] - m);
                             r[n][e] = m;
-                            rv[n][e] = mv;
+                            xv[n][e] = mv;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) o[i][n][e] *= fv, o[i][n][2 + e] *= fv;
                         }
@@ -675,27 +686,29 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            s_ref[warp][8 * n + 2 * c + e] = make_float4(r[n][e], rv[n][e], l[n][e], 0.f);
+                            s_ref[warp][8 * n + 2 * c + e] = make_float4(r[n][e], xv[n][e], l[n][e], 0.f);
                 __syncthreads();
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float R = kF8None, Rv = kF8None, L = 0.f;
+                        float R = kF8None, X = -INFINITY, L = 0.f;
                         float4 m[W];
 #pragma unroll
                         for (int w = 0; w < W; ++w) {
                             m[w] = s_ref[w][8 * n + 2 * c + e];
                             R = fmaxf(R, m[w].x);
-                            Rv = fmaxf(Rv, m[w].y);
                         }
 #pragma unroll
-                        for (int w = 0; w < W; ++w) L += m[w].z * f8_exp2(m[w].x - R);
-                        const float f = f8_exp2(rv[n][e] - Rv);
+                        for (int w = 0; w < W; ++w) {
+                            X = fmaxf(X, (m[w].x - R) + m[w].y);
+                            L += m[w].z * f8_exp2(m[w].x - R);
+                        }
+                        const float f = f8_exp2(((r[n][e] - R) + xv[n][e]) - X);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) o[i][n][e] *= f, o[i][n][2 + e] *= f;
                         r[n][e] = R;
-                        rv[n][e] = Rv;
+                        xv[n][e] = X;
                         l[n][e] = L;
                     }
                 auto put = [&](int at) {
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int h = 8 * n + 2 * c + e;
-                        const float2 f = f8_norm(r[n][e], rv[n][e], l[n][e]);
+                        const float2 f = f8_norm(xv[n][e], l[n][e]);
                         if (h < nh)
 #pragma unroll
                             for (int i0 = 0; i0 < D / 16; i0 += 8) {
@@ -760,7 +773,7 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            a.meta[slot * HEADS + 8 * n + 2 * c + e] = make_float4(r[n][e], rv[n][e], l[n][e], 0.f);
+                            a.meta[slot * HEADS + 8 * n + 2 * c + e] = make_float4(r[n][e], xv[n][e], l[n][e], 0.f);
                 if (lane == 0) s_part[which] = sg;
             }
             __syncwarp();  // qf is free
@@ -805,16 +818,16 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                 for (int y = 0; y < HEADS / W; ++y)
                     ms[y] = lane < count ? __ldcg(a.meta + slot(lane) * HEADS + warp + y * W)
-                                         : make_float4(kF8None, kF8None, 0.f, 0.f);
+                                         : make_float4(kF8None, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < HEADS / W; ++y) {
                     const int h = warp + y * W;
                     const float4 m = ms[y];
-                    const float R = warp_max(m.x), Rv = warp_max(m.y);
+                    const float R = warp_max(m.x), at = (m.x - R) + m.y, X = warp_max(at);
                     const float L = warp_sum(m.z * f8_exp2(m.x - R));
-                    js.fac[lane][h] = f8_exp2(m.y - Rv);
-                    const float2 f = f8_norm(R, Rv, L);
-                    if (lane == 0) js.tot[h] = fin ? make_float4(f.x, f.y, L, 0.f) : make_float4(R, Rv, L, 0.f);
+                    js.fac[lane][h] = f8_exp2(at - X);
+                    const float2 f = f8_norm(X, L);
+                    if (lane == 0) js.tot[h] = fin ? make_float4(f.x, f.y, L, 0.f) : make_float4(R, X, L, 0.f);
                 }
                 __syncthreads();  // the factors
             }
