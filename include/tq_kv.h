@@ -496,7 +496,8 @@ tq_status tq_f8_load(const tq_f8_cache* cache, const void* cache_buf, const int3
  *   out      device [batch][H_q][d], out_dtype (F32, BF16, F16)
  *   block_table, seq_lens as for tq_f8_load; a block id outside
  *            [0, num_blocks) is skipped (TQ_DEVERR_BLOCK)
- *   scale    softmax scale; <= 0 means 1/sqrt(d)
+ *   scale    softmax scale; <= 0 means 1/sqrt(d).  The scores times log2(e), and
+ *            scale * max|q| * max|k|, lie within fp32's range
  * The products run on 16-bit operands that hold the codes exactly.  With
  * 16-bit q and out the probabilities are rounded to fp16 once; where q or out
  * is F32 both q and the probabilities go in as two fp16 parts (~22 bits).

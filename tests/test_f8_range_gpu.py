@@ -52,3 +52,17 @@ def _ranked(d, g, lens, kinds, size, qt, ot, seed, v_scales=(-12, 13)):
 def test_value_scales_beside_large_scores(d, g, lens, qt, ot, size):
     for i, kinds in enumerate(([1.0], [-1.0], [-1, -1, -1, 0, 1.0])):
         _ranked(d, g, lens, kinds, size, qt, ot, i)
+
+
+@pytest.mark.parametrize("size", [2.0 ** 51, 2.0 ** 60, 1.375 * 2.0 ** 62])
+@pytest.mark.parametrize("d,g,lens,qt,ot", [
+    (128, 4, [1, 40, 300, 0, 17], "bf16", "bf16"),
+    (128, 8, [9000, 3], "f32", "f32"),
+    (256, 16, [1, 700], "bf16", "f32"),
+    (128, 2, [60] * 700, "bf16", "bf16"),
+])
+def test_scores_down_to_the_end_of_the_range(d, g, lens, qt, ot, size):
+    """Every score of a sequence far below zero (2^102 .. 2^125): its values, not those of
+    a sequence without a token."""
+    for i, kinds in enumerate(([-1.0], [-1, -1, -0.25])):
+        _ranked(d, g, lens, kinds, size, qt, ot, 10 + i)

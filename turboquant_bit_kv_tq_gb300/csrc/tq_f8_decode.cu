@@ -62,8 +62,9 @@ constexpr int kF8Threads = 32 * kF8Warps;
 // weights are kept below kF8Most and the reference is set so that the largest
 // is 2^kF8Head: small weights stay normal fp16 numbers further down
 constexpr float kF8Most = 4096.f, kF8Head = 4.f;
-// the reference of an empty sum; any score is far above it
-constexpr float kF8None = -1e30f;
+// the reference of an empty sum: no finite score lies below it, and any other is so
+// far above (a unit of the last place is 2^104) that its weight moves the reference
+constexpr float kF8None = -3.4028234664e38f;
 
 __device__ __forceinline__ float f8_exp2(float x) {
     float r;
