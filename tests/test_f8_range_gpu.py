@@ -66,3 +66,29 @@ def test_scores_down_to_the_end_of_the_range(d, g, lens, qt, ot, size):
     a sequence without a token."""
     for i, kinds in enumerate(([-1.0], [-1, -1, -0.25])):
         _ranked(d, g, lens, kinds, size, qt, ot, 10 + i)
+
+
+@pytest.mark.parametrize("d,g,qt,ot", [(128, 4, "f32", "f32"), (128, 16, "bf16", "bf16"), (256, 8, "bf16", "f32")])
+def test_exponent_byte_zero(d, g, qt, ot):
+    """Pages that something else filled: the byte 0 is 2^-127 for keys, too."""
+    rng = _rng(52, d, g)
+    lens = [70, 5, 400]
+    table, blocks = _table(rng, lens)
+    c = _cache(d, 1, g, blocks, len(lens), table.shape[1])
+    n = sum(lens)
+    k, v = rng.standard_normal((n, 1, d)), rng.standard_normal((n, 1, d))
+    slots = _slots(table, lens)
+    c.store(_gpu(k, torch.float32), _gpu(v, torch.float32), _gpu(slots))
+    host = c.pages().cpu().numpy()
+    f8.parts(host, d)[2][slots // 16, 0, slots % 16] = rng.integers(0, 3, n)
+    c.pages().copy_(_gpu(host))
+    q = torch.from_numpy(rng.standard_normal((len(lens), g, d)) * 2.0 ** 121).to(DT[qt])
+    got = c.decode(q.cuda(), _gpu(table), _gpu(np.array(lens, np.int32)), out_dtype=DT[ot])
+    assert c.device_error() == 0
+    for b, m in enumerate(lens):
+        kb, vb = f8.rows(host, table[b], m, d)
+        args = _np(q)[b:b + 1], kb, vb, 1 / np.sqrt(d)
+        ref, _, mag = f8.attention(*args)
+        tol = _bound(*args, mag, ref, "f32" in (qt, ot), got.dtype)[0]
+        err = np.abs(_np(got)[b] - ref[0])
+        assert (err <= tol).all(), (b, err.max(), (err / tol).max())

@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         // a vector stored as NaN has zero codes and E = 255: 0 * inf here
-                        const float ck = __uint_as_float((uint32_t)ex[tok + 8 * u] << 23);
+                        // (0 stands for 2^-127, a subnormal)
+                        const float ck = __uint_as_float(max((uint32_t)ex[tok + 8 * u] << 23, 0x00400000u));
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
