@@ -92,3 +92,30 @@ def test_exponent_byte_zero(d, g, qt, ot):
         tol = _bound(*args, mag, ref, "f32" in (qt, ot), got.dtype)[0]
         err = np.abs(_np(got)[b] - ref[0])
         assert (err <= tol).all(), (b, err.max(), (err / tol).max())
+
+
+@pytest.mark.parametrize("d,hkv,g", [(128, 8, 1), (256, 4, 2), (128, 4, 12)])
+def test_long_sums_are_rounded_not_cut_off(d, hkv, g):
+    """fp32, positive values, many steps per warp: the outputs are right on average.
+    What is rounded to nearest leaves no mean error; a tensor-core product may lose up to
+    2^-23 of its own sum, and at most four are added up before the next rounding."""
+    rng = _rng(53, d, g)
+    lens = [40000, 39999]
+    table, blocks = _table(rng, lens)
+    c = _cache(d, hkv, hkv * g, blocks, 2, table.shape[1])
+    n = sum(lens)
+    gen = torch.Generator("cuda").manual_seed(53)
+    k = torch.randn((n, hkv, d), generator=gen, device="cuda")
+    v = torch.rand((n, hkv, d), generator=gen, device="cuda") + 0.5
+    c.store(k, v, _gpu(_slots(table, lens)))
+    q = torch.randn((2, hkv * g, d), generator=gen, device="cuda")
+    got = _np(c.decode(q, _gpu(table), _gpu(np.array(lens, np.int32))))
+    assert c.device_error() == 0
+    pages = c.pages().cpu().numpy()
+    for b, m in enumerate(lens):
+        kb, vb = f8.rows(pages, table[b], m, d)
+        ref, _, mag = f8.attention(_np(q)[b:b + 1], kb, vb, 1 / np.sqrt(d))
+        tol = _bound(_np(q)[b:b + 1], kb, vb, 1 / np.sqrt(d), mag, ref, True, torch.float32)[0]
+        assert (np.abs(got[b] - ref[0]) <= tol).all()
+        mean = ((got[b] - ref[0]) / ref[0]).mean()
+        assert abs(mean) <= 4 * 2.0 ** -23, (b, mean)
