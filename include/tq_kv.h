@@ -499,8 +499,10 @@ tq_status tq_f8_load(const tq_f8_cache* cache, const void* cache_buf, const int3
  *   scale    softmax scale; <= 0 means 1/sqrt(d).  The scores times log2(e), and
  *            scale * max|q| * max|k|, lie within fp32's range
  * The products run on 16-bit operands that hold the codes exactly.  With
- * 16-bit q and out the probabilities are rounded to fp16 once; where q or out
- * is F32 both q and the probabilities go in as two fp16 parts (~22 bits).
+ * 16-bit q and out the probabilities, times their values' scales, are rounded
+ * to fp16 once; where q or out is F32 both q and they go in as two fp16 parts
+ * (~22 bits).  Steps are at least 2^-28 of a head's largest: what lies below
+ * half of one counts as 0.
  * A query with an infinity or a NaN gets NaN.  1 <= batch <= max_batch.  One
  * launch of a fixed grid: the caches' pages are dealt out evenly whatever the
  * lengths, and the last block to finish a (sequence, KV head) joins its parts

@@ -191,3 +191,42 @@ def test_one_score_above_all_others(d, g, lq, causal, dtype, size):
     top = np.array([kind[:i + 1].max() for i in range(lq)]) if causal else np.full(lq, kind.max())
     z = top[:, None] * size * size * (141 / 128) * (159 / 128)
     assert (np.abs(lse.double().cpu().numpy() - z) <= 2.0 ** -22 * np.abs(z) + 8).all()
+
+
+@pytest.mark.parametrize("d,g", [(128, 4), (256, 8)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 2.0 ** 30), ("f16", 2.0 ** 14)])
+def test_large_scores_in_key_parts(d, g, dtype, size):
+    """Few rows over many keys: parts with scores of size^2, of its negative and of small
+    size, a few warps of them in the loop for large ones; captured and replayed."""
+    rng = np.random.default_rng((38, d))
+    lq, m = 20, 4500
+    kind = np.full(m, -1.0)
+    kind[1000:2500] = rng.choice([0.0, 1e-9], 1500)
+    kind[3000:] = rng.choice([-1.0, 0.0], m - 3000)
+    at = rng.choice(m, 3, replace=False)
+    kind[at] = 1
+    q, k = np.zeros((lq, g, d)), np.zeros((m, 1, d))
+    q[..., 3] = size * 141 / 128
+    q[10:] *= -1
+    k[:, 0, 3] = kind * size * 159 / 128
+    v = _gpu(rng.standard_normal(k.shape), DT[dtype])
+    p = tq.TQPrompt(head_dim=d, num_kv_heads=1, num_q_heads=g, dtype=DT[dtype], max_batch=1, max_tokens=lq)
+    args = _gpu(q, DT[dtype]), _gpu(k, DT[dtype]), v, _gpu(_starts([lq])), _gpu(_starts([m]))
+    out, lse = _run(p, *args, causal=False, scale=1.0)
+    assert p.device_error() == 0
+    # the largest: kind 1, and for the negated queries kind -1
+    top = np.where(np.arange(lq)[:, None] < 10, kind == 1, kind == -1)
+    for i in (0, 10):
+        near = np.zeros((10, g, d)), np.zeros((m, 1, d))
+        near[0][..., 0] = 1
+        near[1][:, 0, 0] = np.where(top[i], 0, -60)
+        _check(_gpu(near[0], DT[dtype]), _gpu(near[1], DT[dtype]), v, [10], [m], False, out[i:i + 10], None, scale=1.0)
+    graph = torch.cuda.CUDAGraph()
+    again = torch.zeros_like(out)
+    with torch.cuda.graph(graph):
+        p.attention(*args, out=again, causal=False, scale=1.0)
+    for _ in range(2):
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, out)

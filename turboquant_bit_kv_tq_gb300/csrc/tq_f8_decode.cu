@@ -32,10 +32,11 @@
 // block to arrive, in groups first where there are many.
 //
 // Measured: 16 x 8192 tokens, 32/8 heads, d = 128: 55 us, 4.9 TB/s; 4 x up to 131072,
-// 64/8 heads: 123 us, 5.5 TB/s; 8 x up to 32768, 32/4 heads, d = 256, fp32: 59 us,
+// 64/8 heads: 121 us, 5.6 TB/s; 8 x up to 32768, 32/4 heads, d = 256, fp32: 58 us,
 // 5.1 TB/s (a plain copy: 6.8).  Longer caches add bytes at 6.3 to 6.7 TB/s; the rest
-// is about 15 us a call: the first pages are under way after 2.5 us and there after 4,
-// blocks with equal runs end within 9 us, arriving takes 2 and the last join 5.
+// is about 15 us a call: the first pages are under way after 3 us; of 16 x 8192, blocks
+// with equal runs end between 35 and 47 us (four fifths of them between 39 and 45),
+// arriving takes 1.5 and the last join up to 5.
 
 #include <algorithm>
 
@@ -370,8 +371,10 @@ __global__ void __launch_bounds__(kF8Threads, F8Cfg<D, NT, PREC>::CTAS) f8_decod
             const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
             const int qh0 = kvh * a.group + hg * a.hp;
 
-            // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9)
-            // (exact for bf16 and fp16 inputs), in fragment order
+            // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9), in
+            // fragment order.  Exact for fp16 elements down to 2^-22 of the head's largest
+            // and bf16 ones down to 2^-25; below, they are rounded to steps of at most 2^-32
+            // of it, which is less than the fp32 score's rounding
             float cqr[NT][2];
             constexpr int QB = HEADS * D <= 8 * 128 ? 8 : 4;  // heads loaded at once
             const int64_t qoff = (int64_t)sg.b * a.q_stride + (int64_t)qh0 * D + 4 * lane;
@@ -1039,8 +1042,8 @@ extern "C" tq_status tq_f8_decode_attention(const tq_f8_cache* c, const void* q,
     a.hp = c->geom.hp;
     a.max_blocks = c->cfg.max_blocks_per_seq;
     // fp32 in or out: query and weights in two fp16 parts.  Up to 8 heads a unit that
-    // costs nothing (8 x 20480 tokens: 64 us either way); with 16, 75 us for 63 at d =
-    // 128 and 97 for 67 at d = 256 (16 x 8192), so 16-bit calls do without.
+    // costs nothing (8 x 20480 tokens: 63 us, 64 without); with 16, 74 us for 63 at d =
+    // 128 and 96 for 62 at d = 256 (16 x 8192), so 16-bit calls do without.
     const bool prec = q_dtype == TQ_DTYPE_F32 || out_dtype == TQ_DTYPE_F32;
     cudaStream_t s = (cudaStream_t)stream;
     return d == 128 ? dispatch_f8_decode<128>(a, c->geom.nt, prec, s) : dispatch_f8_decode<256>(a, c->geom.nt, prec, s);

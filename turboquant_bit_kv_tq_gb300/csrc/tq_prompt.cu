@@ -27,8 +27,10 @@ static tq_status prompt_check(const tq_prompt_config& c) {
 }
 
 // The workspace: error word and item counters (256 bytes), then the sums and
-// {m, l} of part_rows rows.  A call is cut into parts only while its blocks fit
-// two waves of kPromptSms SMs with 128 (d = 256) or 256 (d = 128) rows each.
+// {m, l} of part_rows rows: what two waves of kPromptSms blocks with full items (128
+// rows at d = 256, 256 at d = 128) can write, or 16 parts of the most rows if that is
+// less.  A call is cut into z parts only while z times its rows fit (prompt_parts);
+// items that are not full can be more than two waves of blocks.
 constexpr int kPromptSms = 160;
 static int64_t prompt_part_rows(const tq_prompt_config& c) {
     const int64_t all = (int64_t)kPromptParts * c.max_tokens * c.num_q_heads;

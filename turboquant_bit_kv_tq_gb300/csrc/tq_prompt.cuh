@@ -35,10 +35,11 @@
 // output goes to the workspace and prompt_join_kernel adds the parts up.
 //
 // Measured (32/8 heads, causal, bf16; 2 d multiply-adds per visible pair): 1 x 8192,
-// d = 128: 375 us, 1467 TFLOP/s (cuBLAS: 1931 in a burst); 1 x 16384: 1549; 1 x 8192,
-// 32/4 heads, d = 256: 1530 to 1600; 16 prompts of up to 2048, d = 128: 219 us, 994 (an
-// item costs about 4.6 us beside its key tiles, whose masked halves do not count);
-// 96 rows after 16384 keys, d = 256: 49 us, 1060.
+// d = 128: 366 us, 1502 TFLOP/s (cuBLAS: 1931 in a burst); 1 x 16384: 1602; 1 x 8192,
+// 32/4 heads, d = 256: 1555 to 1600; 16 prompts of up to 2048, d = 128: 218 us, 998 (an
+// item of 1, 2, 4, 8, 16 key tiles takes 6.2, 8.4, 12.4, 19.2, 32.0 us: 1.6 a tile, and
+// 4.6 or more beside them; masked halves of tiles do not count); 96 rows after 16384
+// keys, d = 256: 48 us, 1070.
 //
 // Warps: 0-3 (and 4-7 at d = 128) softmax and output of query tile 0 (1), then
 // one for the copies (TMA), two that issue MMAs and an idle one that completes
@@ -986,7 +987,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 }
 
 // Parts of the keys: as many as shorten the longest run of a block, the join
-// (about 5 us) counted in (96 rows after 16384 keys, 24 items: 271 us in one part, 49
+// (about 5 us) counted in (96 rows after 16384 keys, 24 items: 271 us in one part, 48
 // in six; 8192 rows are not cut).  The lengths are on the device; what the host knows is
 // the row counts.
 template <class C>
