@@ -81,7 +81,7 @@ enum {
     TQ_ERR_MISALIGNED = -5        /* a device pointer is not 16-byte aligned */
 };
 
-/* TQ_DTYPE_F16: the 8-bit cache and prompt attention calls only. */
+/* TQ_DTYPE_F16: the calls of the 8-bit and 4-bit caches, prompt attention and norm with rotation only. */
 enum { TQ_DTYPE_F32 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F16 = 2 };
 /*
  * Decode output flag, OR-ed into out_dtype: with MSE-quantised values, return
@@ -110,7 +110,8 @@ enum {
     TQ_DEVERR_SEQLEN = 1u << 2,    /* decode: seq_len < 0 or > 16*max_blocks_per_seq; clamped */
     TQ_DEVERR_TAIL = 1u << 3,      /* decode: tail_len < 0 or > tail_cap; clamped */
     TQ_DEVERR_TIMEOUT = 1u << 4,   /* a bounded wait (2^24 polls) on a staged tile or an MMA gave up; work abandoned */
-    TQ_DEVERR_CHUNK = 1u << 5      /* extend: a token row outside every sequence's chunk (cu_q); its output is 0 */
+    TQ_DEVERR_CHUNK = 1u << 5,     /* extend: a token row outside every sequence's chunk (cu_q); its output is 0 */
+    TQ_DEVERR_POOL = 1u << 6       /* plan: the list of free blocks ran out; the tokens behind it get no slot */
 };
 
 typedef struct tq_cache_config {
@@ -573,6 +574,204 @@ tq_status tq_prompt_attention(const tq_prompt* p, const void* q, const void* k, 
 
 /* Read and clear the handle's device error word, like tq_get_device_error. */
 tq_status tq_prompt_get_device_error(const tq_prompt* p, uint32_t* flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit cache: plain 4-bit integers with one scale for 16 elements, beside
+ * TurboQuant's rotated codebooks: any group size, three dtypes, a store without a
+ * rotation, rows that can be read back.  The pages have no counterpart.
+ *
+ * Same paging again, [num_blocks][num_kv_heads][page_bytes], a page holding 16
+ * tokens of one KV head, all arrays token by token:
+ *   K codes   16 x d/2   byte j of a token: elements 2j (low half) and 2j + 1
+ *   V codes   16 x d/2
+ *   K scales  16 x d/16  scale byte u of elements 16 i .. 16 i + 15
+ *   V scales  16 x d/16
+ *   K exps    16         exponent byte E of the vector
+ *   V exps    16         (E = 255: the vector is NaN)
+ * page_bytes = 18 d + 32: 4.56 bits an element at d = 128.  Code n under u and E
+ * stands for (n - 8) S(u) 2^(E - 127), where S(u) is the fp16 number with the
+ * bits u << 7: five bits of exponent, three behind the point.  S(u) <= 32, u <=
+ * 160: larger scale bytes are not read back right.  The store writes n = 1 .. 15
+ * and E = 1 .. 248 and 255.
+ * ------------------------------------------------------------------------ */
+typedef struct tq_i4_config {
+    int32_t head_dim;           /* d, 128 or 256 */
+    int32_t num_kv_heads;       /* H_kv >= 1 */
+    int32_t num_q_heads;        /* H_q = G * H_kv, any G >= 1; q head h reads KV head h / G */
+    int32_t block_size;         /* tokens per cache block; must be 16 */
+    int64_t num_blocks;         /* blocks in the cache pool; num_blocks * H_kv < 2^31 */
+    int32_t max_batch;          /* sequences per load or decode call */
+    int32_t max_blocks_per_seq; /* columns of the block table;
+                                   max_batch * (max_blocks_per_seq + 24) * H_kv * ceil(G / 16) < 2^31 */
+} tq_i4_config;
+
+typedef struct tq_i4_cache tq_i4_cache;
+
+/* Sizes, in bytes, of the caller-owned device buffers; any pointer may be NULL. */
+tq_status tq_i4_cache_sizes(const tq_i4_config* cfg, size_t* page_bytes, size_t* cache_bytes,
+                            size_t* workspace_bytes);
+
+/* Make and release a handle, as tq_f8_cache_create and tq_f8_cache_destroy: one handle = one workspace. */
+tq_status tq_i4_cache_create(const tq_i4_config* cfg, void* workspace_dev, void* stream, tq_i4_cache** out);
+tq_status tq_i4_cache_destroy(tq_i4_cache* cache);
+
+/*
+ * Quantise new vectors into the 4-bit cache.  For every token t with
+ * slot_mapping[t] >= 0, every KV head and both k and v:
+ *   a = max_i |x_i|;  E = the smallest integer >= 1 with a <= 240 * 2^(E - 127);
+ *   y = x * 2^(127 - E); for each 16 elements g = max |y|, and u = 0 if g <= 2^-18,
+ *   else the smallest u >= 1 with g <= 7.5 S(u): the finest scale that leaves no
+ *   element more than half a step from its code;
+ *   n = clamp(round(y / S(u)), -7, 7) + 8, ties to even; 8 where u = 0.
+ * Each decision is that of exact arithmetic, whatever in_dtype is.  A vector with
+ * an infinity or a NaN is stored as E = 255 with zero scales and codes 8.
+ * Arguments, skipped slots and errors as for tq_f8_store.
+ */
+tq_status tq_i4_store(const tq_i4_cache* cache, const void* k, const void* v, int in_dtype, int64_t k_stride,
+                      int64_t v_stride, int64_t num_tokens, const int64_t* slot_mapping, void* cache_buf,
+                      void* stream);
+
+/*
+ * Read sequences of the 4-bit cache back into packed rows (tq_prompt_attention
+ * over a stored prefix), rounded once to out_dtype; as tq_f8_load.
+ */
+tq_status tq_i4_load(const tq_i4_cache* cache, const void* cache_buf, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* cu_out, int batch, int64_t n_rows, void* k_out,
+                     void* v_out, int out_dtype, void* stream);
+
+/*
+ * Decode attention over the 4-bit cache, one new query per sequence: arguments,
+ * definition, limits and order of the sums as for tq_f8_decode_attention.  The
+ * products run on 16-bit operands that hold code times scale exactly.
+ */
+tq_status tq_i4_decode_attention(const tq_i4_cache* cache, const void* q, int q_dtype, int64_t q_stride,
+                                 const void* cache_buf, const int32_t* block_table, const int32_t* seq_lens,
+                                 float scale, int batch, void* out, int out_dtype, void* stream);
+
+/* Read and clear the handle's device error word, like tq_get_device_error. */
+tq_status tq_i4_get_device_error(const tq_i4_cache* cache, uint32_t* flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norm of query and key heads with the rotation of positions, one pass over the
+ * rows of a projection, before prompt or decode attention and the store.  The
+ * pages have no counterpart.
+ * ------------------------------------------------------------------------ */
+typedef struct tq_norm_rope_config {
+    int32_t head_dim;     /* d, 128 or 256 */
+    int32_t num_kv_heads; /* H_kv >= 1 */
+    int32_t num_q_heads;  /* H_q >= 1 */
+    int32_t rot_dim;      /* the first rot_dim elements of a head are rotated: a multiple of 16, 0 .. d */
+    int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    int32_t norm;         /* 1: norm, then rotation; 0: rotation alone */
+    float eps;            /* of the norm, >= 0 */
+    double base;          /* > 0; pair i turns by base^(-2 i / rot_dim) a position, unless inv_freq is given */
+} tq_norm_rope_config;
+
+typedef struct tq_norm_rope_plan tq_norm_rope_plan;
+
+/* Bytes of the caller-owned device workspace of a configuration. */
+tq_status tq_norm_rope_sizes(const tq_norm_rope_config* cfg, size_t* workspace_bytes);
+
+/*
+ * Make a handle that records workspace_dev (>= workspace_bytes, 16-byte aligned)
+ * and writes the turns per position of its pairs there.  inv_freq: host double
+ * [rot_dim / 2], radians per position (scaled variants), or NULL for the powers
+ * of cfg->base.  Synchronises `stream` (set-up only).  Calls of one handle may
+ * overlap on the GPU: nothing but the error word is written.
+ */
+tq_status tq_norm_rope_create(const tq_norm_rope_config* cfg, const double* inv_freq, void* workspace_dev,
+                              void* stream, tq_norm_rope_plan** out);
+tq_status tq_norm_rope_destroy(tq_norm_rope_plan* plan);
+
+/*
+ * For token t and each head x of q and k:
+ *   y = x / sqrt(mean_i x_i^2 + eps) * w   (norm; w = q_weight or k_weight, or 1)
+ *   (a, b) -> (a cos p - b sin p, b cos p + a sin p) for each pair of the first
+ *   rot_dim elements, p = positions[t] * inv_freq of the pair,
+ * in fp32, rounded once to dtype.  The angle is reduced exactly, in 64-bit turns,
+ * so that far positions keep their digits.  Heads of v are moved as they are.
+ *   q, k, v    device [num_tokens][heads][d], dtype (F32, BF16, F16); row t starts
+ *              the stride's elements after row t - 1.  v may be NULL (with v_out)
+ *   q_weight, k_weight  device [d], w_dtype, or NULL
+ *   positions  device int32 [num_tokens], any value
+ *   kv_rows    device int32 [num_tokens] or NULL: the rows of k_out and v_out that
+ *              token t's k and v go to (NULL: row t).  -1 leaves them out; any other
+ *              row outside [0, num_kv_rows) does, too, and sets TQ_DEVERR_CHUNK.  Rows
+ *              of one call must differ
+ *   q_out      [num_tokens][H_q][d]; k_out, v_out [num_kv_rows][H_kv][d], at least
+ *              num_tokens rows without kv_rows.  q_out may be q with its stride and, without
+ *              kv_rows, k_out may be k and v_out v; no other overlap
+ * Bases and strides: multiples of 16 bytes.  Rows no token names are left as they
+ * were.  num_tokens == 0 is a no-op.
+ */
+tq_status tq_norm_rope(const tq_norm_rope_plan* plan, const void* q, const void* k, const void* v, int dtype,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
+                       const void* k_weight, int w_dtype, const int32_t* positions, const int32_t* kv_rows,
+                       int64_t num_tokens, int64_t num_kv_rows, void* q_out, void* k_out, void* v_out,
+                       int64_t q_out_stride, int64_t k_out_stride, int64_t v_out_stride, void* stream);
+
+/* Read and clear the handle's device error word, like tq_get_device_error. */
+tq_status tq_norm_rope_get_device_error(const tq_norm_rope_plan* plan, uint32_t* flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The plan of a step: block-table entries, slots, positions and row starts of the
+ * new tokens of a batch, made on the GPU from the requests' lengths and a list of
+ * free blocks, for the caches', prompt attention's and norm-and-rotation's calls.
+ * The pages have no counterpart.
+ * ------------------------------------------------------------------------ */
+typedef struct tq_plan_config {
+    int32_t max_batch;          /* requests per call, 1 .. 8192 */
+    int32_t max_blocks_per_seq; /* columns of the block table; max_batch * max_blocks_per_seq * 16 < 2^31 */
+} tq_plan_config;
+
+typedef struct tq_plan tq_plan;
+
+/* Bytes of the caller-owned device workspace of a configuration. */
+tq_status tq_plan_sizes(const tq_plan_config* cfg, size_t* workspace_bytes);
+
+/*
+ * Make a handle that records workspace_dev (>= workspace_bytes, 16-byte aligned);
+ * synchronises `stream` once (set-up only).  As with the caches, calls and captured
+ * graphs of one handle must not overlap on the GPU.
+ */
+tq_status tq_plan_create(const tq_plan_config* cfg, void* workspace_dev, void* stream, tq_plan** out);
+tq_status tq_plan_destroy(tq_plan* plan);
+
+/*
+ * Request b has L = lens[b] tokens stored in ceil(L / 16) blocks of its row of the
+ * table, and n = new_lens[b] new ones (1 each where new_lens is NULL).
+ *   blocks   the ceil((L + n) / 16) - ceil(L / 16) blocks it still needs are taken from
+ *            free_blocks, request by request from entry *next_free on, and written
+ *            to its row of the table
+ *   tokens   packed, request by request: token i of request b is row cu_q[b] + i, with
+ *            position L + i, slot table[b][(L + i) / 16] * 16 + (L + i) % 16, and row
+ *            cu_k[b] + L + i of packed keys (tq_f8_load's and tq_norm_rope's rows,
+ *            tq_prompt_attention's cu_k)
+ *   lengths  seq_lens[b] = L + n; cu_q, cu_k [batch + 1]: sums of n and of seq_lens;
+ *            *next_free_out = *next_free + the blocks taken
+ * lens, new_lens   device int32 [batch]
+ * free_blocks      device int32 [num_free]; ids are passed on unchecked, but a
+ *                  token whose block id is negative gets slot -1
+ * block_table      device int32 [batch][max_blocks_per_seq], other entries left as they were
+ * slot_mapping     device int64 [num_tokens]; positions, kv_rows device int32
+ *                  [num_tokens].  Rows behind the last token (a padded batch) get slot
+ *                  -1, position 0 and row -1: the calls above skip them
+ * seq_lens may be lens and next_free_out next_free: a captured step can be
+ * replayed.  No other overlap.
+ * What does not fit is left out, and a request's length grows by its tokens with a
+ * slot only: beyond its row of the table (TQ_DEVERR_SEQLEN), beyond the list
+ * (TQ_DEVERR_POOL), beyond num_tokens (TQ_DEVERR_CHUNK, cu_q cut off there).  Such
+ * tokens get slot -1 and row -1.  lens outside [0, 16 max_blocks_per_seq] and negative
+ * new_lens are clamped (TQ_DEVERR_SEQLEN), *next_free to [0, num_free] (TQ_DEVERR_POOL).
+ * 1 <= batch <= max_batch; 0 <= num_tokens, num_free < 2^31.  One launch.
+ */
+tq_status tq_plan_step(const tq_plan* plan, const int32_t* lens, const int32_t* new_lens, int batch,
+                       const int32_t* free_blocks, int64_t num_free, const int32_t* next_free, int32_t* block_table,
+                       int64_t num_tokens, int64_t* slot_mapping, int32_t* positions, int32_t* kv_rows,
+                       int32_t* seq_lens, int32_t* cu_q, int32_t* cu_k, int32_t* next_free_out, void* stream);
+
+/* Read and clear the handle's device error word, like tq_get_device_error. */
+tq_status tq_plan_get_device_error(const tq_plan* plan, uint32_t* flags, void* stream);
 
 #ifdef __cplusplus
 }

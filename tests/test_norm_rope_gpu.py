@@ -1,0 +1,245 @@
+"""Norm with rotation on the GPU against its fp64 oracle (oracle/serve.py).
+
+The bound.  The norm's factor: squares and their sum round at most 20 times (16 in
+a lane, 4 or 5 exchanges) by 2^-24 of a sum of positive terms, half of which
+reaches the root; rsqrt errs by 2^-22; with the products by it and by the weight an
+element is off by at most 2^-24 (10 + 4 + 2) = 2^-20 of itself.  The angle is cut
+off to 2^-32 of a turn (2^-29) and rounded to 2^-25 of half a turn (2^-23); sine
+and cosine err by 2^-22 at most: together 2^-21.  The two products of a rotation
+add 2^-23.  So 2^-19.3 of |a| + |b|, the elements of the pair; then half a step of
+the output's type."""
+
+import numpy as np
+import pytest
+
+import turboquant_bit_kv_tq_gb300 as tq
+from oracle import serve
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _gpu(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def _check(got, x, w, pos, f, eps, interleaved=False, norm=True):
+    want, size = serve.norm_rope(_np(x), None if w is None else _np(w), pos, f, eps, interleaved, norm)
+    fin = torch.finfo(got.dtype)
+    # (a subnormal of the type rounds by half its step, a result beyond it to an infinity)
+    tol = 2.0 ** -19.3 * size + np.maximum(fin.eps / 2 * np.abs(want), fin.smallest_normal * fin.eps / 2) + 2.0 ** -149
+    g = _np(got)
+    assert np.isfinite(g).all()
+    err = np.abs(g - want)
+    assert (err <= tol).all(), (err.max(), (err / tol).max())
+
+
+def _inputs(seed, n, hq, hk, d, dtype, wt=None, gain=1.0):
+    rng = np.random.default_rng((81, seed))
+    made = [_gpu(rng.standard_normal((n, h, d)) * gain * np.exp(rng.uniform(-3, 3, (n, h, 1))), DT[dtype])
+            for h in (hq, hk, hk)]
+    w = [_gpu(1 + 0.2 * rng.standard_normal(d), DT[wt or dtype]) for _ in range(2)]
+    pos = rng.integers(-50, 1 << 20, n).astype(np.int32)
+    return made, w, pos
+
+
+@pytest.mark.parametrize("n,hq,hk,d,rot,dtype,wt,interleaved", [
+    (1, 32, 8, 128, 128, "bf16", "bf16", False),
+    (1, 1, 1, 128, 128, "f32", "f32", True),
+    (37, 5, 1, 128, 64, "f16", "f32", False),
+    (16, 8, 2, 256, 256, "bf16", "f32", False),
+    (19, 3, 3, 256, 96, "f32", "bf16", True),
+    (50, 4, 4, 128, 16, "bf16", "f16", False),
+    (33, 2, 1, 256, 16, "f16", "f16", True),
+    (9, 7, 2, 128, 0, "bf16", "bf16", False),
+    (700, 32, 8, 128, 128, "bf16", "bf16", True),
+    (1500, 12, 4, 256, 64, "f32", "f32", False),
+    (5000, 3, 1, 128, 96, "bf16", "bf16", False),
+    (2000, 64, 8, 128, 128, "bf16", "bf16", False),
+    (3, 300, 2, 128, 128, "bf16", "bf16", False),
+])
+def test_norm_and_rotation(n, hq, hk, d, rot, dtype, wt, interleaved):
+    (q, k, v), (wq, wk), pos = _inputs(n + hq, n, hq, hk, d, dtype, wt)
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk, rot_dim=rot, base=5e5, interleaved=interleaved)
+    f = serve.powers(5e5, rot) if rot else np.zeros(0)
+    qo, ko = h.apply(q, k, _gpu(pos), wq, wk)
+    some = np.arange(n) if n < 60 else np.r_[0:20, n // 2:n // 2 + 9, n - 20:n]
+    at = _gpu(some)
+    eps = float(np.float32(1e-6))
+    _check(qo[at], q[at], wq, pos[some], f, eps, interleaved)
+    _check(ko[at], k[at], wk, pos[some], f, eps, interleaved)
+    # keys and values to rows of longer buffers, some left out; other rows stay
+    rng = np.random.default_rng((82, n))
+    rows = rng.permutation(2 * n + 1)[:n].astype(np.int32)
+    rows[::5] = -1
+    long = [torch.full((2 * n + 1, hk, d), -7.0, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    out = h.apply(q, k, _gpu(pos), wq, wk, k_out=long[0], v=v, v_out=long[1], kv_rows=_gpu(rows))
+    assert out[1] is long[0] and out[2] is long[1] and torch.equal(out[0], qo)
+    want = [torch.full_like(long[0], -7.0) for _ in range(2)]
+    live = _gpu(np.flatnonzero(rows >= 0))
+    want[0][_gpu(rows[rows >= 0]).long()], want[1][_gpu(rows[rows >= 0]).long()] = ko[live], v[live]
+    assert torch.equal(long[0], want[0]) and torch.equal(long[1], want[1])
+    assert h.device_error() == 0
+
+
+def test_far_positions_and_given_frequencies():
+    rng = np.random.default_rng(83)
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1234567890, 10 ** 6 + 1, -77], np.int32)
+    f = np.r_[rng.uniform(0, 3, 58), 6.5, 100.25, 1e-9, 0.0, -0.3, 2.0 ** 40 + 0.125]
+    q, k = _gpu(rng.standard_normal((8, 2, 128)), torch.float32), _gpu(rng.standard_normal((8, 1, 128)), torch.float32)
+    for interleaved in (False, True):
+        h = tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=1, inv_freq=f, interleaved=interleaved)
+        qo, ko = h.apply(q, k, _gpu(pos))
+        _check(qo, q, None, pos, f, float(np.float32(1e-6)), interleaved)
+        _check(ko, k, None, pos, f, float(np.float32(1e-6)), interleaved)
+
+
+def test_rotation_alone_and_one_weight():
+    (q, k, _), (wq, _), pos = _inputs(5, 21, 4, 2, 128, "bf16")
+    f = serve.powers(1e4, 128)
+    h = tq.TQNormRope(head_dim=128, num_q_heads=4, num_kv_heads=2, norm=0)
+    qo, ko = h.apply(q, k, _gpu(pos), wq)  # (weights are the norm's)
+    _check(qo, q, None, pos, f, 0.0, norm=False)
+    _check(ko, k, None, pos, f, 0.0, norm=False)
+    h = tq.TQNormRope(head_dim=128, num_q_heads=4, num_kv_heads=2, eps=1e-3)
+    qo, ko = h.apply(q, k, _gpu(pos), q_weight=wq)
+    _check(qo, q, wq, pos, f, float(np.float32(1e-3)))
+    _check(ko, k, None, pos, f, float(np.float32(1e-3)))
+
+
+@pytest.mark.parametrize("dtype,gains", [("f32", (2.0 ** 100, 2.0 ** 120, 2.0 ** -70, 2.0 ** -120, 2.0 ** -135)),
+                                         ("bf16", (2.0 ** 100, 2.0 ** 120, 2.0 ** -70, 2.0 ** -120)),
+                                         ("f16", (2.0 ** 9, 2.0 ** -9))])
+@pytest.mark.parametrize("d", [128, 256])
+def test_squares_beyond_the_range(dtype, gains, d):
+    """Elements whose squares over- or underflow, beside an ordinary eps, a tiny one and none."""
+    pos = np.arange(6, dtype=np.int32)
+    f = serve.powers(1e4, d)
+    for gain in gains:
+        for eps in (1e-6, 1e-35, 0.0):
+            (q, k, _), (wq, wk), _ = _inputs(6, 6, 2, 1, d, dtype, gain=gain)
+            q[2] = 0 if eps else q[1]
+            h = tq.TQNormRope(head_dim=d, num_q_heads=2, num_kv_heads=1, eps=eps)
+            qo, ko = h.apply(q, k, _gpu(pos), wq, wk)
+            _check(qo, q, wq, pos, f, float(np.float32(eps)))
+            _check(ko, k, wk, pos, f, float(np.float32(eps)))
+
+
+def test_what_is_not_finite_stays_in_its_head():
+    (q, k, _), (wq, wk), pos = _inputs(7, 9, 4, 2, 128, "bf16")
+    h = tq.TQNormRope(head_dim=128, num_q_heads=4, num_kv_heads=2, rot_dim=64)
+    clean = h.apply(q, k, _gpu(pos), wq, wk)
+    q[3, 1, 5], k[4, 0, 100] = float("nan"), float("inf")
+    got = h.apply(q, k, _gpu(pos), wq, wk)
+    assert torch.isnan(got[0][3, 1]).all() and torch.isnan(got[1][4, 0, 100])
+    for a, b, (t, hd) in ((got[0], clean[0], (3, 1)), (got[1], clean[1], (4, 0))):
+        a[t, hd], b[t, hd] = 0, 0
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,dtype,interleaved", [(128, "bf16", False), (256, "f32", True)])
+def test_rows_of_a_projection_in_place_streams_and_graphs(d, dtype, interleaved):
+    n, hq, hk = 45, 6, 2
+    (q, k, v), (wq, wk), pos = _inputs(8, n, hq, hk, d, dtype)
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk, interleaved=interleaved)
+    p = _gpu(pos)
+    want = h.apply(q, k, p, wq, wk)
+    qkv = torch.cat([q, k, v], 1)
+    a, b, c = qkv.split([hq, hk, hk], 1)
+    got = h.apply(a, b, p, wq, wk)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    keep = qkv.clone()
+    h.apply(a, b, p, wq, wk, q_out=a, k_out=b)
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, v)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = h.apply(q, k, p, wq, wk, v=v, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.apply(a, b, p, wq, wk, q_out=a, k_out=b)
+    for _ in range(2):
+        qkv.copy_(keep)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, v)
+
+
+def test_outputs_are_allocated_on_the_given_stream():
+    (q, k, _), (wq, wk), pos = _inputs(9, 60, 4, 4, 128, "bf16")
+    h = tq.TQNormRope(head_dim=128, num_q_heads=4, num_kv_heads=4)
+    p = _gpu(pos)
+    want = h.apply(q, k, p, wq, wk)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty_like(q) for _ in range(200)]  # every free block of this size
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for x in old:
+        x.fill_(3)
+    del old, x
+    got = h.apply(q, k, p, wq, wk, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_outside_are_left_out_and_reported():
+    (q, k, v), (wq, wk), pos = _inputs(10, 6, 2, 1, 128, "bf16")
+    h = tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=1)
+    ko, vo = (torch.full((4, 1, 128), -7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rows = np.array([3, -1, 4, -2, 0, 2 ** 31 - 1], np.int32)
+    h.apply(q, k, _gpu(pos), wq, wk, k_out=ko, v=v, v_out=vo, kv_rows=_gpu(rows))
+    assert h.device_error() == tq.TQ_DEVERR_CHUNK and h.device_error() == 0
+    assert torch.equal(vo[3], v[0]) and torch.equal(vo[0], v[4]) and (vo[1:3] == -7).all() and (ko[1:3] == -7).all()
+    h.apply(q[:0], k[:0], _gpu(pos[:0]), wq, wk)  # no token: nothing
+
+
+def test_many_vectors():
+    """More vectors than 2^31 elements of output offsets."""
+    n, hq, hk, d = 70000, 250, 1, 128
+    q = torch.randn((1, hq, d), device="cuda").to(torch.bfloat16).expand(n, hq, d).contiguous()
+    k = torch.randn((n, hk, d), device="cuda").to(torch.bfloat16)
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk)
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    h.apply(q, k, pos, q_out=q)
+    assert torch.equal(q[0], q[-1]) and torch.equal(q[0], q[n // 2 + 1]) and bool((q == q[:1]).all())
+    _check(q[:1], q[:1], None, [0], serve.powers(1e4, 128), 0.0, norm=True)
+
+
+def test_refusals():
+    (q, k, v), (wq, wk), pos = _inputs(11, 6, 2, 1, 128, "bf16")
+    h = tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=1)
+    p = _gpu(pos)
+    for error, call in [
+        (TypeError, lambda: h.apply(q.half(), k, p)),
+        (TypeError, lambda: h.apply(q, k, p, wq, wk.float())),
+        (TypeError, lambda: h.apply(q, k, p.long())),
+        (TypeError, lambda: h.apply(q, k, p, wq.int())),
+        (ValueError, lambda: h.apply(q, k[:5], p)),
+        (ValueError, lambda: h.apply(q, k, p[:5])),
+        (ValueError, lambda: h.apply(q[:, :1], k, p)),
+        (ValueError, lambda: h.apply(q, k, p, wq[:64])),
+        (ValueError, lambda: h.apply(q, k, p, q_out=q[:3])),
+        (ValueError, lambda: h.apply(q, k, p, k_out=torch.cat([k, k]))),
+        (ValueError, lambda: h.apply(q, k, p, kv_rows=p)),
+        (ValueError, lambda: h.apply(q, k, p, v=v[:4])),
+        (ValueError, lambda: h.apply(q, k, p, v_out=v)),
+        (ValueError, lambda: h.apply(q.cpu(), k, p)),
+        (ValueError, lambda: h.apply(q, k, p.cpu())),
+    ]:
+        with pytest.raises(error):
+            call()
+    odd = torch.zeros(6 * 2 * 128 + 8, dtype=torch.bfloat16, device="cuda")[1:-7].view(6, 2, 128)
+    with pytest.raises(tq.TQError) as e:
+        h.apply(odd, k, p)
+    assert e.value.status == -5
+    with pytest.raises(tq.TQError) as e:
+        tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=1, inv_freq=np.full(64, np.nan))
+    assert e.value.status == -1

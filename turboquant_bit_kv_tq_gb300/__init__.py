@@ -26,7 +26,13 @@ __all__ = [
     "TQ_DTYPE_F16", "tq_f8_config", "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store",
     "tq_f8_load", "tq_f8_decode_attention", "tq_f8_get_device_error", "TQF8Cache",
     "tq_prompt_config", "tq_prompt_sizes", "tq_prompt_create", "tq_prompt_destroy", "tq_prompt_attention",
-    "tq_prompt_get_device_error", "TQPrompt",
+    "tq_prompt_get_device_error", "TQPrompt", "TQ_DEVERR_POOL",
+    "tq_i4_config", "tq_i4_cache_sizes", "tq_i4_cache_create", "tq_i4_cache_destroy", "tq_i4_store", "tq_i4_load",
+    "tq_i4_decode_attention", "tq_i4_get_device_error", "TQI4Cache",
+    "tq_norm_rope_config", "tq_norm_rope_sizes", "tq_norm_rope_create", "tq_norm_rope_destroy", "tq_norm_rope",
+    "tq_norm_rope_get_device_error", "TQNormRope",
+    "tq_plan_config", "tq_plan_sizes", "tq_plan_create", "tq_plan_destroy", "tq_plan_step",
+    "tq_plan_get_device_error", "TQPlan", "TQPlanStep",
 ]
 
 TQ_DTYPE_F32, TQ_DTYPE_BF16, TQ_DTYPE_F16 = 0, 1, 2
@@ -34,7 +40,7 @@ TQ_OUT_ROTATED = 0x100
 TQ_V_MSE, TQ_V_G32 = 0, 1
 TQ_CODEBOOK_LLOYD, TQ_CODEBOOK_UNIFORM = 0, 1
 TQ_DEVERR_SLOT, TQ_DEVERR_BLOCK, TQ_DEVERR_SEQLEN, TQ_DEVERR_TAIL = 1, 2, 4, 8
-TQ_DEVERR_TIMEOUT, TQ_DEVERR_CHUNK = 16, 32
+TQ_DEVERR_TIMEOUT, TQ_DEVERR_CHUNK, TQ_DEVERR_POOL = 16, 32, 64
 
 # every function include/tq_kv.h declares
 EXPORTED = [
@@ -46,6 +52,11 @@ EXPORTED = [
     "tq_f8_cache_sizes", "tq_f8_cache_create", "tq_f8_cache_destroy", "tq_f8_store", "tq_f8_load",
     "tq_f8_decode_attention", "tq_f8_get_device_error",
     "tq_prompt_sizes", "tq_prompt_create", "tq_prompt_destroy", "tq_prompt_attention", "tq_prompt_get_device_error",
+    "tq_i4_cache_sizes", "tq_i4_cache_create", "tq_i4_cache_destroy", "tq_i4_store", "tq_i4_load",
+    "tq_i4_decode_attention", "tq_i4_get_device_error",
+    "tq_norm_rope_sizes", "tq_norm_rope_create", "tq_norm_rope_destroy", "tq_norm_rope",
+    "tq_norm_rope_get_device_error",
+    "tq_plan_sizes", "tq_plan_create", "tq_plan_destroy", "tq_plan_step", "tq_plan_get_device_error",
 ]
 TQ_PROF_STORE, TQ_PROF_DECODE_SPLIT = 0, 1
 
@@ -101,6 +112,13 @@ class tq_f8_config(ctypes.Structure):
         super().__init__(**{**dict(block_size=16, max_batch=1), **kw})
 
 
+class tq_i4_config(ctypes.Structure):
+    _fields_ = tq_f8_config._fields_
+
+    def __init__(self, **kw):
+        super().__init__(**{**dict(block_size=16, max_batch=1), **kw})
+
+
 class tq_prompt_config(ctypes.Structure):
     _fields_ = [
         ("head_dim", ctypes.c_int32),
@@ -113,6 +131,29 @@ class tq_prompt_config(ctypes.Structure):
 
     def __init__(self, **kw):
         super().__init__(**{**dict(dtype=TQ_DTYPE_BF16, max_batch=1), **kw})
+
+
+class tq_norm_rope_config(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("base", ctypes.c_double),
+    ]
+
+    def __init__(self, **kw):
+        super().__init__(**{**dict(rot_dim=kw.get("head_dim", 0), norm=1, eps=1e-6, base=1e4), **kw})
+
+
+class tq_plan_config(ctypes.Structure):
+    _fields_ = [("max_batch", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32)]
+
+    def __init__(self, **kw):
+        super().__init__(**{**dict(max_batch=1), **kw})
 
 
 _LIB = None
@@ -177,6 +218,24 @@ def load_library():
             "tq_prompt_attention": (
                 i32, [_P, _P, _P, _P, i64, i64, i64, _P, _P, i32, i32, i32, ctypes.c_float, i32, _P, _P, _P]),
             "tq_prompt_get_device_error": (i32, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
+        })
+        i4p = ctypes.POINTER(tq_i4_config)
+        sig.update({name.replace("f8", "i4"): (res, [i4p if a is f8p else a for a in args])
+                    for name, (res, args) in list(sig.items()) if name.startswith("tq_f8_")})
+        nrp, u32 = ctypes.POINTER(tq_norm_rope_config), ctypes.POINTER(ctypes.c_uint32)
+        plp = ctypes.POINTER(tq_plan_config)
+        sig.update({
+            "tq_norm_rope_sizes": (i32, [nrp, sz]),
+            "tq_norm_rope_create": (i32, [nrp, dp, _P, _P, ctypes.POINTER(_P)]),
+            "tq_norm_rope_destroy": (i32, [_P]),
+            "tq_norm_rope": (i32, [_P, _P, _P, _P, i32, i64, i64, i64, _P, _P, i32, _P, _P, i64, i64, _P, _P, _P, i64,
+                                   i64, i64, _P]),
+            "tq_norm_rope_get_device_error": (i32, [_P, u32, _P]),
+            "tq_plan_sizes": (i32, [plp, sz]),
+            "tq_plan_create": (i32, [plp, _P, _P, ctypes.POINTER(_P)]),
+            "tq_plan_destroy": (i32, [_P]),
+            "tq_plan_step": (i32, [_P, _P, _P, i32, _P, i64, _P, _P, i64, _P, _P, _P, _P, _P, _P, _P, _P]),
+            "tq_plan_get_device_error": (i32, [_P, u32, _P]),
         })
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -483,7 +542,7 @@ class TQCache:
             pass
 
 
-# ------------------------------------- 8-bit cache and prompt attention
+# ------------------- 8-bit and 4-bit caches, prompt attention, norm and rotation, plan
 # These calls run for a few microseconds on the GPU, so their checks are kept
 # short: every tensor is asked for its device index, shape and strides once.
 _TORCH = None
@@ -556,9 +615,10 @@ def _index(t, name, dtype, least, dev):
     return t.data_ptr()
 
 
-def _pages(cache, cfg):
-    """Pointer of an 8-bit cache's pages."""
-    need = cfg.num_blocks * cfg.num_kv_heads * (32 * cfg.head_dim + 32)
+def _pages(cache, cfg, bits=8):
+    """Pointer of an 8-bit or 4-bit cache's pages."""
+    page = (32 if bits == 8 else 18) * cfg.head_dim + 32
+    need = cfg.num_blocks * cfg.num_kv_heads * page
     if cache is None or not cache.is_cuda or not cache.is_contiguous() or cache.nbytes < need:
         raise ValueError(f"cache must be a contiguous CUDA tensor of at least {need} bytes")
     return cache.data_ptr()
@@ -811,6 +871,366 @@ class TQPrompt:
     def close(self):
         if self.handle:
             tq_prompt_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------------- 4-bit cache
+def tq_i4_cache_sizes(cfg):
+    vals = [ctypes.c_size_t() for _ in range(3)]
+    _check(load_library().tq_i4_cache_sizes(ctypes.byref(cfg), *[ctypes.byref(v) for v in vals]), "tq_i4_cache_sizes")
+    return dict(zip(["page_bytes", "cache_bytes", "workspace_bytes"], [v.value for v in vals]))
+
+
+def tq_i4_cache_create(cfg, workspace, stream=None):
+    h = _P()
+    _check(load_library().tq_i4_cache_create(ctypes.byref(cfg), _P(workspace.data_ptr()), _stream_ptr(stream),
+                                             ctypes.byref(h)), "tq_i4_cache_create")
+    return h
+
+
+def tq_i4_cache_destroy(handle):
+    _check(load_library().tq_i4_cache_destroy(handle), "tq_i4_cache_destroy")
+
+
+def tq_i4_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
+    """k, v [T, H_kv, d] (f32, bf16 or f16, same dtype; rows may lie apart);
+    slot_mapping int64 [T]."""
+    dt = _code(k, "k")
+    if k.dtype != v.dtype or k.shape != v.shape:
+        raise ValueError("k and v must have the same shape and dtype")
+    dev = cache.get_device() if cache is not None else k.get_device()
+    heads, d = cfg.num_kv_heads, cfg.head_dim
+    kp, ks = _rows(k, "k", heads, d, dev)
+    vp, vs = _rows(v, "v", heads, d, dev)
+    n = k.shape[0]
+    st = load_library().tq_i4_store(handle, kp, vp, dt, ks, vs, n,
+                                    _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _pages(cache, cfg, 4),
+                                    _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_i4_store")
+
+
+def tq_i4_load(handle, cfg, cache, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
+    """block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]; cu_out
+    int32 [B] (or more): first row of each sequence in k_out, v_out [rows,
+    H_kv, d] (f32, bf16 or f16)."""
+    dt = _code(k_out, "k_out")
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have the same shape and dtype")
+    dev = cache.get_device() if cache is not None else k_out.get_device()
+    b, n, i32 = seq_lens.shape[0], k_out.shape[0], _TORCH.int32
+    shape = (n, cfg.num_kv_heads, cfg.head_dim)
+    st = load_library().tq_i4_load(
+        handle, _pages(cache, cfg, 4), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        _index(seq_lens, "seq_lens", i32, b, dev), _index(cu_out, "cu_out", i32, b, dev), b, n,
+        _plain(k_out, "k_out", shape, None, dev), _plain(v_out, "v_out", shape, None, dev), dt,
+        _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_i4_load")
+
+
+def tq_i4_decode_attention(handle, cfg, q, cache, block_table, seq_lens, out, scale=0.0, stream=None):
+    """q, out [B, H_q, d] (f32, bf16 or f16 each; q's rows may lie apart);
+    block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]."""
+    qt, ot = _code(q, "q"), _code(out, "out")
+    dev = cache.get_device() if cache is not None else q.get_device()
+    heads, d = cfg.num_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", heads, d, dev)
+    b = q.shape[0]
+    st = load_library().tq_i4_decode_attention(
+        handle, qp, qt, qs, _pages(cache, cfg, 4), _table(block_table, b, cfg.max_blocks_per_seq, dev),
+        _index(seq_lens, "seq_lens", _TORCH.int32, b, dev), scale, b, _plain(out, "out", (b, heads, d), None, dev), ot,
+        _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_i4_decode_attention")
+
+
+def tq_i4_get_device_error(handle, stream=None):
+    flags = ctypes.c_uint32()
+    _check(load_library().tq_i4_get_device_error(handle, ctypes.byref(flags), _stream_ptr(stream)),
+           "tq_i4_get_device_error")
+    return flags.value
+
+
+class TQI4Cache:
+    """Owns (or adopts) the pages of a 4-bit cache, its workspace and the
+    library handle.  ``cache``: an existing uint8 tensor of cache_bytes."""
+
+    def __init__(self, device="cuda", cache=None, **cfg_kwargs):
+        self.handle = None
+        self.cfg = tq_i4_config(**cfg_kwargs)
+        self.sizes = tq_i4_cache_sizes(self.cfg)
+        self.device = _cuda_device(device)
+        torch = _TORCH
+        if cache is None:
+            cache = torch.zeros(self.sizes["cache_bytes"], dtype=torch.uint8, device=self.device)
+        elif (cache.dtype != torch.uint8 or cache.numel() != self.sizes["cache_bytes"] or not cache.is_contiguous()
+              or cache.device != self.device):
+            raise ValueError(f"cache must be {self.sizes['cache_bytes']} contiguous uint8 bytes on {self.device}")
+        self.cache = cache
+        self.workspace = torch.empty(self.sizes["workspace_bytes"], dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            self.handle = tq_i4_cache_create(self.cfg, self.workspace)
+
+    @property
+    def page_bytes(self):
+        return self.sizes["page_bytes"]
+
+    def pages(self):
+        """The cache as [num_blocks, H_kv, page_bytes]."""
+        return self.cache.view(self.cfg.num_blocks, self.cfg.num_kv_heads, self.page_bytes)
+
+    def store(self, k, v, slot_mapping, stream=None):
+        tq_i4_store(self.handle, self.cfg, k, v, slot_mapping, self.cache, stream)
+
+    def load(self, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
+        tq_i4_load(self.handle, self.cfg, self.cache, block_table, seq_lens, cu_out, k_out, v_out, stream)
+        return k_out, v_out
+
+    def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
+        if out is None:
+            out = _output(q, out_dtype or q.dtype, stream)
+        tq_i4_decode_attention(self.handle, self.cfg, q, self.cache, block_table, seq_lens, out, scale, stream)
+        return out
+
+    def device_error(self, stream=None):
+        return tq_i4_get_device_error(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            tq_i4_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------- norm with rotation
+def tq_norm_rope_sizes(cfg):
+    n = ctypes.c_size_t()
+    _check(load_library().tq_norm_rope_sizes(ctypes.byref(cfg), ctypes.byref(n)), "tq_norm_rope_sizes")
+    return dict(workspace_bytes=n.value)
+
+
+def tq_norm_rope_create(cfg, workspace, inv_freq=None, stream=None):
+    """inv_freq: rot_dim / 2 radians per position (float64 on the host), or None."""
+    f = None
+    if inv_freq is not None:
+        f = np.ascontiguousarray(inv_freq, np.float64)
+        if f.shape != (cfg.rot_dim // 2,):
+            raise ValueError(f"inv_freq must have {cfg.rot_dim // 2} entries, got {f.shape}")
+    h = _P()
+    _check(load_library().tq_norm_rope_create(ctypes.byref(cfg), None if f is None else _dptr(f),
+                                              _P(workspace.data_ptr()), _stream_ptr(stream), ctypes.byref(h)),
+           "tq_norm_rope_create")
+    return h
+
+
+def tq_norm_rope_destroy(handle):
+    _check(load_library().tq_norm_rope_destroy(handle), "tq_norm_rope_destroy")
+
+
+def tq_norm_rope(handle, cfg, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, v=None, v_out=None,
+                 kv_rows=None, stream=None):
+    """q, q_out [T, H_q, d], k, v [T, H_kv, d], k_out, v_out [rows, H_kv, d], all of
+    one dtype (f32, bf16 or f16), rows may lie apart; positions, kv_rows int32 [T];
+    weights [d], both of one dtype."""
+    dt = _code(q, "q")
+    dtype, dev = q.dtype, q.get_device()
+    hq, hk, d, i32 = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, _TORCH.int32
+    if k.dtype != dtype or q_out.dtype != dtype or k_out.dtype != dtype:
+        raise TypeError("q, k and the outputs must all have the same dtype")
+    qp, qs = _rows(q, "q", hq, d, dev)
+    kp, ks = _rows(k, "k", hk, d, dev)
+    qo, qos = _rows(q_out, "q_out", hq, d, dev)
+    ko, kos = _rows(k_out, "k_out", hk, d, dev)
+    n, rows = q.shape[0], k_out.shape[0]
+    if k.shape[0] != n or q_out.shape[0] != n:
+        raise ValueError("q, k and q_out must have the same number of rows")
+    if kv_rows is None and rows != n:
+        raise ValueError(f"k_out must have {n} rows, got {rows} (or kv_rows must be given)")
+    vp = vo = None
+    vs = vos = 0
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    if v is not None:
+        if v.dtype != dtype or v_out.dtype != dtype:
+            raise TypeError("v and v_out must have q's dtype")
+        vp, vs = _rows(v, "v", hk, d, dev)
+        vo, vos = _rows(v_out, "v_out", hk, d, dev)
+        if v.shape[0] != n or v_out.shape[0] != rows:
+            raise ValueError("v must have k's rows and v_out k_out's")
+    wt, wp = 0, [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
+        if w is not None:
+            wt, wp[i] = _code(w, "weight"), _plain(w, "weight", (d,), None, dev)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have the same dtype")
+    st = load_library().tq_norm_rope(
+        handle, qp, kp, vp, dt, qs, ks, vs, wp[0], wp[1], wt, _index(positions, "positions", i32, n, dev),
+        None if kv_rows is None else _index(kv_rows, "kv_rows", i32, n, dev), n, rows, qo, ko, vo, qos, kos, vos,
+        _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_norm_rope")
+
+
+def tq_norm_rope_get_device_error(handle, stream=None):
+    flags = ctypes.c_uint32()
+    _check(load_library().tq_norm_rope_get_device_error(handle, ctypes.byref(flags), _stream_ptr(stream)),
+           "tq_norm_rope_get_device_error")
+    return flags.value
+
+
+class TQNormRope:
+    """Owns the workspace and library handle of norm with rotation for one head
+    configuration: rot_dim (default: the whole head), base or inv_freq, eps,
+    interleaved, norm (0: rotation alone)."""
+
+    def __init__(self, device="cuda", inv_freq=None, **cfg_kwargs):
+        self.handle = None
+        self.cfg = tq_norm_rope_config(**cfg_kwargs)
+        self.sizes = tq_norm_rope_sizes(self.cfg)
+        self.device = _cuda_device(device)
+        self.workspace = _TORCH.empty(self.sizes["workspace_bytes"], dtype=_TORCH.uint8, device=self.device)
+        with _TORCH.cuda.device(self.device):
+            self.handle = tq_norm_rope_create(self.cfg, self.workspace, inv_freq)
+
+    def apply(self, q, k, positions, q_weight=None, k_weight=None, q_out=None, k_out=None, v=None, v_out=None,
+              kv_rows=None, stream=None):
+        """(q_out, k_out), and v_out where v is given.  With kv_rows, k_out and v_out are
+        the caller's longer buffers."""
+        if q.get_device() != self.device.index:
+            raise _wrong_device(q, "q", self.device.index)
+        if kv_rows is not None and (k_out is None or (v is not None and v_out is None)):
+            raise ValueError("kv_rows name rows of k_out and v_out: give them")
+        if q_out is None:
+            q_out = _output(q, q.dtype, stream)
+        if k_out is None:
+            k_out = _output(k, k.dtype, stream)
+        if v is not None and v_out is None:
+            v_out = _output(v, v.dtype, stream)
+        tq_norm_rope(self.handle, self.cfg, q, k, positions, q_out, k_out, q_weight, k_weight, v, v_out, kv_rows, stream)
+        return (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+    def device_error(self, stream=None):
+        return tq_norm_rope_get_device_error(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            tq_norm_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------------ plan of a step
+def tq_plan_sizes(cfg):
+    n = ctypes.c_size_t()
+    _check(load_library().tq_plan_sizes(ctypes.byref(cfg), ctypes.byref(n)), "tq_plan_sizes")
+    return dict(workspace_bytes=n.value)
+
+
+def tq_plan_create(cfg, workspace, stream=None):
+    h = _P()
+    _check(load_library().tq_plan_create(ctypes.byref(cfg), _P(workspace.data_ptr()), _stream_ptr(stream),
+                                         ctypes.byref(h)), "tq_plan_create")
+    return h
+
+
+def tq_plan_destroy(handle):
+    _check(load_library().tq_plan_destroy(handle), "tq_plan_destroy")
+
+
+def tq_plan_step(handle, cfg, lens, new_lens, block_table, free_blocks, next_free, slot_mapping, positions, kv_rows,
+                 seq_lens, cu_q, cu_k, next_free_out, stream=None):
+    """lens, new_lens (or None: 1 each), seq_lens int32 [B]; block_table int32 [B,
+    max_blocks_per_seq]; free_blocks int32 [F]; next_free, next_free_out int32 [1];
+    slot_mapping int64 [T]; positions, kv_rows int32 [T]; cu_q, cu_k int32 [B + 1]."""
+    dev, i32 = block_table.get_device(), _torch().int32
+    b, n = lens.shape[0], slot_mapping.shape[0]
+    st = load_library().tq_plan_step(
+        handle, _index(lens, "lens", i32, b, dev),
+        None if new_lens is None else _index(new_lens, "new_lens", i32, b, dev), b,
+        _index(free_blocks, "free_blocks", i32, 0, dev), free_blocks.numel(),
+        _index(next_free, "next_free", i32, 1, dev), _table(block_table, b, cfg.max_blocks_per_seq, dev), n,
+        _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _index(positions, "positions", i32, n, dev),
+        _index(kv_rows, "kv_rows", i32, n, dev), _index(seq_lens, "seq_lens", i32, b, dev),
+        _index(cu_q, "cu_q", i32, b + 1, dev), _index(cu_k, "cu_k", i32, b + 1, dev),
+        _index(next_free_out, "next_free_out", i32, 1, dev), _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_plan_step")
+
+
+def tq_plan_get_device_error(handle, stream=None):
+    flags = ctypes.c_uint32()
+    _check(load_library().tq_plan_get_device_error(handle, ctypes.byref(flags), _stream_ptr(stream)),
+           "tq_plan_get_device_error")
+    return flags.value
+
+
+class TQPlanStep:
+    """The tensors that a plan's step writes, for ``batch`` requests and ``tokens``
+    rows: slot_mapping, positions, kv_rows, seq_lens, cu_q, cu_k, next_free."""
+
+    def __init__(self, batch, tokens, device, stream=None):
+        torch = _torch()
+
+        # (memory of the stream that will write it, as in _output)
+        with torch.cuda.stream(stream):
+            def make(n, dtype=torch.int32):
+                return torch.empty(n, dtype=dtype, device=device)
+
+            self.slot_mapping = make(tokens, torch.int64)
+            self.positions, self.kv_rows = make(tokens), make(tokens)
+            self.seq_lens, self.cu_q, self.cu_k = make(batch), make(batch + 1), make(batch + 1)
+            self.next_free = make(1)
+
+
+class TQPlan:
+    """Owns the workspace and library handle of the plan of steps of up to
+    max_batch requests and max_blocks_per_seq blocks each."""
+
+    def __init__(self, device="cuda", **cfg_kwargs):
+        self.handle = None
+        self.cfg = tq_plan_config(**cfg_kwargs)
+        self.sizes = tq_plan_sizes(self.cfg)
+        self.device = _cuda_device(device)
+        self.workspace = _TORCH.empty(self.sizes["workspace_bytes"], dtype=_TORCH.uint8, device=self.device)
+        with _TORCH.cuda.device(self.device):
+            self.handle = tq_plan_create(self.cfg, self.workspace)
+
+    def outputs(self, batch, tokens, stream=None):
+        """Tensors for ``step``; they can be used again from step to step."""
+        return TQPlanStep(batch, tokens, self.device, stream)
+
+    def step(self, lens, new_lens, block_table, free_blocks, next_free, out, stream=None):
+        """Plan one step into ``out`` (a TQPlanStep) and block_table; returns ``out``.  In a
+        loop, lens and next_free may be out.seq_lens and out.next_free."""
+        if block_table.get_device() != self.device.index:
+            raise _wrong_device(block_table, "block_table", self.device.index)
+        tq_plan_step(self.handle, self.cfg, lens, new_lens, block_table, free_blocks, next_free, out.slot_mapping,
+                     out.positions, out.kv_rows, out.seq_lens, out.cu_q, out.cu_k, out.next_free, stream)
+        return out
+
+    def device_error(self, stream=None):
+        return tq_plan_get_device_error(self.handle, stream)
+
+    def close(self):
+        if self.handle:
+            tq_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
