@@ -182,6 +182,20 @@ def _decode_case(d, hkv, g, lens, qt, seed, k_gain=1.0, v_scales=None, q_gain=1.
     return c, q, table
 
 
+def _steps(q, k, v, exps, scale):
+    """What the weights' steps add.  A weight p_t 2^e_t (e_t the value's exponent) goes in as one or two fp16 parts
+    whose steps are 2^-24 at least, beside a largest weight of at least 2^4: it is off by up to 2^-29 of the
+    sequence's largest, times |v_t| 2^-e_t.  (A 4-bit code of the largest can be 0: then that is all there is.)"""
+    out = np.zeros((q.shape[1], v.shape[2]))
+    g = q.shape[1] // k.shape[1]
+    for h in range(q.shape[1]):
+        z = k[:, h // g] @ q[0, h] * scale
+        size = np.exp2(exps[:, h // g] - 127.0)
+        most = (np.exp(z - z.max()) * size).max() / np.exp(z - z.max()).sum()
+        out[h] = 2.0 ** -29 * most * (np.abs(v[:, h // g]) / size[:, None]).sum(0)
+    return out
+
+
 def _check_decode(c, q, table, lens, got, scale=0.0):
     d = c.cfg.head_dim
     pages = c.pages().cpu().numpy()
@@ -194,7 +208,9 @@ def _check_decode(c, q, table, lens, got, scale=0.0):
             continue
         k, v = i4.rows(pages, table[b], n, d)
         ref, _, mag = f8.attention(qn[b:b + 1], k, v, sc)
-        tol = _bound(qn[b:b + 1], k, v, sc, mag, ref, precise, got.dtype)[0]
+        t = np.arange(n)
+        exps = i4.parts(pages, d)[1][2][table[b, t // 16], :, t % 16].astype(np.float64)
+        tol = _bound(qn[b:b + 1], k, v, sc, mag, ref, precise, got.dtype)[0] + _steps(qn[b:b + 1], k, v, exps, sc)
         err = np.abs(gn[b] - ref[0])
         assert (err <= tol).all(), (b, n, err.max(), (err / tol).max())
 

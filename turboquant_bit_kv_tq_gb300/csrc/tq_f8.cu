@@ -263,9 +263,9 @@ static tq_status f8_check(const tq_f8_config& c) {
         c.max_blocks_per_seq > 0x7FFFFFFF / kBlock)
         return TQ_ERR_INVALID_ARG;
     // q rows and the pages of all block-table entries, KV heads and head groups within int32
-    const F8Geom g = f8_geom(c);
+    const PagedGeom g = paged_geom(c);
     if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF ||
-        (double)c.max_batch * (c.max_blocks_per_seq + kF8UnitCost) * c.num_kv_heads * g.nhg > 2147483647.0 ||
+        (double)c.max_batch * (c.max_blocks_per_seq + kPagedUnitCost) * c.num_kv_heads * g.nhg > 2147483647.0 ||
         (double)c.num_blocks * c.num_kv_heads > 2147483647.0)
         return TQ_ERR_INVALID_ARG;
     return TQ_OK;
@@ -285,7 +285,7 @@ tq_status tq_f8_cache_sizes(const tq_f8_config* cfg, size_t* page_bytes, size_t*
     const size_t page = f8_page_bytes(cfg->head_dim);
     if (page_bytes) *page_bytes = page;
     if (cache_bytes) *cache_bytes = (size_t)cfg->num_blocks * cfg->num_kv_heads * page;
-    if (workspace_bytes) *workspace_bytes = f8_workspace(*cfg).total;
+    if (workspace_bytes) *workspace_bytes = paged_workspace(*cfg).total;
     return TQ_OK;
 }
 
@@ -297,10 +297,10 @@ tq_status tq_f8_cache_create(const tq_f8_config* cfg, void* workspace_dev, void*
     if ((uintptr_t)workspace_dev & 15) return TQ_ERR_MISALIGNED;
     tq_f8_cache* h = new (std::nothrow) tq_f8_cache();
     if (!h) return TQ_ERR_INVALID_ARG;
-    const F8Workspace w = f8_workspace(*cfg);
+    const PagedWorkspace w = paged_workspace(*cfg);
     uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
     h->cfg = *cfg;
-    h->geom = f8_geom(*cfg);
+    h->geom = paged_geom(*cfg);
     h->err = reinterpret_cast<uint32_t*>(ws + w.err);
     h->cnt = reinterpret_cast<uint32_t*>(ws + w.cnt);
     h->gcnt = reinterpret_cast<uint32_t*>(ws + w.gcnt);

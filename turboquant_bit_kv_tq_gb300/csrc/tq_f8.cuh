@@ -1,55 +1,9 @@
 // The 8-bit cache: its handle and the device helpers its kernels share.
 #pragma once
 
-#include "tq_device.cuh"
+#include "tq_paged.cuh"
 
 namespace tq {
-
-// Decode grids: kF8Warps warps per block, at most kF8Ctas blocks per SM and
-// kF8MaxSms SMs; the workspace holds two partial sums for each block.
-constexpr int kF8Warps = 4, kF8Ctas = 3, kF8MaxSms = 160;
-constexpr int kF8Slots = 2 * kF8Ctas * kF8MaxSms;
-// Places a unit takes beside its pages where pages are dealt out, at most: its start
-// and its sums take a block about as long as 8 (d = 128) to 16 (d = 256) pages.  With
-// 0, 4, 8, 16, 24, 32: 8 x up to 32768 tokens, d = 256: 81, 73, 68, 60, 59, 58 us;
-// 64 x up to 2000, d = 128: 56, 48, 37, 35, 34, 35 us.
-constexpr int kF8UnitCost = 24;
-
-// Query heads of one KV head that one work unit serves (nhg units per KV head
-// share its pages through L2 when G > 16), in n-tiles of 8 heads.
-struct F8Geom {
-    int group, nhg, hp, nt;
-};
-inline F8Geom f8_geom(const tq_f8_config& c) {
-    F8Geom g;
-    g.group = c.num_q_heads / c.num_kv_heads;
-    g.nhg = (g.group + 15) / 16;
-    g.hp = (g.group + g.nhg - 1) / g.nhg;
-    g.nt = g.hp > 8 ? 2 : 1;
-    return g;
-}
-
-struct F8Workspace {
-    // err: the error word; cnt: one counter per (sequence, KV head, head group);
-    // gcnt: one per slot; part: [kF8Slots][d/16][nt][32][4] fp32 sums in
-    // fragment order; meta: [kF8Slots][8 nt] {r, x, l, -}
-    size_t err, cnt, gcnt, zeroed, part, meta, total;
-};
-inline F8Workspace f8_workspace(const tq_f8_config& c) {
-    const F8Geom g = f8_geom(c);
-    F8Workspace w;
-    w.err = 0;
-    w.cnt = 16;
-    w.gcnt = w.cnt + (size_t)c.max_batch * c.num_kv_heads * g.nhg * 4;
-    w.zeroed = w.gcnt + (size_t)kF8Slots * 4;
-    size_t off = (w.zeroed + 255) & ~(size_t)255;
-    w.part = off;
-    off += (size_t)kF8Slots * 8 * g.nt * c.head_dim * 4;
-    w.meta = off;
-    off += (size_t)kF8Slots * 8 * g.nt * 16;
-    w.total = off;
-    return w;
-}
 
 // Element conversions of the calls' dtypes.
 struct F8Elem {
@@ -116,7 +70,7 @@ __host__ __device__ constexpr int f8_page_bytes(int d) { return 32 * d + 32; }
 
 struct tq_f8_cache {
     tq_f8_config cfg;
-    tq::F8Geom geom;
+    tq::PagedGeom geom;
     uint32_t* err;
     uint32_t *cnt, *gcnt;
     float4 *part, *meta;

@@ -264,9 +264,9 @@ static tq_status i4_check(const tq_i4_config& c) {
         c.max_blocks_per_seq > 0x7FFFFFFF / kBlock)
         return TQ_ERR_INVALID_ARG;
     // q rows and the pages of all block-table entries, KV heads and head groups within int32
-    const int nhg = (c.num_q_heads / c.num_kv_heads + 15) / 16;
+    const int nhg = paged_geom(c).nhg;
     if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF ||
-        (double)c.max_batch * (c.max_blocks_per_seq + kF8UnitCost) * c.num_kv_heads * nhg > 2147483647.0 ||
+        (double)c.max_batch * (c.max_blocks_per_seq + kPagedUnitCost) * c.num_kv_heads * nhg > 2147483647.0 ||
         (double)c.num_blocks * c.num_kv_heads > 2147483647.0)
         return TQ_ERR_INVALID_ARG;
     return TQ_OK;
@@ -286,7 +286,7 @@ tq_status tq_i4_cache_sizes(const tq_i4_config* cfg, size_t* page_bytes, size_t*
     const size_t page = i4_page_bytes(cfg->head_dim);
     if (page_bytes) *page_bytes = page;
     if (cache_bytes) *cache_bytes = (size_t)cfg->num_blocks * cfg->num_kv_heads * page;
-    if (workspace_bytes) *workspace_bytes = 16;
+    if (workspace_bytes) *workspace_bytes = paged_workspace(*cfg).total;
     return TQ_OK;
 }
 
@@ -298,10 +298,17 @@ tq_status tq_i4_cache_create(const tq_i4_config* cfg, void* workspace_dev, void*
     if ((uintptr_t)workspace_dev & 15) return TQ_ERR_MISALIGNED;
     tq_i4_cache* h = new (std::nothrow) tq_i4_cache();
     if (!h) return TQ_ERR_INVALID_ARG;
+    const PagedWorkspace w = paged_workspace(*cfg);
+    uint8_t* ws = static_cast<uint8_t*>(workspace_dev);
     h->cfg = *cfg;
-    h->err = static_cast<uint32_t*>(workspace_dev);
+    h->geom = paged_geom(*cfg);
+    h->err = reinterpret_cast<uint32_t*>(ws + w.err);
+    h->cnt = reinterpret_cast<uint32_t*>(ws + w.cnt);
+    h->gcnt = reinterpret_cast<uint32_t*>(ws + w.gcnt);
+    h->part = reinterpret_cast<float4*>(ws + w.part);
+    h->meta = reinterpret_cast<float4*>(ws + w.meta);
     cudaStream_t s = (cudaStream_t)stream;
-    tq_status cs = cuda_status(cudaMemsetAsync(workspace_dev, 0, 16, s));
+    tq_status cs = cuda_status(cudaMemsetAsync(ws, 0, w.zeroed, s));
     if (cs == TQ_OK) cs = cuda_status(cudaStreamSynchronize(s));
     if (cs != TQ_OK) {
         delete h;

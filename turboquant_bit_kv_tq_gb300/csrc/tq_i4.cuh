@@ -24,5 +24,8 @@ __device__ __forceinline__ __half2 i4_pair(uint32_t w, int i) {
 
 struct tq_i4_cache {
     tq_i4_config cfg;
+    tq::PagedGeom geom;
     uint32_t* err;
+    uint32_t *cnt, *gcnt;
+    float4 *part, *meta;
 };
