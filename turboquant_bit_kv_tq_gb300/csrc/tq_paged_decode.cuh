@@ -83,6 +83,14 @@ __device__ __forceinline__ void paged_mma(float (&c)[4], uint32_t a0, uint32_t a
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
+// (the first of a chain)
+__device__ __forceinline__ void paged_mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t paged_transpose(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -112,26 +120,25 @@ __device__ __forceinline__ void paged_page_copy(uint32_t dst, const CUtensorMap*
             : "memory");
 }
 // 4-bit codes as fp16: code times scale.  A code masked in place under the exponent of
-// 1024 is 1024 + n (or, four bits higher, 1024 + 16 n), and (1024 + n) S - 1032 S = (n - 8) S,
-// (1024 + 16 n) S / 16 - 72 S likewise: one fma, exact in every part, since S has four
-// bits and lies between 2^-17 and 32.
+// 1024 is 1024 + n (four bits higher, under that of 64: 64 + n), and (1024 + n) S - 1032 S
+// = (n - 8) S, (64 + n) S - 72 S likewise: one fma, exact in every part, since S has
+// four bits and lies between 2^-17 and 32.
 struct PagedScale {
-    __half2 s, off, s16, off16;
+    __half2 s, low_off, high_off;
     __device__ __forceinline__ explicit PagedScale(uint32_t pair) {  // fp16 pair of scales
         s = *reinterpret_cast<const __half2*>(&pair);
-        off = __hmul2(s, __float2half2_rn(-1032.f));
-        s16 = __hmul2(s, __float2half2_rn(0.0625f));
-        off16 = __hmul2(s, __float2half2_rn(-72.f));
+        low_off = __hmul2(s, __float2half2_rn(-1032.f));
+        high_off = __hmul2(s, __float2half2_rn(-72.f));
     }
     // codes in bits 0..3 (low) or 4..7 of both halves of x
     __device__ __forceinline__ uint32_t low(uint32_t x) const {
         x = (x & 0x000F000Fu) | 0x64006400u;
-        const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s, off);
+        const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s, low_off);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
     __device__ __forceinline__ uint32_t high(uint32_t x) const {
-        x = (x & 0x00F000F0u) | 0x64006400u;
-        const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s16, off16);
+        x = (x & 0x00F000F0u) | 0x54005400u;
+        const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s, high_off);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
 };
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     const uint32_t jbar = smem_u32(&s_jbar);
     if (tid == 0) mbar_init(jbar, 1);
     if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
+        for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, PP);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
@@ -366,44 +373,46 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         if (cons.left <= 0) return;  // (solo: no unit starts here)
         PagedWalk prod = cons;
 
-        // ---- producer: this warp's steps, segment after segment
+        // ---- producer: this warp's steps, segment after segment.  Lane pp of a step copies
+        // its page pp; lane x of a batch of steps has looked up the batch's page x
         PagedSeg ps = paged_next(a, prod, nj, cost);
-        int pst = sw;
-        int made = 0, used = 0;  // steps copied, steps taken
-        int ids = -1, ids_at = 0, ids_n = 0;  // block ids of ids_n pages: this warp's steps from ids_at on
+        int pn = ps.p0 + sw * PP;  // first page of the next step
+        int made = 0, used = 0;    // steps copied, steps taken
+        uint32_t phase = 0;        // of the ring stage to be read
+        int pg = 0, toks = 0, at = 32;  // pages and their tokens (0: none) from entry `at` on
         auto produce = [&](int stage) {
-            while (ps.p0 + pst * PP >= ps.p1) {
-                if (prod.left <= 0) return;
-                ps = paged_next(a, prod, nj, cost);
-                pst = sw;
-                ids_n = 0;
+            if (pn >= ps.p1) {
+                do {
+                    if (prod.left <= 0) return;
+                    ps = paged_next(a, prod, nj, cost);
+                    pn = ps.p0 + sw * PP;
+                } while (pn >= ps.p1);
+                at = 32;
             }
-            if (ids_at >= ids_n) {
-                ids_at = 0;
-                ids_n = 32;
-                const int p = ps.p0 + (pst + sn * (lane / PP)) * PP + lane % PP;
-                ids = p < ps.p1 ? __ldg(a.table + (int64_t)ps.b * a.max_blocks + p) : -1;
-                if (p < ps.p1 && (ids < 0 || ids >= a.num_blocks)) {
-                    set_error(a.err, TQ_DEVERR_BLOCK);
-                    ids = -1;
+            if (at >= 32) {
+                at = 0;
+                const int p = pn + sn * PP * (lane / PP) + lane % PP;
+                const int h = a.nhg == 1 ? ps.j : ps.j / a.nhg;
+                const int blk = p < ps.p1 ? __ldg(a.table + (int64_t)ps.b * a.max_blocks + p) : -1;
+                const bool there = blk >= 0 && blk < a.num_blocks;
+                if (p < ps.p1 && !there) set_error(a.err, TQ_DEVERR_BLOCK);
+                pg = blk * a.heads + h;
+                toks = there ? min(16, ps.len - 16 * p) : 0;
+            }
+            const int page = __shfl_sync(0xffffffffu, pg, at + lane % PP);
+            const int n = __shfl_sync(0xffffffffu, toks, at + lane % PP);
+            if (lane < PP) {
+                info[stage * PP + lane] = n;
+                mbar_expect_tx(bars + 8 * stage, n > 0 ? C::PAGE : 0);
+                if (n > 0) {
+                    paged_page_copy<BITS>(smem_u32(ring) + stage * C::STEP + lane * C::CODES, &pages, page, bars + 8 * stage);
+                    bulk_copy(smem_u32(metas) + (stage * PP + lane) * C::META, a.cache + (int64_t)page * C::PAGE + C::CODES, C::META,
+                              bars + 8 * stage);
                 }
             }
-            const int h = a.nhg == 1 ? ps.j : ps.j / a.nhg;
-            // lane pp: page pp of the step (one behind the segment's last has block id -1 too)
-            const int blk = __shfl_sync(0xffffffffu, ids, ids_at + (lane < PP ? lane : 0));
-            const bool there = lane < PP && blk >= 0;
-            const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
-            if (lane == 0) mbar_expect_tx(bars + 8 * stage, n * C::PAGE);
-            if (lane < PP) info[stage * PP + lane] = there ? min(16, ps.len - 16 * (ps.p0 + pst * PP + lane)) : 0;
-            __syncwarp();
-            if (there) {
-                const int page = blk * a.heads + h;
-                paged_page_copy<BITS>(smem_u32(ring) + stage * C::STEP + lane * C::CODES, &pages, page, bars + 8 * stage);
-                bulk_copy(smem_u32(metas) + (stage * PP + lane) * C::META, a.cache + (int64_t)page * C::PAGE + C::CODES, C::META,
-                          bars + 8 * stage);
-            }
-            pst += sn;
-            ids_at += PP;
+            __syncwarp();  // (the numbers of tokens)
+            pn += sn * PP;
+            at += PP;
             ++made;
         };
 #pragma unroll
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
             for (int p = sg.p0 + sw * PP; p < sg.p1; p += sn * PP) {
                 __syncwarp();  // the last step's stage (and qf) is settled
                 if (!dead) produce(stage == 0 ? S - 1 : stage - 1);
-                if (!dead) dead = !mbar_wait(bars + 8 * stage, (used / S) & 1, a.err);
+                if (!dead) dead = !mbar_wait(bars + 8 * stage, phase, a.err);
                 dead = __any_sync(0xffffffffu, dead);
                 ++used;
                 const uint8_t* sp = ring + stage * C::STEP;
@@ -526,13 +535,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                 // that is only one, and the queries' second parts in their own
                 constexpr int CH = PP * NT == 1 ? 2 : 1, ACC = CH * (PREC ? 2 : 1);
                 float acc[ACC][PP][NT][4];
-#pragma unroll
-                for (int x = 0; x < ACC; ++x)
-#pragma unroll
-                    for (int pp = 0; pp < PP; ++pp)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            acc[x][pp][n][0] = acc[x][pp][n][1] = acc[x][pp][n][2] = acc[x][pp][n][3] = 0.f;
                 // 16 bytes of a row are 16 elements of a lane's four steps, or 32 of eight
                 constexpr int KS = BITS == 8 ? 4 : 8;
 #pragma unroll
@@ -565,8 +567,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                             if constexpr (PREC) bl = qf[(D / 16) * NT * 32 + at];
 #pragma unroll
                             for (int pp = 0; pp < PP; ++pp) {
-                                paged_mma(acc[k % CH][pp][n], x[pp][0], x[pp][1], x[pp][2], x[pp][3], b);
-                                if constexpr (PREC) paged_mma(acc[CH + k % CH][pp][n], x[pp][0], x[pp][1], x[pp][2], x[pp][3], bl);
+                                auto product = [&](float (&to)[4], uint2 y) {
+                                    if (h == 0 && k < CH) paged_mma0(to, x[pp][0], x[pp][1], x[pp][2], x[pp][3], y);
+                                    else paged_mma(to, x[pp][0], x[pp][1], x[pp][2], x[pp][3], y);
+                                };
+                                product(acc[k % CH][pp][n], b);
+                                if constexpr (PREC) product(acc[CH + k % CH][pp][n], bl);
                             }
                         }
                     };
@@ -746,7 +752,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                 constexpr int VP = PREC ? PP : 1;  // pages whose products are summed apart
 #pragma unroll
                 for (int p0 = 0; p0 < PP; p0 += VP) {
-                    if (VP == 1 && nv[p0] == 0) continue;
+                    if (BITS == 8 && VP == 1 && nv[p0] == 0) continue;  // (4 bits: both pages' instructions mixed)
 #pragma unroll
                     for (int h = 0; h < D / 128; ++h) {
                         using Piece = std::conditional_t<BITS == 8, uint4, uint2>;  // 16 elements
@@ -765,9 +771,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                                         sp + (p0 + pp) * C::CODES + 16 * C::ROW + (t + 8 * (u >> 1)) * C::ROW +
                                         (((4 * h + (g >> 1)) ^ (C::ROW == 64 ? t >> 1 & 3 : t)) << 4) + 8 * (g & 1));
                                 if constexpr (BITS == 4)
-                                    vs[pp][u >> 1] |= (uint32_t)metas[(stage * PP + p0 + pp) * C::META + D +
-                                                                      (t + 8 * (u >> 1)) * (D / 16) + 8 * h + g]
-                                                      << (u & 1 ? 23 : 7);
+                                    vs[pp][u >> 1] += (uint32_t)metas[(stage * PP + p0 + pp) * C::META + D +
+                                                                      (t + 8 * (u >> 1)) * (D / 16) + 8 * h + g] *
+                                                      (u & 1 ? 0x00800000u : 0x00000080u);
                             }
                         }
 #pragma unroll
@@ -829,6 +835,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                         }
                     }
                 }
+                phase ^= stage == S - 1;
                 stage = stage == S - 1 ? 0 : stage + 1;
             }
 
