@@ -130,26 +130,28 @@ struct PagedScale {
         low_off = __hmul2(s, __float2half2_rn(-1032.f));
         high_off = __hmul2(s, __float2half2_rn(-72.f));
     }
-    // codes in bits 0..3 (low) or 4..7 of both halves of x
+    // codes in bits 0..3 (low) or 4..7 of both halves of x.  (a & b | c, which the compiler
+    // would make two instructions of: 16 x 8192 tokens 50 us, as one 44)
     __device__ __forceinline__ uint32_t low(uint32_t x) const {
-        x = (x & 0x000F000Fu) | 0x64006400u;
+        asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(x) : "r"(x), "r"(0x64006400u));
         const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s, low_off);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
     __device__ __forceinline__ uint32_t high(uint32_t x) const {
-        x = (x & 0x00F000F0u) | 0x54005400u;
+        asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(x) : "r"(x), "r"(0x54005400u));
         const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), s, high_off);
         return *reinterpret_cast<const uint32_t*>(&r);
     }
 };
-// Token of row g (and, 8 further, of row g + 8) of the score product, so that the
-// copies' swizzle leaves the operand reads without bank conflicts.  Rows of 128 bytes:
-// the swizzle puts 16-byte chunk x of row t at x ^ (t & 7); with this order the rows a
-// quarter warp reads together differ in bit 2 (keys: rows 2i, 2i + 1, chunks c) and in
-// bits 1..2 (values: rows 2c, chunks g), so that its 8 lanes hit 8 chunk places.  Rows of
-// 64 bytes (4 bits, d = 128), chunk x of row t at x ^ (t >> 1 & 3) of half t & 1 of 128
-// bytes: a quarter warp's two key rows differ in bit 0, a half warp's four value rows in
-// bits 0 and 2, and its 16 lanes hit 16 pieces of 8 bytes.
+// Token of row g (and, 8 further, of row g + 8) of the score product, for operand reads
+// with few bank conflicts.  Rows of 128 bytes, copied with a swizzle that puts 16-byte
+// chunk x of row t at x ^ (t & 7): with this order the rows a quarter warp reads together
+// differ in bit 2 (keys: rows 2i, 2i + 1, chunks c) and in bits 1..2 (values: rows 2c,
+// chunks g), so that its 8 lanes hit 8 chunk places.  Rows of 64 bytes, copied as they
+// lie: a quarter warp's two key rows differ in bit 0, so they have no conflict, and of a
+// half warp's four value rows two and two do: their four reads take twice as long, which
+// is less than the swizzled copy took (one plain copy instead of two, 16 x 8192: 42 us,
+// 44 with the swizzle).
 template <int ROW>
 __device__ __forceinline__ int paged_token(int g) {
     if constexpr (ROW == 64) return (g & 4) | ((g & 1) << 1) | ((g ^ (g >> 1)) & 1);
@@ -159,16 +161,19 @@ __device__ __forceinline__ int paged_token(int g) {
 template <int BITS, int D, int NT, bool PREC>
 struct PagedCfg {
     static constexpr int PP = 256 / D;                 // pages per step
-    static constexpr int CODES = 4 * BITS * D;         // bytes of a page's codes in the ring
+    static constexpr int CODES = 4 * BITS * D;         // bytes of a page's codes
     static constexpr int PAGE = BITS == 8 ? f8_page_bytes(D) : i4_page_bytes(D);
     static constexpr int META = PAGE - CODES;          // and of its scales and exponents
+    // 4 bits, d = 128: the page comes as it lies, by one copy, and the ring holds it whole
+    static constexpr bool WHOLE = BITS == 4 && D == 128;
+    static constexpr int STRIDE = WHOLE ? PAGE : CODES;  // bytes from page to page in the ring
     static constexpr int ROW = BITS == 8 ? 128 : D / 2;  // bytes of a row in the ring
-    static constexpr int STEP = PP * CODES;            // bytes of a ring stage
+    static constexpr int STEP = PP * STRIDE;           // bytes of a ring stage
     static constexpr int HEADS = 8 * NT;
     static constexpr int QF = (D / 16) * NT * 32 * 8 * (PREC ? 2 : 1);  // query operands of a warp
     // blocks per SM (three where two stages per warp and the registers allow it,
     // else two), and as deep a ring as fits then
-    static constexpr int EXTRA = PP * (META + 4) + 8;  // scales, valid tokens and barrier of a stage
+    static constexpr int EXTRA = PP * ((WHOLE ? 0 : META) + 4) + 8;  // scales, valid tokens and barrier of a stage
     static constexpr int per_cta(int n) { return 233472 / n - 1024 - 1280 - 1024; }
     static constexpr int fit(int n) { return (per_cta(n) / kPagedWarps - QF) / (STEP + EXTRA); }
     static constexpr int CTAS = fit(3) >= 2 && NT == 1 && D == 128 ? 3 : fit(2) >= 2 ? 2 : 1;
@@ -176,7 +181,7 @@ struct PagedCfg {
     static_assert(STAGES >= 2, "ring");
     static constexpr int off_q = kPagedWarps * STAGES * STEP;
     static constexpr int off_ex = off_q + kPagedWarps * QF;                   // [warps][STAGES][PP][META]
-    static constexpr int off_bar = off_ex + kPagedWarps * STAGES * PP * META;   // [warps][STAGES]
+    static constexpr int off_bar = off_ex + (WHOLE ? 0 : kPagedWarps * STAGES * PP * META);   // [warps][STAGES]
     static constexpr int off_info = off_bar + kPagedWarps * STAGES * 8;       // [warps][STAGES][PP] valid tokens
     static constexpr int total = off_info + kPagedWarps * STAGES * PP * 4 + 1024;  // + alignment to 1024
     static constexpr int ITEMS = D / 16 * NT * 32;     // float4 per partial sum
@@ -270,6 +275,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     uint8_t* ring = smem + warp * (S * C::STEP);
     uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q + warp * C::QF);
     uint8_t* metas = smem + C::off_ex + warp * S * PP * C::META;
+    // a ring page's scales and exponents
+    auto meta = [&](int stage, int pp) {
+        return C::WHOLE ? ring + stage * C::STEP + pp * C::STRIDE + C::CODES : metas + (stage * PP + pp) * C::META;
+    };
+    // 16-byte chunk x of row t, as the copy's swizzle places it
+    auto chunk = [](int x, int t) { return C::WHOLE ? x : x ^ t; };
     const uint32_t bars = smem_u32(smem + C::off_bar) + warp * S * 8;
     int* info = reinterpret_cast<int*>(smem + C::off_info) + warp * S * PP;
     const int tok = paged_token<C::ROW>(g);
@@ -405,9 +416,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                 info[stage * PP + lane] = n;
                 mbar_expect_tx(bars + 8 * stage, n > 0 ? C::PAGE : 0);
                 if (n > 0) {
-                    paged_page_copy<BITS>(smem_u32(ring) + stage * C::STEP + lane * C::CODES, &pages, page, bars + 8 * stage);
-                    bulk_copy(smem_u32(metas) + (stage * PP + lane) * C::META, a.cache + (int64_t)page * C::PAGE + C::CODES, C::META,
-                              bars + 8 * stage);
+                    const uint32_t to = smem_u32(ring) + stage * C::STEP + lane * C::STRIDE;
+                    const uint8_t* from = a.cache + (int64_t)page * C::PAGE;
+                    if constexpr (C::WHOLE) {
+                        bulk_copy(to, from, C::PAGE, bars + 8 * stage);
+                    } else {
+                        paged_page_copy<BITS>(to, &pages, page, bars + 8 * stage);
+                        bulk_copy(smem_u32(metas) + (stage * PP + lane) * C::META, from + C::CODES, C::META, bars + 8 * stage);
+                    }
                 }
             }
             __syncwarp();  // (the numbers of tokens)
@@ -550,9 +566,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                                     sp + pp * C::CODES + (h >> 1) * 4096 + (tok + 8 * u) * 128 + (((4 * (h & 1) + c) ^ tok) << 4));
                             } else {
                                 ka[pp][u] = *reinterpret_cast<const uint4*>(
-                                    sp + pp * C::CODES + (tok + 8 * u) * C::ROW + (((4 * h + c) ^ (C::ROW == 64 ? tok >> 1 & 3 : tok)) << 4));
+                                    sp + pp * C::STRIDE + (tok + 8 * u) * C::ROW + (chunk(4 * h + c, tok) << 4));
                                 sc[pp][u] = *reinterpret_cast<const uint16_t*>(
-                                    metas + (stage * PP + pp) * C::META + (tok + 8 * u) * (D / 16) + 2 * (c + 4 * h));
+                                    meta(stage, pp) + (tok + 8 * u) * (D / 16) + 2 * (c + 4 * h));
                             }
                         }
                     auto word = [&](int pp, int u, int i) {
@@ -627,7 +643,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                 for (int pp = 0; pp < PP; ++pp) {
                     nv[pp] = info[stage * PP + pp];
                     full &= nv[pp] == 16;
-                    const uint8_t* ex = metas + (stage * PP + pp) * C::META + C::META - 32;
+                    const uint8_t* ex = meta(stage, pp) + C::META - 32;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         // a vector stored as NaN has zero codes and E = 255: 0 * inf here
@@ -739,7 +755,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                         for (int idx = lane; idx < PP * 16 * (D / 128); idx += 32) {
                             const int pp = idx / (D / 8), x = idx % (D / 8), t = x / (D / 128);  // 8-byte piece x of the values' scales
                             if (t >= info[stage * PP + pp])
-                                *reinterpret_cast<uint2*>(metas + (stage * PP + pp) * C::META + D + 8 * x) = make_uint2(0u, 0u);
+                                *reinterpret_cast<uint2*>(meta(stage, pp) + D + 8 * x) = make_uint2(0u, 0u);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
@@ -768,11 +784,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                                                                                (t + 8 * (u >> 1)) * 128 + ((g ^ t) << 4));
                                 else
                                     v[pp][u] = *reinterpret_cast<const uint2*>(
-                                        sp + (p0 + pp) * C::CODES + 16 * C::ROW + (t + 8 * (u >> 1)) * C::ROW +
-                                        (((4 * h + (g >> 1)) ^ (C::ROW == 64 ? t >> 1 & 3 : t)) << 4) + 8 * (g & 1));
+                                        sp + (p0 + pp) * C::STRIDE + 16 * C::ROW + (t + 8 * (u >> 1)) * C::ROW +
+                                        (chunk(4 * h + (g >> 1), t) << 4) + 8 * (g & 1));
                                 if constexpr (BITS == 4)
-                                    vs[pp][u >> 1] += (uint32_t)metas[(stage * PP + p0 + pp) * C::META + D +
-                                                                      (t + 8 * (u >> 1)) * (D / 16) + 8 * h + g] *
+                                    vs[pp][u >> 1] += (uint32_t)meta(stage, p0 + pp)[D + (t + 8 * (u >> 1)) * (D / 16) + 8 * h + g] *
                                                       (u & 1 ? 0x00800000u : 0x00000080u);
                             }
                         }
@@ -1114,7 +1129,7 @@ static tq_status paged_page_map(CUtensorMap* m, const void* cache, int64_t pages
     const cuuint32_t box4[3] = {(cuuint32_t)C::ROW, 32, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, N, const_cast<void*>(cache), BITS == 8 ? dims8 : dims4,
                            BITS == 8 ? strides8 : strides4, BITS == 8 ? box8 : box4, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           C::ROW == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return driver_failure("cuTensorMapEncodeTiled failed (CUresult %d) for %lld pages at %p", (int)r,
@@ -1132,9 +1147,11 @@ static tq_status launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     if (st != TQ_OK) return st;
     // one wave of resident blocks
     const int grid = C::CTAS * std::min(sms, kPagedMaxSms);
-    CUtensorMap pages;
-    st = paged_page_map<BITS, D>(&pages, a.cache, a.num_blocks * a.heads);
-    if (st != TQ_OK) return st;
+    CUtensorMap pages = {};
+    if constexpr (!C::WHOLE) {
+        st = paged_page_map<BITS, D>(&pages, a.cache, a.num_blocks * a.heads);
+        if (st != TQ_OK) return st;
+    }
     // launched programmatically: the launch overlaps the previous kernel's end,
     // and the kernel waits for it before its first read
     return cuda_status(launch_pdl(true, paged_decode_kernel<BITS, D, NT, PREC>, dim3(grid), dim3(kPagedThreads), C::total, s, a, pages));
