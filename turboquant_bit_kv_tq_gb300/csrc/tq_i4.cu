@@ -17,20 +17,38 @@ struct I4StoreArgs {
     uint8_t* cache;
     int64_t num_slots;
     int heads;
+    bool wide;  // rows start at multiples of 32 bytes
     uint32_t* err;
 };
 
 constexpr int kI4StoreThreads = 128;
+
+// 32 bytes at once: a whole sector of memory
+__device__ __forceinline__ void i4_load32(const uint4* p, uint4& a, uint4& b) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
+}
+__device__ __forceinline__ void i4_store32(uint4* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
 
 // 16 elements, as they lie in memory
 template <int DT>
 struct I4Raw {
     static constexpr int N = DT == TQ_DTYPE_F32 ? 4 : 2;
     uint4 w[N];
-    __device__ __forceinline__ void load(const void* base, int64_t off) {
+    __device__ __forceinline__ void load(const void* base, int64_t off, bool wide) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off * (DT == TQ_DTYPE_F32 ? 4 : 2));
+        if (wide) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = __ldg(p + i);
+            for (int i = 0; i < N; i += 2) i4_load32(p + i, w[i], w[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __ldg(p + i);
+        }
     }
     // the largest magnitude's fp32 bits: without the sign a number's bits are ordered
     // like integers, inf and NaN above every number
@@ -138,8 +156,8 @@ __global__ void __launch_bounds__(kI4StoreThreads) i4_store_kernel(I4StoreArgs a
     int64_t slot = -1;
     if (t < a.n_tokens) {
         slot = __ldg(a.slots + t);
-        k.load(a.k, t * a.k_stride + (int64_t)h * D + 16 * sub);
-        v.load(a.v, t * a.v_stride + (int64_t)h * D + 16 * sub);
+        k.load(a.k, t * a.k_stride + (int64_t)h * D + 16 * sub, a.wide);
+        v.load(a.v, t * a.v_stride + (int64_t)h * D + 16 * sub, a.wide);
     }
     if (slot >= a.num_slots || slot < -1) {
         if (sub == 0) set_error(a.err, TQ_DEVERR_SLOT);
@@ -185,13 +203,14 @@ struct I4LoadArgs {
     int batch, heads, max_blocks;
     int64_t num_blocks, n_rows;
     void *k, *v;
+    bool wide;  // rows start at multiples of 32 bytes
     uint32_t* err;
 };
 
 constexpr int kI4LoadThreads = 256;
 
 template <int OT>
-__device__ __forceinline__ void i4_put16(void* base, int64_t off, uint2 codes, float scale) {
+__device__ __forceinline__ void i4_put16(void* base, int64_t off, uint2 codes, float scale, bool wide) {
     float f[16];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -200,7 +219,25 @@ __device__ __forceinline__ void i4_put16(void* base, int64_t off, uint2 codes, f
             const float2 x = __half22float2(i4_pair(j ? codes.y : codes.x, i));
             f[8 * j + i] = x.x * scale, f[8 * j + 4 + i] = x.y * scale;
         }
-    f8_store16(base, off, f, OT);
+    if (!wide) {
+        f8_store16(base, off, f, OT);
+        return;
+    }
+    uint4 w[OT == TQ_DTYPE_F32 ? 4 : 2];
+    if constexpr (OT == TQ_DTYPE_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                              __float_as_uint(f[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = make_uint4(f8_pack16(f[8 * i], f[8 * i + 1], OT), f8_pack16(f[8 * i + 2], f[8 * i + 3], OT),
+                              f8_pack16(f[8 * i + 4], f[8 * i + 5], OT), f8_pack16(f[8 * i + 6], f[8 * i + 7], OT));
+    }
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + off * (OT == TQ_DTYPE_F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (OT == TQ_DTYPE_F32 ? 4 : 2); i += 2) i4_store32(p + i, w[i], w[i + 1]);
 }
 
 template <int D, int OT>
@@ -259,7 +296,7 @@ __global__ void __launch_bounds__(kI4LoadThreads) i4_load_kernel(I4LoadArgs a) {
                         continue;
                     }
                     // (exact: multiples of 2^-144, at most 2^127)
-                    i4_put16<OT>(r < 16 ? a.k : a.v, (row * a.heads + h) * D + 16 * ch, c[j], i4_scale(sb[j]) * scale);
+                    i4_put16<OT>(r < 16 ? a.k : a.v, (row * a.heads + h) * D + 16 * ch, c[j], i4_scale(sb[j]) * scale, a.wide);
                 }
             }
             done += units;
@@ -369,6 +406,7 @@ tq_status tq_i4_store(const tq_i4_cache* c, const void* k, const void* v, int in
     a.cache = static_cast<uint8_t*>(cache_buf);
     a.num_slots = c->cfg.num_blocks * kBlock;
     a.heads = c->cfg.num_kv_heads;
+    a.wide = !(((uintptr_t)k | (uintptr_t)v | (uintptr_t)(k_stride * sz) | (uintptr_t)(v_stride * sz)) & 31);
     a.err = c->err;
     cudaStream_t s = (cudaStream_t)stream;
     if (c->cfg.head_dim == 128)
@@ -399,6 +437,7 @@ tq_status tq_i4_load(const tq_i4_cache* c, const void* cache_buf, const int32_t*
     a.n_rows = n_rows;
     a.k = k_out;
     a.v = v_out;
+    a.wide = !(((uintptr_t)k_out | (uintptr_t)v_out) & 31);
     a.err = c->err;
     cudaStream_t s = (cudaStream_t)stream;
     if (c->cfg.head_dim == 128)

@@ -4,7 +4,10 @@
 //
 // d/16 lanes hold a head, 16 elements each: for a rotated part the two pieces of 8
 // whose elements (or, interleaved, whose halves) are paired, so that a rotation needs
-// no exchange; elsewhere two neighbouring pieces.
+// no exchange; elsewhere two neighbouring pieces.  A warp takes a token, 4 (d = 128) or 2
+// heads at a time, and computes the token's sines once, each lane some of those that
+// the lanes beside it with the same pieces need, too.  With few tokens a token's heads go
+// to several warps.  Bound by memory (every element in and out once).
 //
 // A pair turns by F 2^-64 of a full turn a position, F = its frequency / 2 pi in
 // 64-bit fixed point, so position * F modulo 2^64 is the angle, reduced without any
@@ -35,27 +38,43 @@ struct NormRopeArgs {
     uint32_t* err;
     float eps;
     int q_heads, kv_heads, rot, interleaved, norm, w_dtype;
+    int parts;  // warps per token
 };
 
 constexpr int kRopeThreads = 128;
 
-// 8 elements of any dtype, in fp32
+// 8 elements, as they lie in memory
 template <int DT>
-__device__ __forceinline__ void rope_load8(const void* base, int64_t i, float* x) {
-    if constexpr (DT == TQ_DTYPE_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-        const float4 a = p[0], b = p[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct RopeRaw {
+    static constexpr int N = DT == TQ_DTYPE_F32 ? 2 : 1;
+    uint4 w[N];
+    __device__ __forceinline__ void load(const void* base, int64_t i) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (DT == TQ_DTYPE_F32 ? 4 : 2));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = DT == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(u[j]) : F8Elem::from_f16x2(u[j]);
-            x[2 * j] = f.x, x[2 * j + 1] = f.y;
+        for (int j = 0; j < N; ++j) w[j] = p[j];
+    }
+    __device__ __forceinline__ void store(void* base, int64_t i) const {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + i * (DT == TQ_DTYPE_F32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = w[j];
+    }
+    __device__ __forceinline__ void values(float* x) const {
+        if constexpr (DT == TQ_DTYPE_F32) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[4 * j] = __uint_as_float(w[j].x), x[4 * j + 1] = __uint_as_float(w[j].y);
+                x[4 * j + 2] = __uint_as_float(w[j].z), x[4 * j + 3] = __uint_as_float(w[j].w);
+            }
+        } else {
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = DT == TQ_DTYPE_BF16 ? F8Elem::from_bf16x2(u[j]) : F8Elem::from_f16x2(u[j]);
+                x[2 * j] = f.x, x[2 * j + 1] = f.y;
+            }
         }
     }
-}
+};
 template <int DT>
 __device__ __forceinline__ void rope_store8(void* base, int64_t i, const float* x) {
     if constexpr (DT == TQ_DTYPE_F32) {
@@ -68,117 +87,189 @@ __device__ __forceinline__ void rope_store8(void* base, int64_t i, const float* 
     }
 }
 
-template <int D, int DT>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-    constexpr int LPV = D / 16;
-    const int sub = threadIdx.x % LPV;
-    const int heads = a.q_heads + a.kv_heads * (a.v ? 2 : 1);
-    const int64_t vec = (int64_t)blockIdx.x * (kRopeThreads / LPV) + threadIdx.x / LPV;
-    const int64_t t = vec / heads;
-    const int h = (int)(vec - t * heads);
-    pdl_wait();
-    const bool here = t < a.n_tokens;
-    const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.kv_heads ? 1 : 2;
-    int64_t row = t;
-    if (here && kind && a.rows) {
-        row = __ldg(a.rows + t);
-        if (row < -1 || row >= a.n_rows) {
-            if (sub == 0) set_error(a.err, TQ_DEVERR_CHUNK);
-            row = -1;
-        }
-    }
-    // the lane's two pieces of 8
-    const int rp = a.rot / 16;
-    const bool turned = sub < rp && kind < 2;
-    const int p0 = sub < rp ? sub : 2 * sub, p1 = sub < rp ? sub + rp : 2 * sub + 1;
-    const int hk = kind == 0 ? h : h - a.q_heads - (kind == 2 ? a.kv_heads : 0);
-    const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const int64_t from = t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)hk * D;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (here) {
-        rope_load8<DT>(src, from + 8 * p0, x);
-        rope_load8<DT>(src, from + 8 * p1, x + 8);
-    }
-    if (a.norm && kind < 2) {
-        auto squares = [&]() {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            return ss;
-        };
-        float ss = squares(), eps = a.eps;
-        // Squares that leave fp32's range: once more with x 2^-e, the larger of sqrt(eps)
-        // and the largest element near 1 (0, infinities and NaN stay what they are)
-        const bool far = !(ss < INFINITY) || fmaf(ss, 1.f / D, eps) < 0x1p-100f;
-        if (__any_sync(0xffffffffu, far)) {
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
-#pragma unroll
-            for (int o = LPV / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = fmaxf(top, sqrtf(eps));
-            if (far && top > 0.f && top < INFINITY) {
-                const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e), subnormal for the largest
-                const float f = __uint_as_float(e < 254u ? (254u - max(e, 1u)) << 23 : 0x00400000u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= f;
-                eps = eps * f * f;
-            }
-            const float again = squares();  // (whole warps)
-            if (far) ss = again;
-        }
-        const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-        const void* w = kind == 0 ? a.qw : a.kw;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= r;
-        if (w) {
-            float g[16];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = 8 * (j ? p1 : p0);
-                if (a.w_dtype == TQ_DTYPE_F32) rope_load8<TQ_DTYPE_F32>(w, at, g + 8 * j);
-                else if (a.w_dtype == TQ_DTYPE_BF16) rope_load8<TQ_DTYPE_BF16>(w, at, g + 8 * j);
-                else rope_load8<TQ_DTYPE_F16>(w, at, g + 8 * j);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= g[i];
-        }
-    }
-    if (here && turned) {
-        const uint64_t p = (uint64_t)(int64_t)__ldg(a.pos + t);
-        auto turn = [&](int pair, float& u, float& w) {
-            const int32_t part = (int32_t)((p * __ldg(a.turns + pair)) >> 32);
-            float c, s;
-            sincospif((float)part * 0x1p-31f, &s, &c);
-            const float uu = u, ww = w;
-            u = fmaf(uu, c, -ww * s);
-            w = fmaf(ww, c, uu * s);
-        };
-        if (a.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) turn(4 * (i < 4 ? p0 : p1) + (i & 3), x[2 * i], x[2 * i + 1]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) turn(8 * p0 + i, x[i], x[8 + i]);
-        }
-    }
-    if (!here || row < 0) return;
-    void* dst = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
-    const int64_t to = row * (kind == 0 ? a.qo_stride : kind == 1 ? a.ko_stride : a.vo_stride) + (int64_t)hk * D;
-    rope_store8<DT>(dst, to + 8 * p0, x);
-    rope_store8<DT>(dst, to + 8 * p1, x + 8);
+// sine and cosine of position p for one pair
+__device__ __forceinline__ float2 rope_turn(uint64_t p, uint64_t turns) {
+    const int32_t part = (int32_t)((p * turns) >> 32);  // of a full turn, in 2^-32
+    float s, c;
+    sincospif((float)part * 0x1p-31f, &s, &c);
+    return make_float2(s, c);
 }
 
 template <int D, int DT>
-static tq_status launch_norm_rope(const NormRopeArgs& a, cudaStream_t s) {
-    const int heads = a.q_heads + a.kv_heads * (a.v ? 2 : 1);
-    constexpr int VPB = kRopeThreads / (D / 16);
-    if (a.n_tokens > (int64_t)0x7FFFFFFF * VPB / heads - VPB) return TQ_ERR_INVALID_ARG;
-    const int64_t blocks = (a.n_tokens * heads + VPB - 1) / VPB;
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+    constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes per head, heads at a time
+    constexpr int U = DT == TQ_DTYPE_F32 ? 2 : 4;  // steps whose loads are under way together
+    const int lane = threadIdx.x & 31, sub = lane % LPV, slot = lane / LPV;
+    const int64_t item = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = item / a.parts;
+    if (t >= a.n_tokens) return;  // (whole warps)
+    const int part = (int)(item - t * a.parts);
+    // this warp's steps: VPW heads of q, of k or of v each
+    const int nq = (a.q_heads + VPW - 1) / VPW, nk = (a.kv_heads + VPW - 1) / VPW, all = nq + (a.v ? 2 : 1) * nk;
+    const int i0 = (int)((int64_t)all * part / a.parts), i1 = (int)((int64_t)all * (part + 1) / a.parts);
+    // the lane's two pieces of 8
+    const int rp = a.rot / 16;
+    const bool turned = sub < rp;
+    const int p0 = turned ? sub : 2 * sub, p1 = turned ? sub + rp : 2 * sub + 1;
+    // its share of the turns: pairs VPS slot .. of the eight that its pieces need (they
+    // never change, so they can be read before the previous kernel's end)
+    constexpr int VPS = 8 / VPW;
+    uint64_t turns[VPS] = {};
+    const bool sines = rp > 0 && i0 < nq + nk;
+    auto pair = [&](int i) { return a.interleaved ? 4 * (i < 4 ? p0 : p1) + (i & 3) : 8 * p0 + i; };
+    if (sines && turned)
+#pragma unroll
+        for (int i = 0; i < VPS; ++i) turns[i] = __ldg(a.turns + pair(VPS * slot + i));
+    pdl_wait();  // (the launch overlaps the previous kernel's end)
+
+    int64_t row = t;
+    if (a.rows) {
+        row = a.rows[t];
+        if (row < -1 || row >= a.n_rows) {
+            if (lane == 0) set_error(a.err, TQ_DEVERR_CHUNK);
+            row = -1;
+        }
+    }
+    float sn[8], cs[8];
+    if (sines) {
+        const uint64_t p = (uint64_t)(int64_t)a.pos[t];
+        float2 mine[VPS];
+#pragma unroll
+        for (int i = 0; i < VPS; ++i) mine[i] = rope_turn(p, turns[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            sn[i] = __shfl_sync(0xffffffffu, mine[i % VPS].x, i / VPS * LPV + sub);
+            cs[i] = __shfl_sync(0xffffffffu, mine[i % VPS].y, i / VPS * LPV + sub);
+        }
+    }
+
+    float w[16];  // the weights of kind wk
+    int wk = -1;
+#pragma unroll 1
+    for (int ib = i0; ib < i1; ib += U) {
+        RopeRaw<DT> raw[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ib + u, kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
+            const int h = (i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * VPW + slot;
+            if (i >= i1 || h >= (kind ? a.kv_heads : a.q_heads) || (kind && row < 0)) {
+#pragma unroll
+                for (int j = 0; j < RopeRaw<DT>::N; ++j) raw[u][0].w[j] = raw[u][1].w[j] = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+            const int64_t from = t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)h * D;
+            raw[u][0].load(src, from + 8 * p0);
+            raw[u][1].load(src, from + 8 * p1);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = ib + u, kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
+            if (i >= i1 || (kind && row < 0)) continue;  // (the same for the whole warp)
+            const int h = (i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * VPW + slot;
+            const bool here = h < (kind ? a.kv_heads : a.q_heads);
+            void* dst = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
+            const int64_t to = (kind ? row : t) * (kind == 0 ? a.qo_stride : kind == 1 ? a.ko_stride : a.vo_stride) + (int64_t)h * D;
+            if (kind == 2) {
+                if (here) raw[u][0].store(dst, to + 8 * p0), raw[u][1].store(dst, to + 8 * p1);
+                continue;
+            }
+            float x[16];
+            raw[u][0].values(x);
+            raw[u][1].values(x + 8);
+            if (a.norm) {
+                auto squares = [&]() {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+                    for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    return ss;
+                };
+                float ss = squares(), eps = a.eps;
+                // Squares that leave fp32's range: once more with x 2^-e, the larger of sqrt(eps)
+                // and the largest element near 1 (0, infinities and NaN stay what they are)
+                const bool far = !(ss < INFINITY) || fmaf(ss, 1.f / D, eps) < 0x1p-100f;
+                if (__any_sync(0xffffffffu, far)) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+                    for (int o = LPV / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    top = fmaxf(top, sqrtf(eps));
+                    if (far && top > 0.f && top < INFINITY) {
+                        const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e), subnormal for the largest
+                        const float f = __uint_as_float(e < 254u ? (254u - max(e, 1u)) << 23 : 0x00400000u);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] *= f;
+                        eps = eps * f * f;
+                    }
+                    const float again = squares();  // (whole warps)
+                    if (far) ss = again;
+                }
+                const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
+                const void* g = kind == 0 ? a.qw : a.kw;
+                if (wk != kind) {
+                    wk = kind;
+                    if (g) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int at = 8 * (j ? p1 : p0);
+                            if (a.w_dtype == TQ_DTYPE_F32) {
+                                RopeRaw<TQ_DTYPE_F32> z;
+                                z.load(g, at);
+                                z.values(w + 8 * j);
+                            } else if (a.w_dtype == TQ_DTYPE_BF16) {
+                                RopeRaw<TQ_DTYPE_BF16> z;
+                                z.load(g, at);
+                                z.values(w + 8 * j);
+                            } else {
+                                RopeRaw<TQ_DTYPE_F16> z;
+                                z.load(g, at);
+                                z.values(w + 8 * j);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = 1.f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
+            }
+            if (turned) {
+                auto turn = [&](int j, float& y, float& z) {
+                    const float yy = y, zz = z;
+                    y = fmaf(yy, cs[j], -zz * sn[j]);
+                    z = fmaf(zz, cs[j], yy * sn[j]);
+                };
+                if (a.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) turn(j, x[2 * j], x[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) turn(j, x[j], x[8 + j]);
+                }
+            }
+            if (here) {
+                rope_store8<DT>(dst, to + 8 * p0, x);
+                rope_store8<DT>(dst, to + 8 * p1, x + 8);
+            }
+        }
+    }
+}
+
+template <int D, int DT>
+static tq_status launch_norm_rope(NormRopeArgs a, cudaStream_t s) {
+    constexpr int VPW = 32 / (D / 16), W = kRopeThreads / 32;
+    int sms = 0;
+    const tq_status st = device_sms(&sms);
+    if (st != TQ_OK) return st;
+    // a warp per token, or as many as give every SM 16 warps
+    const int64_t steps = (a.q_heads + VPW - 1) / VPW + (a.v ? 2 : 1) * (int64_t)((a.kv_heads + VPW - 1) / VPW);
+    a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(steps, 16 * (int64_t)sms / a.n_tokens));
+    if (a.n_tokens > ((int64_t)0x7FFFFFFF - 1) * W / a.parts) return TQ_ERR_INVALID_ARG;
+    const int64_t blocks = (a.n_tokens * a.parts + W - 1) / W;
     return cuda_status(launch_pdl(true, norm_rope_kernel<D, DT>, dim3((unsigned)blocks), dim3(kRopeThreads), 0, s, a));
 }
 
