@@ -38,7 +38,8 @@ struct NormRopeArgs {
     uint32_t* err;
     float eps;
     int q_heads, kv_heads, rot, interleaved, norm, w_dtype;
-    int parts;  // warps per token
+    int parts;  // warps (many tokens: pieces) per token
+    int slice;  // heads per piece
 };
 
 constexpr int kRopeThreads = 128;
@@ -48,15 +49,30 @@ template <int DT>
 struct RopeRaw {
     static constexpr int N = DT == TQ_DTYPE_F32 ? 2 : 1;
     uint4 w[N];
-    __device__ __forceinline__ void load(const void* base, int64_t i) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (DT == TQ_DTYPE_F32 ? 4 : 2));
+    __device__ __forceinline__ void load(const void* base, int64_t bytes) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + bytes);
 #pragma unroll
         for (int j = 0; j < N; ++j) w[j] = p[j];
     }
-    __device__ __forceinline__ void store(void* base, int64_t i) const {
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + i * (DT == TQ_DTYPE_F32 ? 4 : 2));
+    __device__ __forceinline__ void store(void* base, int64_t bytes) const {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + bytes);
 #pragma unroll
         for (int j = 0; j < N; ++j) p[j] = w[j];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void set(const float* x) {
+        if constexpr (DT == TQ_DTYPE_F32) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[j] = make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]), __float_as_uint(x[4 * j + 2]),
+                                  __float_as_uint(x[4 * j + 3]));
+        } else {
+            w[0] = make_uint4(f8_pack16(x[0], x[1], DT), f8_pack16(x[2], x[3], DT), f8_pack16(x[4], x[5], DT),
+                              f8_pack16(x[6], x[7], DT));
+        }
     }
     __device__ __forceinline__ void values(float* x) const {
         if constexpr (DT == TQ_DTYPE_F32) {
@@ -75,16 +91,59 @@ struct RopeRaw {
         }
     }
 };
-template <int DT>
-__device__ __forceinline__ void rope_store8(void* base, int64_t i, const float* x) {
-    if constexpr (DT == TQ_DTYPE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+// 8 weights from element `at` on
+__device__ __forceinline__ void rope_weights(const void* g, int at, int dtype, float* w) {
+    if (dtype == TQ_DTYPE_F32) {
+        RopeRaw<TQ_DTYPE_F32> z;
+        z.load(g, at * 4);
+        z.values(w);
+    } else if (dtype == TQ_DTYPE_BF16) {
+        RopeRaw<TQ_DTYPE_BF16> z;
+        z.load(g, at * 2);
+        z.values(w);
     } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
-            make_uint4(f8_pack16(x[0], x[1], DT), f8_pack16(x[2], x[3], DT), f8_pack16(x[4], x[5], DT), f8_pack16(x[6], x[7], DT));
+        RopeRaw<TQ_DTYPE_F16> z;
+        z.load(g, at * 2);
+        z.values(w);
     }
+}
+
+// sums over the d/16 lanes of a head of U heads' values, the exchanges side by side
+template <int LPV, int U>
+__device__ __forceinline__ void rope_sums(float (&v)[U]) {
+#pragma unroll
+    for (int o = LPV / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+}
+__device__ __forceinline__ float rope_squares(const float (&x)[16]) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) s[0] = fmaf(x[j], x[j], s[0]), s[1] = fmaf(x[j + 1], x[j + 1], s[1]);
+    return s[0] + s[1];
+}
+// Squares that leave fp32's range: the mean square of x 2^-e, with x 2^-e in place of x
+// and eps 4^-e added, the larger of sqrt(eps) and the largest element near 1 (0,
+// infinities and NaN stay what they are).  Whole warps; `far`: this lane's head
+template <int D>
+__device__ __forceinline__ float rope_far(float (&x)[16], float mean, float eps, bool far) {
+    constexpr int LPV = D / 16;
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+    for (int o = LPV / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, sqrtf(eps));
+    if (far && top > 0.f && top < INFINITY) {
+        const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e), subnormal for the largest
+        const float f = __uint_as_float(e < 254u ? (254u - max(e, 1u)) << 23 : 0x00400000u);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= f;
+        eps = eps * f * f;
+    }
+    float ss[1] = {rope_squares(x)};
+    rope_sums<LPV>(ss);
+    return far ? fmaf(ss[0], 1.f / D, eps) : mean;
 }
 
 // sine and cosine of position p for one pair
@@ -98,7 +157,7 @@ __device__ __forceinline__ float2 rope_turn(uint64_t p, uint64_t turns) {
 template <int D, int DT>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes per head, heads at a time
-    constexpr int U = DT == TQ_DTYPE_F32 ? 2 : 4;  // steps whose loads are under way together
+    constexpr int U = 2;  // steps whose loads are under way together
     const int lane = threadIdx.x & 31, sub = lane % LPV, slot = lane / LPV;
     const int64_t item = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int64_t t = item / a.parts;
@@ -143,128 +202,391 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
         }
     }
 
-    float w[16];  // the weights of kind wk
-    int wk = -1;
+    constexpr int SZ = DT == TQ_DTYPE_F32 ? 4 : 2;
+    const int64_t second = (int64_t)(p1 - p0) * 8 * SZ;  // bytes from a lane's first piece to its second
 #pragma unroll 1
-    for (int ib = i0; ib < i1; ib += U) {
-        RopeRaw<DT> raw[U][2];
+    for (int kind = 0, start = 0; kind < (a.v ? 3 : 2); ++kind) {
+        const int heads = kind ? a.kv_heads : a.q_heads, n = kind ? nk : nq;
+        const int lo = max(i0 - start, 0), hi = min(i1 - start, n);
+        start += n;
+        if (lo >= hi || (kind && row < 0)) continue;
+        const void* in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        void* out = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
+        const int64_t lane_at = (int64_t)(lo * VPW + slot) * D + 8 * p0;
+        const uint8_t* src = static_cast<const uint8_t*>(in) + SZ * (t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + lane_at);
+        uint8_t* dst = static_cast<uint8_t*>(out) + SZ * ((kind ? row : t) * (kind == 0 ? a.qo_stride : kind == 1 ? a.ko_stride : a.vo_stride) + lane_at);
+        int h = lo * VPW + slot;
+        // (a, b) of a pair, times the norm's factor, becomes (fc a - gs b, gc b + fs a): weights times sines
+        float fc[8], gc[8], fs[8], gs[8];
+        if (kind < 2) {
+            float w[16];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = ib + u, kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
-            const int h = (i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * VPW + slot;
-            if (i >= i1 || h >= (kind ? a.kv_heads : a.q_heads) || (kind && row < 0)) {
+            for (int j = 0; j < 16; ++j) w[j] = 1.f;
+            const void* g = a.norm ? kind == 0 ? a.qw : a.kw : nullptr;
+            if (g)
 #pragma unroll
-                for (int j = 0; j < RopeRaw<DT>::N; ++j) raw[u][0].w[j] = raw[u][1].w[j] = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-            }
-            const void* src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-            const int64_t from = t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)h * D;
-            raw[u][0].load(src, from + 8 * p0);
-            raw[u][1].load(src, from + 8 * p1);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = ib + u, kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
-            if (i >= i1 || (kind && row < 0)) continue;  // (the same for the whole warp)
-            const int h = (i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * VPW + slot;
-            const bool here = h < (kind ? a.kv_heads : a.q_heads);
-            void* dst = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
-            const int64_t to = (kind ? row : t) * (kind == 0 ? a.qo_stride : kind == 1 ? a.ko_stride : a.vo_stride) + (int64_t)h * D;
-            if (kind == 2) {
-                if (here) raw[u][0].store(dst, to + 8 * p0), raw[u][1].store(dst, to + 8 * p1);
-                continue;
-            }
-            float x[16];
-            raw[u][0].values(x);
-            raw[u][1].values(x + 8);
-            if (a.norm) {
-                auto squares = [&]() {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-                    for (int o = LPV / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    return ss;
-                };
-                float ss = squares(), eps = a.eps;
-                // Squares that leave fp32's range: once more with x 2^-e, the larger of sqrt(eps)
-                // and the largest element near 1 (0, infinities and NaN stay what they are)
-                const bool far = !(ss < INFINITY) || fmaf(ss, 1.f / D, eps) < 0x1p-100f;
-                if (__any_sync(0xffffffffu, far)) {
-                    float top = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-                    for (int o = LPV / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    top = fmaxf(top, sqrtf(eps));
-                    if (far && top > 0.f && top < INFINITY) {
-                        const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e), subnormal for the largest
-                        const float f = __uint_as_float(e < 254u ? (254u - max(e, 1u)) << 23 : 0x00400000u);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] *= f;
-                        eps = eps * f * f;
-                    }
-                    const float again = squares();  // (whole warps)
-                    if (far) ss = again;
+                for (int j = 0; j < 2; ++j) {
+                    const int at = 8 * (j ? p1 : p0);
+                    rope_weights(g, at, a.w_dtype, w + 8 * j);
                 }
-                const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-                const void* g = kind == 0 ? a.qw : a.kw;
-                if (wk != kind) {
-                    wk = kind;
-                    if (g) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int at = 8 * (j ? p1 : p0);
-                            if (a.w_dtype == TQ_DTYPE_F32) {
-                                RopeRaw<TQ_DTYPE_F32> z;
-                                z.load(g, at);
-                                z.values(w + 8 * j);
-                            } else if (a.w_dtype == TQ_DTYPE_BF16) {
-                                RopeRaw<TQ_DTYPE_BF16> z;
-                                z.load(g, at);
-                                z.values(w + 8 * j);
-                            } else {
-                                RopeRaw<TQ_DTYPE_F16> z;
-                                z.load(g, at);
-                                z.values(w + 8 * j);
-                            }
+            for (int j = 0; j < 8; ++j) {
+                const float f = a.interleaved ? w[2 * j] : w[j], g2 = a.interleaved ? w[2 * j + 1] : w[8 + j];
+                fc[j] = turned ? f * cs[j] : f, gc[j] = turned ? g2 * cs[j] : g2;
+                fs[j] = f * sn[j], gs[j] = g2 * sn[j];
+            }
+        }
+#pragma unroll 1
+        for (int i = lo; i < hi; i += U) {
+            RopeRaw<DT> raw[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u < hi && h + u * VPW < heads) {
+                    raw[u][0].load(src, (int64_t)u * VPW * D * SZ);
+                    raw[u][1].load(src + second, (int64_t)u * VPW * D * SZ);
+                } else {
+                    raw[u][0].clear();
+                    raw[u][1].clear();
+                }
+            }
+            float mean[U];  // with eps
+            bool far = false;
+            if (kind < 2 && a.norm) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[16];
+                    raw[u][0].values(x);
+                    raw[u][1].values(x + 8);
+                    mean[u] = rope_squares(x);
+                }
+                rope_sums<LPV>(mean);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool inf = !(mean[u] < INFINITY);
+                    mean[u] = fmaf(mean[u], 1.f / D, a.eps);
+                    far |= inf || mean[u] < 0x1p-100f;
+                }
+                far = __any_sync(0xffffffffu, far);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= hi) break;  // (the same for the whole warp)
+                const bool here = h + u * VPW < heads;
+                if (kind < 2) {
+                    float x[16], r = 1.f;
+                    raw[u][0].values(x);
+                    raw[u][1].values(x + 8);
+                    if (a.norm) {
+                        if (far) mean[u] = rope_far<D>(x, mean[u], a.eps, !(mean[u] < INFINITY) || mean[u] < 0x1p-100f);
+                        r = rsqrtf(mean[u]);
+                    }
+                    auto turn = [&](int j, float& y, float& z) {
+                        const float yy = y * r, zz = z * r;  // (first: small elements may be subnormal)
+                        if (turned) {
+                            y = fmaf(yy, fc[j], -zz * gs[j]);
+                            z = fmaf(zz, gc[j], yy * fs[j]);
+                        } else {
+                            y = yy * fc[j];
+                            z = zz * gc[j];
                         }
+                    };
+                    if (a.interleaved) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) turn(j, x[2 * j], x[2 * j + 1]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = 1.f;
+                        for (int j = 0; j < 8; ++j) turn(j, x[j], x[8 + j]);
                     }
+                    raw[u][0].set(x);
+                    raw[u][1].set(x + 8);
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = x[j] * r * w[j];
-            }
-            if (turned) {
-                auto turn = [&](int j, float& y, float& z) {
-                    const float yy = y, zz = z;
-                    y = fmaf(yy, cs[j], -zz * sn[j]);
-                    z = fmaf(zz, cs[j], yy * sn[j]);
-                };
-                if (a.interleaved) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) turn(j, x[2 * j], x[2 * j + 1]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) turn(j, x[j], x[8 + j]);
+                if (here) {
+                    raw[u][0].store(dst, (int64_t)u * VPW * D * SZ);
+                    raw[u][1].store(dst + second, (int64_t)u * VPW * D * SZ);
                 }
             }
-            if (here) {
-                rope_store8<DT>(dst, to + 8 * p0, x);
-                rope_store8<DT>(dst, to + 8 * p1, x + 8);
+            src += (int64_t)U * VPW * D * SZ;
+            dst += (int64_t)U * VPW * D * SZ;
+            h += U * VPW;
+        }
+    }
+}
+
+// ------------------------------------------------------------ many tokens
+// Resident blocks take pieces of tokens' rows in turn (all heads of q, k and v, where they
+// fit).  A piece comes into a ring in shared memory by bulk copies, is worked on in
+// place, and leaves by bulk copies, so that enough bytes are under way whatever the
+// warps do; v is not touched at all.  The sines of the next piece are computed beside,
+// one pair per thread.  Arithmetic on pairs
+// of elements (fma.rn.f32x2).
+constexpr int kRopeStages = 3, kRopeBulkWarps = 4, kRopeBulkCtas = 5;
+constexpr int kRopePieceBytes = 13312;  // of a stage: 5 blocks of 3 stages share an SM
+// This kernel is taken from so many pieces per SM and bytes of a piece on.  32/8 heads,
+// d = 128, bf16 (12 KB): 152 tokens 3.3 us here, 3.0 by the other one; 304 3.6, 3.9; 1216
+// 6.6, 7.6; 4864 22.0, 27.1.  64/8 heads (2 x 10 KB): 152 3.4, 3.5; 4864 33.8, 41.2.
+// 8/1 heads (2.5 KB): 1216 4.4, 3.8; 2432 6.6, 5.5; 4864 10.9, 11.3.
+constexpr int kRopeBulkFrom = 2, kRopeBulkLeast = 6144;
+
+__device__ __forceinline__ uint64_t rope_pack(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 rope_unpack(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t rope_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t rope_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void rope_bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// cosines and sines of a token's pairs
+struct __align__(16) RopeSines {
+    float c[128], s[128];
+};
+
+template <int D, int DT>
+__global__ void __launch_bounds__(32 * kRopeBulkWarps, kRopeBulkCtas) norm_rope_bulk_kernel(const __grid_constant__ NormRopeArgs a) {
+    constexpr int LPV = D / 16, VPW = 32 / LPV, SZ = DT == TQ_DTYPE_F32 ? 4 : 2, HB = D * SZ, S = kRopeStages, W = kRopeBulkWarps;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RopeSines s_sines[2];
+    __shared__ __align__(16) float s_w[D];  // the keys' weights
+    __shared__ uint64_t s_bars[S];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LPV, slot = lane / LPV;
+    const int all = a.q_heads + a.kv_heads * (a.v ? 2 : 1), end_k = a.q_heads + a.kv_heads;
+    const int rp = a.rot / 16;
+    const bool turned = sub < rp;
+    const int p0 = turned ? sub : 2 * sub, p1 = turned ? sub + rp : 2 * sub + 1;
+    // this block's pieces: a.slice heads of the row [q | k | v] of a token each (grid <= pieces)
+    const int64_t pieces = a.n_tokens * a.parts;
+    const int count = (int)((pieces - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    struct Piece {
+        int64_t t;
+        int h0, h1;  // heads of the row
+    };
+    // from piece to piece without a division
+    const int step_t = (int)(gridDim.x / (unsigned)a.parts), step_h = (int)(gridDim.x % (unsigned)a.parts) * a.slice;
+    auto next = [&](Piece& c) {
+        c.t += step_t;
+        c.h0 += step_h;
+        if (c.h0 >= a.parts * a.slice) c.h0 -= a.parts * a.slice, ++c.t;
+        c.h1 = min(c.h0 + a.slice, all);
+    };
+    Piece c;  // the piece worked on
+    c.t = blockIdx.x / (unsigned)a.parts;
+    c.h0 = (int)(blockIdx.x % (unsigned)a.parts) * a.slice;
+    c.h1 = min(c.h0 + a.slice, all);
+    Piece ahead = c, coming = c;  // the next to be fetched (thread 0), the next to be worked on
+    const uint64_t turns = tid < a.rot / 2 ? __ldg(a.turns + tid) : 0;  // (they never change)
+    const uint32_t bars = smem_u32(s_bars);
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_wait();  // (the launch overlaps the previous kernel's end)
+
+    // the parts of a piece in q, in k and in v: `copy(kind, first head of it, heads, byte in the piece)`
+    auto parts = [&](const Piece& c, auto copy) {
+        if (c.h0 < a.q_heads) copy(0, c.h0, min(c.h1, a.q_heads) - c.h0, 0);
+        const int k0 = max(c.h0, a.q_heads), k1 = min(c.h1, end_k);
+        if (k0 < k1) copy(1, k0 - a.q_heads, k1 - k0, (k0 - c.h0) * HB);
+        const int v0 = max(c.h0, end_k);
+        if (v0 < c.h1) copy(2, v0 - end_k, c.h1 - v0, (v0 - c.h0) * HB);
+    };
+    // thread 0: the next piece, k, into stage k % S
+    auto fetch = [&](int k) {
+        const uint32_t bar = bars + 8 * (k % S), to = smem_u32(ring) + (k % S) * (a.slice * HB);
+        mbar_expect_tx(bar, (ahead.h1 - ahead.h0) * HB);
+        parts(ahead, [&](int kind, int h, int n, int at) {
+            const void* in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+            const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+            bulk_copy(to + at, static_cast<const uint8_t*>(in) + ahead.t * stride * SZ + (int64_t)h * HB, n * HB, bar);
+        });
+        next(ahead);
+    };
+    int fetched = min(count, S - 1), waited = 0;
+    if (tid == 0)
+        for (int k = 0; k < fetched; ++k) fetch(k);
+    for (int i = 8 * tid; i < D; i += 256 * W) {
+        float z[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+        if (a.kw) rope_weights(a.kw, i, a.w_dtype, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_w[i + j] = z[j];
+    }
+    uint64_t wq[8];  // the queries', of the lane's elements
+    {
+        float z[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] = 1.f;
+        if (a.qw) rope_weights(a.qw, 8 * p0, a.w_dtype, z), rope_weights(a.qw, 8 * p1, a.w_dtype, z + 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wq[j] = rope_pack(z[2 * j], z[2 * j + 1]);
+    }
+    auto sines = [&](int k, int p) {
+        if (tid >= a.rot / 2) return;
+        const float2 t = rope_turn((uint64_t)(int64_t)p, turns);
+        RopeSines& o = s_sines[k & 1];
+        o.s[tid] = t.x, o.c[tid] = t.y;
+    };
+    sines(0, a.pos[c.t]);
+    int64_t row = a.rows ? a.rows[c.t] : c.t;
+    next(coming);
+    int pos = count > 1 ? a.pos[coming.t] : 0;
+    __syncthreads();
+
+    bool dead = false;
+    for (int k = 0; k < count; ++k) {
+        const int stage = k % S;
+        if (!dead) dead = !mbar_wait(bars + 8 * stage, (k / S) & 1, a.err);
+        if (!dead) waited = k + 1;
+        const int64_t next_row = k + 1 < count ? a.rows ? a.rows[coming.t] : coming.t : 0;
+        uint8_t* base = ring + stage * (a.slice * HB);
+        const RopeSines& sc = s_sines[k & 1];
+        uint64_t cs[4] = {}, sn[4] = {};  // the lane's sines (interleaved: one of a pair in each)
+        if (turned) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int pr = a.interleaved ? 4 * (j < 2 ? p0 : p1) + 2 * (j & 1) : 8 * p0 + 2 * j;
+                cs[j] = *reinterpret_cast<const uint64_t*>(sc.c + pr);
+                sn[j] = *reinterpret_cast<const uint64_t*>(sc.s + pr);
             }
         }
+        // VPW heads from h on, with the lane's weights in pairs
+        auto work = [&](int h, int top, auto weight) {
+            const bool here = h + slot < top;
+            uint8_t* at = base + ((here ? h + slot : h) - c.h0) * HB;
+            RopeRaw<DT> raw[2];
+            raw[0].load(at, 8 * p0 * SZ);
+            raw[1].load(at, 8 * p1 * SZ);
+            float x[16];
+            raw[0].values(x);
+            raw[1].values(x + 8);
+            if (a.norm) {
+                uint64_t q[2] = {0, 0};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t z = rope_pack(x[2 * j], x[2 * j + 1]);
+                    q[j & 1] = rope_fma2(z, z, q[j & 1]);
+                }
+                const float2 q0 = rope_unpack(q[0]), q1 = rope_unpack(q[1]);
+                float mean[1] = {(q0.x + q0.y) + (q1.x + q1.y)};
+                rope_sums<LPV>(mean);
+                const bool inf = !(mean[0] < INFINITY);
+                mean[0] = fmaf(mean[0], 1.f / D, a.eps);
+                const bool far = inf || mean[0] < 0x1p-100f;
+                if (__any_sync(0xffffffffu, far)) mean[0] = rope_far<D>(x, mean[0], a.eps, far);
+                const float r = rsqrtf(mean[0]);
+                const uint64_t rr = rope_pack(r, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 y = rope_unpack(rope_mul2(rope_mul2(rope_pack(x[2 * j], x[2 * j + 1]), rr), weight(j)));
+                    x[2 * j] = y.x, x[2 * j + 1] = y.y;
+                }
+            }
+            if (turned) {
+                if (a.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 cc = rope_unpack(cs[j / 2]), ss = rope_unpack(sn[j / 2]);
+                        const float y = x[2 * j], z = x[2 * j + 1], co = j & 1 ? cc.y : cc.x, si = j & 1 ? ss.y : ss.x;
+                        x[2 * j] = fmaf(y, co, -z * si);
+                        x[2 * j + 1] = fmaf(z, co, y * si);
+                    }
+                } else {
+                    const uint64_t minus = rope_pack(-1.f, -1.f);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t y = rope_pack(x[2 * j], x[2 * j + 1]), z = rope_pack(x[8 + 2 * j], x[9 + 2 * j]);
+                        const float2 u = rope_unpack(rope_fma2(rope_mul2(z, sn[j]), minus, rope_mul2(y, cs[j])));
+                        const float2 v = rope_unpack(rope_fma2(z, cs[j], rope_mul2(y, sn[j])));
+                        x[2 * j] = u.x, x[2 * j + 1] = u.y, x[8 + 2 * j] = v.x, x[9 + 2 * j] = v.y;
+                    }
+                }
+            }
+            raw[0].set(x);
+            raw[1].set(x + 8);
+            if (here) {
+                raw[0].store(at, 8 * p0 * SZ);
+                raw[1].store(at, 8 * p1 * SZ);
+            }
+        };
+        // the piece's query heads, then its key heads; both in turn to the warps, the last first
+        const int qe = min(c.h1, a.q_heads), ks = max(c.h0, a.q_heads), ke = min(c.h1, end_k);
+        int h = c.h0 + (W - 1 - warp) * VPW;
+        for (; h < qe; h += W * VPW) work(h, qe, [&](int j) { return wq[j]; });
+        // (a step further for each of the warps: h - W VPW was this warp's last of the query heads)
+        if (c.h0 < qe) h = ks + (h - c.h0 - (qe - c.h0 + VPW - 1) / VPW * VPW);
+        for (; h < ke; h += W * VPW)
+            work(h, ke, [&](int j) { return *reinterpret_cast<const uint64_t*>(&s_w[8 * (j < 4 ? p0 : p1) + 2 * (j & 3)]); });
+        if (k + 1 < count) {
+            sines(k + 1, pos);
+            Piece after = coming;
+            next(after);
+            if (k + 2 < count) pos = a.pos[after.t];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();  // the piece's heads and the next one's sines are written
+        if (tid == 0) {
+            const uint32_t from = smem_u32(base);
+            if (row < -1 || (a.rows && row >= a.n_rows)) {
+                if (c.h1 > a.q_heads) set_error(a.err, TQ_DEVERR_CHUNK);
+                row = -1;
+            }
+            if (!dead)
+                parts(c, [&](int kind, int h, int n, int at) {
+                    if (kind && row < 0) return;
+                    void* out = kind == 0 ? a.qo : kind == 1 ? a.ko : a.vo;
+                    const int64_t stride = kind == 0 ? a.qo_stride : kind == 1 ? a.ko_stride : a.vo_stride;
+                    rope_bulk_store(static_cast<uint8_t*>(out) + (kind ? row : c.t) * stride * SZ + (int64_t)h * HB, from + at, n * HB);
+                });
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            // the stage of the piece before this one is free once its heads have left
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            if (!dead && k + S - 1 < count) fetch(k + S - 1), ++fetched;
+        }
+        row = next_row;
+        c = coming;
+        next(coming);
+    }
+    if (tid == 0) {
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        // after a wait that gave up: copies still in flight land before the block ends
+        for (; dead && waited < fetched; ++waited) mbar_wait(bars + 8 * (waited % S), (waited / S) & 1, a.err);
     }
 }
 
 template <int D, int DT>
 static tq_status launch_norm_rope(NormRopeArgs a, cudaStream_t s) {
-    constexpr int VPW = 32 / (D / 16), W = kRopeThreads / 32;
+    constexpr int VPW = 32 / (D / 16), W = kRopeThreads / 32, HB = D * (DT == TQ_DTYPE_F32 ? 4 : 2);
     int sms = 0;
-    const tq_status st = device_sms(&sms);
+    tq_status st = device_sms(&sms);
     if (st != TQ_OK) return st;
+    if (a.n_tokens > (int64_t)1 << 40) return TQ_ERR_INVALID_ARG;
+    // pieces of a token's heads that let kRopeBulkCtas rings share an SM
+    const int64_t heads = a.q_heads + (int64_t)a.kv_heads * (a.v ? 2 : 1);
+    constexpr int most = kRopePieceBytes / HB / VPW * VPW;
+    const int64_t parts = (heads + most - 1) / most;
+    a.slice = (int)(((heads + parts - 1) / parts + VPW - 1) / VPW * VPW);
+    if (a.n_tokens * parts >= kRopeBulkFrom * (int64_t)sms && a.slice * HB >= kRopeBulkLeast) {
+        st = ensure_dynamic_smem((const void*)norm_rope_bulk_kernel<D, DT>, kRopeStages * kRopePieceBytes, "norm_rope_bulk_kernel");
+        if (st != TQ_OK) return st;
+        a.parts = (int)((heads + a.slice - 1) / a.slice);
+        const int64_t grid = std::min<int64_t>(a.n_tokens * a.parts, (int64_t)sms * kRopeBulkCtas);
+        return cuda_status(launch_pdl(true, norm_rope_bulk_kernel<D, DT>, dim3((unsigned)grid), dim3(32 * kRopeBulkWarps),
+                                      (size_t)kRopeStages * a.slice * HB, s, a));
+    }
     // a warp per token, or as many as give every SM 16 warps
     const int64_t steps = (a.q_heads + VPW - 1) / VPW + (a.v ? 2 : 1) * (int64_t)((a.kv_heads + VPW - 1) / VPW);
     a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(steps, 16 * (int64_t)sms / a.n_tokens));
