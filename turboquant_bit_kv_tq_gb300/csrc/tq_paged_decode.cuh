@@ -230,6 +230,13 @@ __device__ __forceinline__ PagedSeg paged_next(const PagedArgs& a, PagedWalk& w,
     return s;
 }
 
+// Where a warp is, between segments: in shared memory, for the steps need every register
+struct PagedState {
+    PagedWalk cons, prod;  // behind the segment worked on, behind the one copied from
+    PagedSeg sg, ps;       // these
+    int u0;                // first place of the run
+};
+
 // Even runs: run i < n takes units [start(i), start(i + 1)) of `total` >= n.
 struct PagedRuns {
     uint32_t q, r, n;
@@ -268,12 +275,16 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     __shared__ int s_last[2][2];  // [unit][level]: each written once, so that no read of one is overtaken
     __shared__ float4 s_ref[W][HEADS];
+    __shared__ float s_cq[HEADS];  // the query heads' factors of the scores
     __shared__ uint64_t s_jbar;  // the joins' copies
+    __shared__ PagedState s_state[W];
+    __shared__ PagedRuns s_runs;
     __shared__ PagedSeg s_part[2];  // segments whose sums are in the workspace (b < 0: none)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int nj = a.heads * a.nhg;
     uint8_t* ring = smem + warp * (S * C::STEP);
-    uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q + warp * C::QF);
+    uint2* qf = reinterpret_cast<uint2*>(smem + C::off_q + warp * C::QF);  // this warp's, where it is alone
+    uint2* qf0 = reinterpret_cast<uint2*>(smem + C::off_q);                // the block's
     uint8_t* metas = smem + C::off_ex + warp * S * PP * C::META;
     // a ring page's scales and exponents
     auto meta = [&](int stage, int pp) {
@@ -341,6 +352,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                   : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, all_pages / units / 16));
     runs.q = (uint32_t)total / runs.n;
     runs.r = (uint32_t)total - runs.q * runs.n;
+    if (tid == 0) s_runs = runs;  // for the joins, behind a barrier
     const uint32_t run = solo ? blockIdx.x * W + warp : blockIdx.x;
 
     if (run < runs.n) {
@@ -382,33 +394,125 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         }
         cons.left = u1 - u0;
         if (cons.left <= 0) return;  // (solo: no unit starts here)
+        PagedState& st = s_state[warp];
+
+        // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9), in
+        // fragment order.  Exact for fp16 elements down to 2^-22 of the head's largest
+        // and bf16 ones down to 2^-25; below, they are rounded to steps of at most 2^-32
+        // of it, which is less than the fp32 score's rounding.
+        // Heads h0 .. of a unit, 4 elements a lane of each 128, as they lie in memory
+        auto load_heads = [&](auto& x, const PagedSeg& sg, int h0) {
+            constexpr int N = sizeof(x) / sizeof(x[0]);
+            const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
+            const int nh = min(a.hp, a.group - hg * a.hp);
+            const int64_t at = (int64_t)sg.b * a.q_stride + (int64_t)(kvh * a.group + hg * a.hp + h0) * D + 4 * lane;
+#pragma unroll
+            for (int hh = 0; hh < N; ++hh)
+#pragma unroll
+                for (int i = 0; i < D / 128; ++i) {
+                    x[hh][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (h0 + hh >= nh) continue;
+                    const int64_t el = at + hh * D + 128 * i;
+                    if (PREC && a.q_dtype == TQ_DTYPE_F32) {
+                        x[hh][i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + el));
+                    } else {
+                        const uint2 y = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + el));
+                        x[hh][i].x = y.x, x[hh][i].y = y.y;
+                    }
+                }
+        };
+        // a head's operands to `to`; returns its factor of the scores
+        auto put_head = [&](const uint4 (&raw)[D / 128], int h, uint2* to) {
+            float4 x[D / 128];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+                if (PREC && a.q_dtype == TQ_DTYPE_F32) {
+                    x[i] = make_float4(__uint_as_float(raw[i].x), __uint_as_float(raw[i].y), __uint_as_float(raw[i].z),
+                                       __uint_as_float(raw[i].w));
+                } else {
+                    const bool bf = a.q_dtype == TQ_DTYPE_BF16;
+                    const float2 u = bf ? F8Elem::from_bf16x2(raw[i].x) : F8Elem::from_f16x2(raw[i].x);
+                    const float2 w = bf ? F8Elem::from_bf16x2(raw[i].y) : F8Elem::from_f16x2(raw[i].y);
+                    x[i] = make_float4(u.x, u.y, w.x, w.y);
+                }
+                top = max(max(top, max(__float_as_uint(x[i].x) & 0x7FFFFFFFu, __float_as_uint(x[i].y) & 0x7FFFFFFFu)),
+                          max(__float_as_uint(x[i].z) & 0x7FFFFFFFu, __float_as_uint(x[i].w) & 0x7FFFFFFFu));
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const bool bad = top >= 0x7F800000u;
+            const uint32_t e = max(top >> 23, 16u);
+            const float mul = bad ? 0.f : __uint_as_float((262u - min(e, 254u)) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+                float4 y = x[i];
+                if (bad) y = make_float4(0.f, 0.f, 0.f, 0.f);
+                y.x *= mul, y.y *= mul, y.z *= mul, y.w *= mul;
+                // elements 128 i + 4 lane ..: K step and lane part of the product
+                int ks, cc;
+                if constexpr (BITS == 8) {
+                    const int el = 128 * i + 4 * lane;
+                    ks = (el >> 6) * 4 + ((el >> 2) & 3), cc = (el >> 4) & 3;
+                } else {
+                    // a word of 8 codes gives the pairs (n, n + 4): half of them to either lane
+                    const bool odd = lane & 1;
+                    const float r0 = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.z, 1);
+                    const float r1 = __shfl_xor_sync(0xffffffffu, odd ? y.y : y.w, 1);
+                    y = odd ? make_float4(r0, y.z, r1, y.w) : make_float4(y.x, r0, y.y, r1);
+                    ks = 8 * i + (lane & 7), cc = lane >> 3;
+                }
+                const uint2 f = make_uint2(paged_pack_f16(y.x, y.y), paged_pack_f16(y.z, y.w));
+                const int at = (ks * NT + (h >> 3)) * 32 + (h & 7) * 4 + cc;
+                to[at] = f;
+                if constexpr (PREC)
+                    to[(D / 16) * NT * 32 + at] = make_uint2(paged_pack_rest(y.x, y.y, f.x), paged_pack_rest(y.z, y.w, f.y));
+            }
+            return bad ? __uint_as_float(0x7FC00000u) : a.scale_log2e * __uint_as_float((e - 8u) << 23);
+        };
+        // the walk's next segment with more than `first` pages; none: false
+        auto advance = [&](PagedWalk& w, PagedSeg& s, int first) {
+            do {
+                if (w.left <= 0) return false;
+                s = paged_next(a, w, nj, cost);
+            } while (s.p0 + first >= s.p1);
+            return true;
+        };
+        PagedSeg s0 = {}, ps = {};
         PagedWalk prod = cons;
+        bool more = advance(cons, s0, 0), again = false;
+        int pn = 0, pend = 0;  // pages to be copied of the segment st.ps
+        if (advance(prod, ps, sw * PP)) pn = ps.p0 + sw * PP, pend = ps.p1;
+        if (lane == 0) st.cons = cons, st.prod = prod, st.sg = s0, st.ps = ps, st.u0 = u0;
+        constexpr int QW = HEADS / W;  // heads of a warp, where the block shares a unit
+        uint4 qx[QW][D / 128];
+        if (!solo && more) load_heads(qx, s0, QW * warp);  // (beside the first pages' look-up)
 
         // ---- producer: this warp's steps, segment after segment.  Lane pp of a step copies
         // its page pp; lane x of a batch of steps has looked up the batch's page x
-        PagedSeg ps = paged_next(a, prod, nj, cost);
-        int pn = ps.p0 + sw * PP;  // first page of the next step
         int made = 0, used = 0;    // steps copied, steps taken
         uint32_t phase = 0;        // of the ring stage to be read
         int pg = 0, toks = 0, at = 32;  // pages and their tokens (0: none) from entry `at` on
         auto produce = [&](int stage) {
-            if (pn >= ps.p1) {
-                do {
-                    if (prod.left <= 0) return;
-                    ps = paged_next(a, prod, nj, cost);
-                    pn = ps.p0 + sw * PP;
-                } while (pn >= ps.p1);
+            if (pn >= pend) {
+                PagedWalk w = st.prod;
+                PagedSeg s = {};
+                if (!advance(w, s, sw * PP)) return;
+                pn = s.p0 + sw * PP;
+                pend = s.p1;
                 at = 32;
+                __syncwarp();
+                if (lane == 0) st.prod = w, st.ps = s;
+                __syncwarp();
             }
             if (at >= 32) {
                 at = 0;
                 const int p = pn + sn * PP * (lane / PP) + lane % PP;
-                const int h = a.nhg == 1 ? ps.j : ps.j / a.nhg;
-                const int blk = p < ps.p1 ? __ldg(a.table + (int64_t)ps.b * a.max_blocks + p) : -1;
+                const int h = a.nhg == 1 ? st.ps.j : st.ps.j / a.nhg;
+                const int blk = p < pend ? __ldg(a.table + (int64_t)st.ps.b * a.max_blocks + p) : -1;
                 const bool there = blk >= 0 && blk < a.num_blocks;
-                if (p < ps.p1 && !there) set_error(a.err, TQ_DEVERR_BLOCK);
+                if (p < pend && !there) set_error(a.err, TQ_DEVERR_BLOCK);
                 pg = blk * a.heads + h;
-                toks = there ? min(16, ps.len - 16 * p) : 0;
+                toks = there ? min(16, st.ps.len - 16 * p) : 0;
             }
             const int page = __shfl_sync(0xffffffffu, pg, at + lane % PP);
             const int n = __shfl_sync(0xffffffffu, toks, at + lane % PP);
@@ -431,101 +535,45 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
             at += PP;
             ++made;
         };
+        __syncwarp();
 #pragma unroll
         for (int s = 0; s < S - 1; ++s) produce(s);
         int stage = 0;
 
-        while (cons.left > 0) {
-            const PagedSeg sg = paged_next(a, cons, nj, cost);
-            if (sg.p0 == sg.p1) continue;
-            const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
-            const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
-            const int qh0 = kvh * a.group + hg * a.hp;
-
-            // ---- query operands: fp16 of q * 2^-x with the largest in [2^8, 2^9), in
-            // fragment order.  Exact for fp16 elements down to 2^-22 of the head's largest
-            // and bf16 ones down to 2^-25; below, they are rounded to steps of at most 2^-32
-            // of it, which is less than the fp32 score's rounding
+        while (more) {
             float cqr[NT][2];
-            constexpr int QB = HEADS * D <= 8 * 128 ? 8 : 4;  // heads loaded at once
-            const int64_t qoff = (int64_t)sg.b * a.q_stride + (int64_t)qh0 * D + 4 * lane;
+            const uint2* qu = solo ? qf : qf0;  // the unit's query operands
+            if (solo) {
+                constexpr int QB = HEADS * D <= 8 * 128 ? 8 : 4;  // heads loaded at once
 #pragma unroll
-            for (int h8 = 0; h8 < HEADS; h8 += QB) {
-                float4 x[QB][D / 128];
-                if (PREC && a.q_dtype == TQ_DTYPE_F32) {
+                for (int h8 = 0; h8 < HEADS; h8 += QB) {
+                    uint4 x[QB][D / 128];
+                    load_heads(x, st.sg, h8);
 #pragma unroll
-                    for (int hh = 0; hh < QB; ++hh)
+                    for (int hh = 0; hh < QB; ++hh) {
+                        const int h = h8 + hh;
+                        const float cq = put_head(x[hh], h, qf);
 #pragma unroll
-                        for (int i = 0; i < D / 128; ++i)
-                            x[hh][i] = h8 + hh < nh ? __ldg(reinterpret_cast<const float4*>(
-                                                          static_cast<const float*>(a.q) + qoff + (h8 + hh) * D + 128 * i))
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-                } else {
-                    uint2 y[QB][D / 128];
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int hh = 0; hh < QB; ++hh)
-#pragma unroll
-                        for (int i = 0; i < D / 128; ++i)
-                            y[hh][i] = h8 + hh < nh ? __ldg(reinterpret_cast<const uint2*>(
-                                                          static_cast<const uint16_t*>(a.q) + qoff + (h8 + hh) * D + 128 * i))
-                                                    : make_uint2(0u, 0u);
-                    const bool bf = a.q_dtype == TQ_DTYPE_BF16;
-#pragma unroll
-                    for (int hh = 0; hh < QB; ++hh)
-#pragma unroll
-                        for (int i = 0; i < D / 128; ++i) {
-                            const float2 u = bf ? F8Elem::from_bf16x2(y[hh][i].x) : F8Elem::from_f16x2(y[hh][i].x);
-                            const float2 w = bf ? F8Elem::from_bf16x2(y[hh][i].y) : F8Elem::from_f16x2(y[hh][i].y);
-                            x[hh][i] = make_float4(u.x, u.y, w.x, w.y);
-                        }
-                }
-#pragma unroll
-                for (int hh = 0; hh < QB; ++hh) {
-                    const int h = h8 + hh;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i)
-                        top = max(max(top, max(__float_as_uint(x[hh][i].x) & 0x7FFFFFFFu,
-                                               __float_as_uint(x[hh][i].y) & 0x7FFFFFFFu)),
-                                  max(__float_as_uint(x[hh][i].z) & 0x7FFFFFFFu,
-                                      __float_as_uint(x[hh][i].w) & 0x7FFFFFFFu));
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    const bool bad = top >= 0x7F800000u;
-                    const uint32_t e = max(top >> 23, 16u);
-                    const float mul = bad ? 0.f : __uint_as_float((262u - min(e, 254u)) << 23);
-                    const float cq =
-                        bad ? __uint_as_float(0x7FC00000u) : a.scale_log2e * __uint_as_float((e - 8u) << 23);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            if (8 * n + 2 * c + u == h) cqr[n][u] = cq;
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        float4 y = x[hh][i];
-                        if (bad) y = make_float4(0.f, 0.f, 0.f, 0.f);
-                        y.x *= mul, y.y *= mul, y.z *= mul, y.w *= mul;
-                        // elements 128 i + 4 lane ..: K step and lane part of the product
-                        int ks, cc;
-                        if constexpr (BITS == 8) {
-                            const int el = 128 * i + 4 * lane;
-                            ks = (el >> 6) * 4 + ((el >> 2) & 3), cc = (el >> 4) & 3;
-                        } else {
-                            // a word of 8 codes gives the pairs (n, n + 4): half of them to either lane
-                            const bool odd = lane & 1;
-                            const float r0 = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.z, 1);
-                            const float r1 = __shfl_xor_sync(0xffffffffu, odd ? y.y : y.w, 1);
-                            y = odd ? make_float4(r0, y.z, r1, y.w) : make_float4(y.x, r0, y.y, r1);
-                            ks = 8 * i + (lane & 7), cc = lane >> 3;
-                        }
-                        const uint2 f = make_uint2(paged_pack_f16(y.x, y.y), paged_pack_f16(y.z, y.w));
-                        const int at = (ks * NT + (h >> 3)) * 32 + (h & 7) * 4 + cc;
-                        qf[at] = f;
-                        if constexpr (PREC)
-                            qf[(D / 16) * NT * 32 + at] =
-                                make_uint2(paged_pack_rest(y.x, y.y, f.x), paged_pack_rest(y.z, y.w, f.y));
+                            for (int u = 0; u < 2; ++u)
+                                if (8 * n + 2 * c + u == h) cqr[n][u] = cq;
                     }
                 }
+            } else {
+                // one copy for the block, a few heads by each warp
+                if (again) load_heads(qx, st.sg, QW * warp);
+                again = true;
+#pragma unroll
+                for (int hh = 0; hh < QW; ++hh) {
+                    const float cq = put_head(qx[hh], QW * warp + hh, qf0);
+                    if (lane == 0) s_cq[QW * warp + hh] = cq;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) cqr[n][u] = s_cq[8 * n + 2 * c + u];
             }
 
             float o[D / 16][NT][4];
@@ -539,7 +587,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
 #pragma unroll
                 for (int e = 0; e < 2; ++e) r[n][e] = kNoScore, xv[n][e] = l[n][e] = 0.f;
 
-            for (int p = sg.p0 + sw * PP; p < sg.p1; p += sn * PP) {
+            const int p1 = st.sg.p1;
+            for (int p = st.sg.p0 + sw * PP; p < p1; p += sn * PP) {
                 __syncwarp();  // the last step's stage (and qf) is settled
                 if (!dead) produce(stage == 0 ? S - 1 : stage - 1);
                 if (!dead) dead = !mbar_wait(bars + 8 * stage, phase, a.err);
@@ -578,9 +627,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const int at = ((KS * h + k) * NT + n) * 32 + lane;
-                            const uint2 b = qf[at];
+                            const uint2 b = qu[at];
                             uint2 bl = make_uint2(0u, 0u);
-                            if constexpr (PREC) bl = qf[(D / 16) * NT * 32 + at];
+                            if constexpr (PREC) bl = qu[(D / 16) * NT * 32 + at];
 #pragma unroll
                             for (int pp = 0; pp < PP; ++pp) {
                                 auto product = [&](float (&to)[4], uint2 y) {
@@ -855,6 +904,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
             }
 
             // ---- the segment's sums
+            const PagedSeg sg = st.sg;
+            const int kvh = a.nhg == 1 ? sg.j : sg.j / a.nhg, hg = sg.j - kvh * a.nhg;
+            const int nh = min(a.hp, a.group - hg * a.hp);  // heads of this unit
+            const int qh0 = kvh * a.group + hg * a.hp;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -943,7 +996,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                             }
                     }
             } else {
-                const int which = u0 >= sg.v0 ? 0 : 1;  // 0: the run starts in this unit
+                const int which = st.u0 >= sg.v0 ? 0 : 1;  // 0: the run starts in this unit
                 const int slot = 2 * (int)run + which;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
@@ -959,7 +1012,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                             a.meta[slot * HEADS + 8 * n + 2 * c + e] = make_float4(r[n][e], xv[n][e], l[n][e], 0.f);
                 if (lane == 0) s_part[which] = sg;
             }
-            __syncwarp();  // qf is free
+            PagedWalk w = st.cons;
+            PagedSeg s = {};
+            more = advance(w, s, 0);
+            __syncwarp();  // qf is free, the state read
+            if (lane == 0) st.cons = w, st.sg = s;
+            __syncwarp();
         }
         // after a wait that gave up: copies still in flight land before the ring is reused
         if (dead)
@@ -1062,13 +1120,14 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     // What a block's part of a unit is joined with: the runs (= blocks) of the unit,
     // c0 .. c1, from the one that holds its first page on; with more than kPagedJoin of
     // them in groups first.
+    const PagedRuns joint = s_runs;
     struct Step {
         int jn, j0, j1, st;  // sums to join: slots j0, then j1 + st, j1 + 2 st, ...
         uint32_t* cnt;
     };
     auto step = [&](const PagedSeg& sg, bool fin, bool& single) {
-        const int c0 = (int)runs.owner(sg.v0), c1 = (int)runs.owner(sg.v0 + sg.np() - 1), n = c1 - c0 + 1;
-        const int first = 2 * c0 + ((int)runs.start(c0) >= sg.v0 ? 0 : 1);  // slot of block c0; the others': 2 c
+        const int c0 = (int)joint.owner(sg.v0), c1 = (int)joint.owner(sg.v0 + sg.np() - 1), n = c1 - c0 + 1;
+        const int first = 2 * c0 + ((int)joint.start(c0) >= sg.v0 ? 0 : 1);  // slot of block c0; the others': 2 c
         const int gi = ((int)run - c0) / kPagedGroup, g0 = c0 + gi * kPagedGroup;
         single = n <= kPagedJoin;
         Step s;
