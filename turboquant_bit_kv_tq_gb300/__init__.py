@@ -1183,20 +1183,29 @@ def tq_plan_get_device_error(handle, stream=None):
 
 class TQPlanStep:
     """The tensors that a plan's step writes, for ``batch`` requests and ``tokens``
-    rows: slot_mapping, positions, kv_rows, seq_lens, cu_q, cu_k, next_free."""
+    rows: slot_mapping, positions, kv_rows, seq_lens, cu_q, cu_k, next_free.  They are
+    its own, so that a step need not look at them again."""
+
+    _NAMES = ("slot_mapping", "positions", "kv_rows", "seq_lens", "cu_q", "cu_k", "next_free")
 
     def __init__(self, batch, tokens, device, stream=None):
         torch = _torch()
-
+        sizes = (tokens, tokens, tokens, batch, batch + 1, batch + 1, 1)
         # (memory of the stream that will write it, as in _output)
         with torch.cuda.stream(stream):
-            def make(n, dtype=torch.int32):
-                return torch.empty(n, dtype=dtype, device=device)
+            made = [torch.empty(n, dtype=torch.int32 if i else torch.int64, device=device)
+                    for i, n in enumerate(sizes)]
+        self._made = dict(zip(self._NAMES, made))
+        self._at = (tokens,) + tuple(t.data_ptr() for t in made)
+        self._of = (batch, made[0].get_device())
 
-            self.slot_mapping = make(tokens, torch.int64)
-            self.positions, self.kv_rows = make(tokens), make(tokens)
-            self.seq_lens, self.cu_q, self.cu_k = make(batch), make(batch + 1), make(batch + 1)
-            self.next_free = make(1)
+    slot_mapping = property(lambda self: self._made["slot_mapping"])
+    positions = property(lambda self: self._made["positions"])
+    kv_rows = property(lambda self: self._made["kv_rows"])
+    seq_lens = property(lambda self: self._made["seq_lens"])
+    cu_q = property(lambda self: self._made["cu_q"])
+    cu_k = property(lambda self: self._made["cu_k"])
+    next_free = property(lambda self: self._made["next_free"])
 
 
 class TQPlan:
@@ -1219,10 +1228,18 @@ class TQPlan:
     def step(self, lens, new_lens, block_table, free_blocks, next_free, out, stream=None):
         """Plan one step into ``out`` (a TQPlanStep) and block_table; returns ``out``.  In a
         loop, lens and next_free may be out.seq_lens and out.next_free."""
-        if block_table.get_device() != self.device.index:
-            raise _wrong_device(block_table, "block_table", self.device.index)
-        tq_plan_step(self.handle, self.cfg, lens, new_lens, block_table, free_blocks, next_free, out.slot_mapping,
-                     out.positions, out.kv_rows, out.seq_lens, out.cu_q, out.cu_k, out.next_free, stream)
+        dev, i32 = self.device.index, _TORCH.int32
+        b = lens.shape[0]
+        if out._of != (b, dev):
+            raise ValueError(f"out is for {out._of[0]} requests on cuda:{out._of[1]}, lens has {b} (cuda:{dev})")
+        st = load_library().tq_plan_step(
+            self.handle, _index(lens, "lens", i32, b, dev),
+            None if new_lens is None else _index(new_lens, "new_lens", i32, b, dev), b,
+            _index(free_blocks, "free_blocks", i32, 0, dev), free_blocks.numel(),
+            _index(next_free, "next_free", i32, 1, dev), _table(block_table, b, self.cfg.max_blocks_per_seq, dev),
+            *out._at, _launch_stream(stream, dev))
+        if st:
+            raise TQError(st, "tq_plan_step")
         return out
 
     def device_error(self, stream=None):
