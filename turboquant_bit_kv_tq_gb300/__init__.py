@@ -898,57 +898,78 @@ def tq_i4_cache_destroy(handle):
     _check(load_library().tq_i4_cache_destroy(handle), "tq_i4_cache_destroy")
 
 
-def tq_i4_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
-    """k, v [T, H_kv, d] (f32, bf16 or f16, same dtype; rows may lie apart);
-    slot_mapping int64 [T]."""
+def _same_rows(t, like, ptr_and_stride, name, heads, d, dev):
+    """_rows of a tensor of like's shape; the same strides need no second look."""
+    if t.stride() == like.stride() and t.get_device() == dev:
+        return t.data_ptr(), ptr_and_stride[1]
+    return _rows(t, name, heads, d, dev)
+
+
+def _i4_store(handle, heads, d, k, v, slot_mapping, pages, dev, stream):
     dt = _code(k, "k")
     if k.dtype != v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have the same shape and dtype")
-    dev = cache.get_device() if cache is not None else k.get_device()
-    heads, d = cfg.num_kv_heads, cfg.head_dim
-    kp, ks = _rows(k, "k", heads, d, dev)
-    vp, vs = _rows(v, "v", heads, d, dev)
+    kr = _rows(k, "k", heads, d, dev)
+    vp, vs = _same_rows(v, k, kr, "v", heads, d, dev)
     n = k.shape[0]
-    st = load_library().tq_i4_store(handle, kp, vp, dt, ks, vs, n,
-                                    _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), _pages(cache, cfg, 4),
-                                    _launch_stream(stream, dev))
+    st = _LIB.tq_i4_store(handle, kr[0], vp, dt, kr[1], vs, n,
+                          _index(slot_mapping, "slot_mapping", _TORCH.int64, n, dev), pages, _launch_stream(stream, dev))
     if st:
         raise TQError(st, "tq_i4_store")
+
+
+def tq_i4_store(handle, cfg, k, v, slot_mapping, cache, stream=None):
+    """k, v [T, H_kv, d] (f32, bf16 or f16, same dtype; rows may lie apart);
+    slot_mapping int64 [T]."""
+    load_library()
+    pages = None if cache is None else _pages(cache, cfg, 4)
+    _i4_store(handle, cfg.num_kv_heads, cfg.head_dim, k, v, slot_mapping, pages,
+              k.get_device() if cache is None else cache.get_device(), stream)
+
+
+def _i4_load(handle, heads, d, columns, block_table, seq_lens, cu_out, k_out, v_out, pages, dev, stream):
+    dt = _code(k_out, "k_out")
+    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out must have the same shape and dtype")
+    b, n, i32 = seq_lens.shape[0], k_out.shape[0], _TORCH.int32
+    shape = (n, heads, d)
+    st = _LIB.tq_i4_load(
+        handle, pages, _table(block_table, b, columns, dev), _index(seq_lens, "seq_lens", i32, b, dev),
+        _index(cu_out, "cu_out", i32, b, dev), b, n, _plain(k_out, "k_out", shape, None, dev),
+        _plain(v_out, "v_out", shape, None, dev), dt, _launch_stream(stream, dev))
+    if st:
+        raise TQError(st, "tq_i4_load")
 
 
 def tq_i4_load(handle, cfg, cache, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
     """block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]; cu_out
     int32 [B] (or more): first row of each sequence in k_out, v_out [rows,
     H_kv, d] (f32, bf16 or f16)."""
-    dt = _code(k_out, "k_out")
-    if k_out.dtype != v_out.dtype or k_out.shape != v_out.shape:
-        raise ValueError("k_out and v_out must have the same shape and dtype")
-    dev = cache.get_device() if cache is not None else k_out.get_device()
-    b, n, i32 = seq_lens.shape[0], k_out.shape[0], _TORCH.int32
-    shape = (n, cfg.num_kv_heads, cfg.head_dim)
-    st = load_library().tq_i4_load(
-        handle, _pages(cache, cfg, 4), _table(block_table, b, cfg.max_blocks_per_seq, dev),
-        _index(seq_lens, "seq_lens", i32, b, dev), _index(cu_out, "cu_out", i32, b, dev), b, n,
-        _plain(k_out, "k_out", shape, None, dev), _plain(v_out, "v_out", shape, None, dev), dt,
+    load_library()
+    pages = None if cache is None else _pages(cache, cfg, 4)
+    _i4_load(handle, cfg.num_kv_heads, cfg.head_dim, cfg.max_blocks_per_seq, block_table, seq_lens, cu_out, k_out,
+             v_out, pages, k_out.get_device() if cache is None else cache.get_device(), stream)
+
+
+def _i4_decode(handle, heads, d, columns, q, pages, dev, block_table, seq_lens, out, scale, stream):
+    qt, ot = _code(q, "q"), _code(out, "out")
+    qp, qs = _rows(q, "q", heads, d, dev)
+    b = q.shape[0]
+    st = _LIB.tq_i4_decode_attention(
+        handle, qp, qt, qs, pages, _table(block_table, b, columns, dev),
+        _index(seq_lens, "seq_lens", _TORCH.int32, b, dev), scale, b, _plain(out, "out", (b, heads, d), None, dev), ot,
         _launch_stream(stream, dev))
     if st:
-        raise TQError(st, "tq_i4_load")
+        raise TQError(st, "tq_i4_decode_attention")
 
 
 def tq_i4_decode_attention(handle, cfg, q, cache, block_table, seq_lens, out, scale=0.0, stream=None):
     """q, out [B, H_q, d] (f32, bf16 or f16 each; q's rows may lie apart);
     block_table int32 [B, max_blocks_per_seq]; seq_lens int32 [B]."""
-    qt, ot = _code(q, "q"), _code(out, "out")
-    dev = cache.get_device() if cache is not None else q.get_device()
-    heads, d = cfg.num_q_heads, cfg.head_dim
-    qp, qs = _rows(q, "q", heads, d, dev)
-    b = q.shape[0]
-    st = load_library().tq_i4_decode_attention(
-        handle, qp, qt, qs, _pages(cache, cfg, 4), _table(block_table, b, cfg.max_blocks_per_seq, dev),
-        _index(seq_lens, "seq_lens", _TORCH.int32, b, dev), scale, b, _plain(out, "out", (b, heads, d), None, dev), ot,
-        _launch_stream(stream, dev))
-    if st:
-        raise TQError(st, "tq_i4_decode_attention")
+    load_library()
+    pages = None if cache is None else _pages(cache, cfg, 4)
+    _i4_decode(handle, cfg.num_q_heads, cfg.head_dim, cfg.max_blocks_per_seq, q, pages,
+               q.get_device() if cache is None else cache.get_device(), block_table, seq_lens, out, scale, stream)
 
 
 def tq_i4_get_device_error(handle, stream=None):
@@ -973,10 +994,17 @@ class TQI4Cache:
         elif (cache.dtype != torch.uint8 or cache.numel() != self.sizes["cache_bytes"] or not cache.is_contiguous()
               or cache.device != self.device):
             raise ValueError(f"cache must be {self.sizes['cache_bytes']} contiguous uint8 bytes on {self.device}")
-        self.cache = cache
+        # (the owner's own memory and sizes, looked at once, here)
+        self._cache, self._at, self._dev = cache, cache.data_ptr(), cache.get_device()
+        self._kv, self._q, self._d = self.cfg.num_kv_heads, self.cfg.num_q_heads, self.cfg.head_dim
+        self._columns = self.cfg.max_blocks_per_seq
         self.workspace = torch.empty(self.sizes["workspace_bytes"], dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             self.handle = tq_i4_cache_create(self.cfg, self.workspace)
+
+    @property
+    def cache(self):
+        return self._cache
 
     @property
     def page_bytes(self):
@@ -987,16 +1015,18 @@ class TQI4Cache:
         return self.cache.view(self.cfg.num_blocks, self.cfg.num_kv_heads, self.page_bytes)
 
     def store(self, k, v, slot_mapping, stream=None):
-        tq_i4_store(self.handle, self.cfg, k, v, slot_mapping, self.cache, stream)
+        _i4_store(self.handle, self._kv, self._d, k, v, slot_mapping, self._at, self._dev, stream)
 
     def load(self, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
-        tq_i4_load(self.handle, self.cfg, self.cache, block_table, seq_lens, cu_out, k_out, v_out, stream)
+        _i4_load(self.handle, self._kv, self._d, self._columns, block_table, seq_lens, cu_out, k_out, v_out, self._at,
+                 self._dev, stream)
         return k_out, v_out
 
     def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
         if out is None:
             out = _output(q, out_dtype or q.dtype, stream)
-        tq_i4_decode_attention(self.handle, self.cfg, q, self.cache, block_table, seq_lens, out, scale, stream)
+        _i4_decode(self.handle, self._q, self._d, self._columns, q, self._at, self._dev, block_table, seq_lens, out,
+                   scale, stream)
         return out
 
     def device_error(self, stream=None):
@@ -1039,20 +1069,15 @@ def tq_norm_rope_destroy(handle):
     _check(load_library().tq_norm_rope_destroy(handle), "tq_norm_rope_destroy")
 
 
-def tq_norm_rope(handle, cfg, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, v=None, v_out=None,
-                 kv_rows=None, stream=None):
-    """q, q_out [T, H_q, d], k, v [T, H_kv, d], k_out, v_out [rows, H_kv, d], all of
-    one dtype (f32, bf16 or f16), rows may lie apart; positions, kv_rows int32 [T];
-    weights [d], both of one dtype."""
+def _norm_rope(handle, hq, hk, d, q, k, positions, q_out, k_out, q_weight, k_weight, v, v_out, kv_rows, dev, stream):
+    dtype, i32 = q.dtype, _TORCH.int32
     dt = _code(q, "q")
-    dtype, dev = q.dtype, q.get_device()
-    hq, hk, d, i32 = cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, _TORCH.int32
     if k.dtype != dtype or q_out.dtype != dtype or k_out.dtype != dtype:
         raise TypeError("q, k and the outputs must all have the same dtype")
     qp, qs = _rows(q, "q", hq, d, dev)
-    kp, ks = _rows(k, "k", hk, d, dev)
+    kr = _rows(k, "k", hk, d, dev)
     qo, qos = _rows(q_out, "q_out", hq, d, dev)
-    ko, kos = _rows(k_out, "k_out", hk, d, dev)
+    kor = _rows(k_out, "k_out", hk, d, dev)
     n, rows = q.shape[0], k_out.shape[0]
     if k.shape[0] != n or q_out.shape[0] != n:
         raise ValueError("q, k and q_out must have the same number of rows")
@@ -1060,27 +1085,39 @@ def tq_norm_rope(handle, cfg, q, k, positions, q_out, k_out, q_weight=None, k_we
         raise ValueError(f"k_out must have {n} rows, got {rows} (or kv_rows must be given)")
     vp = vo = None
     vs = vos = 0
-    if (v is None) != (v_out is None):
-        raise ValueError("v and v_out go together")
-    if v is not None:
+    if v is not None or v_out is not None:
+        if v is None or v_out is None:
+            raise ValueError("v and v_out go together")
         if v.dtype != dtype or v_out.dtype != dtype:
             raise TypeError("v and v_out must have q's dtype")
-        vp, vs = _rows(v, "v", hk, d, dev)
-        vo, vos = _rows(v_out, "v_out", hk, d, dev)
-        if v.shape[0] != n or v_out.shape[0] != rows:
-            raise ValueError("v must have k's rows and v_out k_out's")
-    wt, wp = 0, [None, None]
-    for i, w in enumerate((q_weight, k_weight)):
-        if w is not None:
-            wt, wp[i] = _code(w, "weight"), _plain(w, "weight", (d,), None, dev)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must have the same dtype")
-    st = load_library().tq_norm_rope(
-        handle, qp, kp, vp, dt, qs, ks, vs, wp[0], wp[1], wt, _index(positions, "positions", i32, n, dev),
-        None if kv_rows is None else _index(kv_rows, "kv_rows", i32, n, dev), n, rows, qo, ko, vo, qos, kos, vos,
+        if v.shape != k.shape or v_out.shape != k_out.shape:
+            raise ValueError("v must have k's shape and v_out k_out's")
+        vp, vs = _same_rows(v, k, kr, "v", hk, d, dev)
+        vo, vos = _same_rows(v_out, k_out, kor, "v_out", hk, d, dev)
+    wt, wq, wk = 0, None, None
+    if q_weight is not None:
+        wt, wq = _code(q_weight, "q_weight"), _plain(q_weight, "q_weight", (d,), None, dev)
+    if k_weight is not None:
+        if q_weight is not None and k_weight.dtype != q_weight.dtype:
+            raise TypeError("q_weight and k_weight must have the same dtype")
+        wt, wk = _code(k_weight, "k_weight"), _plain(k_weight, "k_weight", (d,), None, dev)
+    st = _LIB.tq_norm_rope(
+        handle, qp, kr[0], vp, dt, qs, kr[1], vs, wq, wk, wt, _index(positions, "positions", i32, n, dev),
+        None if kv_rows is None else _index(kv_rows, "kv_rows", i32, n, dev), n, rows, qo, kor[0], vo, qos, kor[1], vos,
         _launch_stream(stream, dev))
     if st:
         raise TQError(st, "tq_norm_rope")
+
+
+def tq_norm_rope(handle, cfg, q, k, positions, q_out, k_out, q_weight=None, k_weight=None, v=None, v_out=None,
+                 kv_rows=None, stream=None):
+    """q, q_out [T, H_q, d], k, v [T, H_kv, d], k_out, v_out [rows, H_kv, d], all of
+    one dtype (f32, bf16 or f16), rows may lie apart; positions, kv_rows int32 [T];
+    weights [d], both of one dtype."""
+    load_library()
+    _torch()
+    _norm_rope(handle, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim, q, k, positions, q_out, k_out, q_weight,
+               k_weight, v, v_out, kv_rows, q.get_device(), stream)
 
 
 def tq_norm_rope_get_device_error(handle, stream=None):
@@ -1100,6 +1137,8 @@ class TQNormRope:
         self.cfg = tq_norm_rope_config(**cfg_kwargs)
         self.sizes = tq_norm_rope_sizes(self.cfg)
         self.device = _cuda_device(device)
+        self._dev = self.device.index
+        self._sizes = (self.cfg.num_q_heads, self.cfg.num_kv_heads, self.cfg.head_dim)
         self.workspace = _TORCH.empty(self.sizes["workspace_bytes"], dtype=_TORCH.uint8, device=self.device)
         with _TORCH.cuda.device(self.device):
             self.handle = tq_norm_rope_create(self.cfg, self.workspace, inv_freq)
@@ -1108,8 +1147,6 @@ class TQNormRope:
               kv_rows=None, stream=None):
         """(q_out, k_out), and v_out where v is given.  With kv_rows, k_out and v_out are
         the caller's longer buffers."""
-        if q.get_device() != self.device.index:
-            raise _wrong_device(q, "q", self.device.index)
         if kv_rows is not None and (k_out is None or (v is not None and v_out is None)):
             raise ValueError("kv_rows name rows of k_out and v_out: give them")
         if q_out is None:
@@ -1118,7 +1155,8 @@ class TQNormRope:
             k_out = _output(k, k.dtype, stream)
         if v is not None and v_out is None:
             v_out = _output(v, v.dtype, stream)
-        tq_norm_rope(self.handle, self.cfg, q, k, positions, q_out, k_out, q_weight, k_weight, v, v_out, kv_rows, stream)
+        _norm_rope(self.handle, *self._sizes, q, k, positions, q_out, k_out, q_weight, k_weight, v, v_out, kv_rows,
+                   self._dev, stream)
         return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
     def device_error(self, stream=None):
@@ -1217,6 +1255,7 @@ class TQPlan:
         self.cfg = tq_plan_config(**cfg_kwargs)
         self.sizes = tq_plan_sizes(self.cfg)
         self.device = _cuda_device(device)
+        self._dev, self._columns = self.device.index, self.cfg.max_blocks_per_seq
         self.workspace = _TORCH.empty(self.sizes["workspace_bytes"], dtype=_TORCH.uint8, device=self.device)
         with _TORCH.cuda.device(self.device):
             self.handle = tq_plan_create(self.cfg, self.workspace)
@@ -1228,15 +1267,15 @@ class TQPlan:
     def step(self, lens, new_lens, block_table, free_blocks, next_free, out, stream=None):
         """Plan one step into ``out`` (a TQPlanStep) and block_table; returns ``out``.  In a
         loop, lens and next_free may be out.seq_lens and out.next_free."""
-        dev, i32 = self.device.index, _TORCH.int32
+        dev, i32 = self._dev, _TORCH.int32
         b = lens.shape[0]
         if out._of != (b, dev):
             raise ValueError(f"out is for {out._of[0]} requests on cuda:{out._of[1]}, lens has {b} (cuda:{dev})")
-        st = load_library().tq_plan_step(
+        st = _LIB.tq_plan_step(
             self.handle, _index(lens, "lens", i32, b, dev),
             None if new_lens is None else _index(new_lens, "new_lens", i32, b, dev), b,
             _index(free_blocks, "free_blocks", i32, 0, dev), free_blocks.numel(),
-            _index(next_free, "next_free", i32, 1, dev), _table(block_table, b, self.cfg.max_blocks_per_seq, dev),
+            _index(next_free, "next_free", i32, 1, dev), _table(block_table, b, self._columns, dev),
             *out._at, _launch_stream(stream, dev))
         if st:
             raise TQError(st, "tq_plan_step")
