@@ -105,19 +105,12 @@ __device__ __forceinline__ uint32_t paged_pack_rest(float x, float y, uint32_t h
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     return paged_pack_f16(x - f.x, y - f.y);
 }
-// a page's 32 code rows: box {128 bytes, 32 rows, d/128 halves, 1 page}; at 4 bits {d/2 bytes, 32 rows, 1 page}
-template <int BITS>
+// a page's 32 code rows at 8 bits: box {128 bytes, 32 rows, d/128 halves, 1 page}
 __device__ __forceinline__ void paged_page_copy(uint32_t dst, const CUtensorMap* m, int page, uint32_t bar) {
-    if constexpr (BITS == 8)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
-            "l"(m), "r"(0), "r"(page), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3}], [%4];" ::"r"(dst),
-            "l"(m), "r"(0), "r"(page), "r"(bar)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(0), "r"(page), "r"(bar)
+        : "memory");
 }
 // 4-bit codes as fp16: code times scale.  A code masked in place under the exponent of
 // 1024 is 1024 + n (four bits higher, under that of 64: 64 + n), and (1024 + n) S - 1032 S
@@ -144,14 +137,12 @@ struct PagedScale {
     }
 };
 // Token of row g (and, 8 further, of row g + 8) of the score product, for operand reads
-// with few bank conflicts.  Rows of 128 bytes, copied with a swizzle that puts 16-byte
-// chunk x of row t at x ^ (t & 7): with this order the rows a quarter warp reads together
-// differ in bit 2 (keys: rows 2i, 2i + 1, chunks c) and in bits 1..2 (values: rows 2c,
-// chunks g), so that its 8 lanes hit 8 chunk places.  Rows of 64 bytes, copied as they
-// lie: a quarter warp's two key rows differ in bit 0, so they have no conflict, and of a
-// half warp's four value rows two and two do: their four reads take twice as long, which
-// is less than the swizzled copy took (one plain copy instead of two, 16 x 8192: 42 us,
-// 44 with the swizzle).
+// with few bank conflicts.  8 bits, copied with a swizzle that puts 16-byte chunk x of
+// row t at x ^ (t & 7): with this order the rows a quarter warp reads together differ in
+// bit 2 (keys: rows 2i, 2i + 1, chunks c) and in bits 1..2 (values: rows 2c, chunks g), so
+// that its 8 lanes hit 8 chunk places.  Rows of 64 bytes (4 bits, d = 128), as they lie: a
+// quarter warp's two key rows differ in bit 0 and have no conflict, a half warp's four
+// value rows are two and two.  (Rows of 128 bytes without a swizzle are two and four.)
 template <int ROW>
 __device__ __forceinline__ int paged_token(int g) {
     if constexpr (ROW == 64) return (g & 4) | ((g & 1) << 1) | ((g ^ (g >> 1)) & 1);
@@ -160,12 +151,17 @@ __device__ __forceinline__ int paged_token(int g) {
 
 template <int BITS, int D, int NT, bool PREC>
 struct PagedCfg {
-    static constexpr int PP = 256 / D;                 // pages per step
+    // pages per step (4 bits, d = 256: one leaves too little to do beside its start, and two
+    // need the registers of a second n-tile; 8 x up to 32768, bf16: 48 us, two 43)
+    static constexpr int PP = BITS == 4 && D == 256 && NT == 1 ? 2 : 256 / D;
     static constexpr int CODES = 4 * BITS * D;         // bytes of a page's codes
     static constexpr int PAGE = BITS == 8 ? f8_page_bytes(D) : i4_page_bytes(D);
     static constexpr int META = PAGE - CODES;          // and of its scales and exponents
-    // 4 bits, d = 128: the page comes as it lies, by one copy, and the ring holds it whole
-    static constexpr bool WHOLE = BITS == 4 && D == 128;
+    // 4 bits: the page comes as it lies, by one copy, and the ring holds it whole.  Bank
+    // conflicts of its operand reads cost less than a swizzled copy of the codes with one of
+    // the rest beside it (16 x 8192, d = 128: 42.9 us, 44.3; 8 x up to 32768, d = 256, fp32:
+    // 50.4, 52.0)
+    static constexpr bool WHOLE = BITS == 4;
     static constexpr int STRIDE = WHOLE ? PAGE : CODES;  // bytes from page to page in the ring
     static constexpr int ROW = BITS == 8 ? 128 : D / 2;  // bytes of a row in the ring
     static constexpr int STEP = PP * STRIDE;           // bytes of a ring stage
@@ -290,8 +286,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     auto meta = [&](int stage, int pp) {
         return C::WHOLE ? ring + stage * C::STEP + pp * C::STRIDE + C::CODES : metas + (stage * PP + pp) * C::META;
     };
-    // 16-byte chunk x of row t, as the copy's swizzle places it
-    auto chunk = [](int x, int t) { return C::WHOLE ? x : x ^ t; };
     const uint32_t bars = smem_u32(smem + C::off_bar) + warp * S * 8;
     int* info = reinterpret_cast<int*>(smem + C::off_info) + warp * S * PP;
     const int tok = paged_token<C::ROW>(g);
@@ -525,7 +519,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                     if constexpr (C::WHOLE) {
                         bulk_copy(to, from, C::PAGE, bars + 8 * stage);
                     } else {
-                        paged_page_copy<BITS>(to, &pages, page, bars + 8 * stage);
+                        paged_page_copy(to, &pages, page, bars + 8 * stage);
                         bulk_copy(smem_u32(metas) + (stage * PP + lane) * C::META, from + C::CODES, C::META, bars + 8 * stage);
                     }
                 }
@@ -615,7 +609,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                                     sp + pp * C::CODES + (h >> 1) * 4096 + (tok + 8 * u) * 128 + (((4 * (h & 1) + c) ^ tok) << 4));
                             } else {
                                 ka[pp][u] = *reinterpret_cast<const uint4*>(
-                                    sp + pp * C::STRIDE + (tok + 8 * u) * C::ROW + (chunk(4 * h + c, tok) << 4));
+                                    sp + pp * C::STRIDE + (tok + 8 * u) * C::ROW + ((4 * h + c) << 4));
                                 sc[pp][u] = *reinterpret_cast<const uint16_t*>(
                                     meta(stage, pp) + (tok + 8 * u) * (D / 16) + 2 * (c + 4 * h));
                             }
@@ -834,7 +828,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
                                 else
                                     v[pp][u] = *reinterpret_cast<const uint2*>(
                                         sp + (p0 + pp) * C::STRIDE + 16 * C::ROW + (t + 8 * (u >> 1)) * C::ROW +
-                                        (chunk(4 * h + (g >> 1), t) << 4) + 8 * (g & 1));
+                                        ((4 * h + (g >> 1)) << 4) + 8 * (g & 1));
                                 if constexpr (BITS == 4)
                                     vs[pp][u >> 1] += (uint32_t)meta(stage, p0 + pp)[D + (t + 8 * (u >> 1)) * (D / 16) + 8 * h + g] *
                                                       (u & 1 ? 0x00800000u : 0x00000080u);
@@ -1170,26 +1164,19 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     }
 }
 
-// the code rows of the cache: {128 bytes, 32 rows, d/128 halves of a row, pages}, at 4 bits {d/2 bytes, 32 rows, pages}
-template <int BITS, int D>
-static tq_status paged_page_map(CUtensorMap* m, const void* cache, int64_t pages) {
-    using C = PagedCfg<BITS, D, 1, false>;
+// the code rows of an 8-bit cache: {128 bytes, 32 rows, d/128 halves of a row, pages}
+static tq_status paged_page_map(CUtensorMap* m, const void* cache, int d, int64_t pages) {
     char why[200] = "";
     auto enc = tensor_map_encoder(why, sizeof why);
     if (!enc) return driver_failure("%s", why);
     const tq_status bs = bind_device_context();
     if (bs != TQ_OK) return bs;
-    constexpr cuuint32_t N = BITS == 8 ? 4 : 3;
-    const cuuint64_t dims8[4] = {128, 32, (cuuint64_t)(D / 128), (cuuint64_t)pages};
-    const cuuint64_t strides8[3] = {(cuuint64_t)D, 128, (cuuint64_t)C::PAGE};
-    const cuuint32_t box8[4] = {128, 32, (cuuint32_t)(D / 128), 1}, estr[4] = {1, 1, 1, 1};
-    const cuuint64_t dims4[3] = {(cuuint64_t)C::ROW, 32, (cuuint64_t)pages};
-    const cuuint64_t strides4[2] = {(cuuint64_t)C::ROW, (cuuint64_t)C::PAGE};
-    const cuuint32_t box4[3] = {(cuuint32_t)C::ROW, 32, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, N, const_cast<void*>(cache), BITS == 8 ? dims8 : dims4,
-                           BITS == 8 ? strides8 : strides4, BITS == 8 ? box8 : box4, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[4] = {128, 32, (cuuint64_t)(d / 128), (cuuint64_t)pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)d, 128, (cuuint64_t)f8_page_bytes(d)};
+    const cuuint32_t box[4] = {128, 32, (cuuint32_t)(d / 128), 1}, estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return driver_failure("cuTensorMapEncodeTiled failed (CUresult %d) for %lld pages at %p", (int)r,
                               (long long)pages, cache);
@@ -1208,7 +1195,7 @@ static tq_status launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     const int grid = C::CTAS * std::min(sms, kPagedMaxSms);
     CUtensorMap pages = {};
     if constexpr (!C::WHOLE) {
-        st = paged_page_map<BITS, D>(&pages, a.cache, a.num_blocks * a.heads);
+        st = paged_page_map(&pages, a.cache, D, a.num_blocks * a.heads);
         if (st != TQ_OK) return st;
     }
     // launched programmatically: the launch overlaps the previous kernel's end,
