@@ -129,16 +129,16 @@ __device__ __forceinline__ uint2 i4_encode16(const I4Raw<DT>& raw, uint32_t mine
         }
     } else {
         if (g == 7.5f * s) r *= 1.f - 4.37e-6f;
-        // 2^(127 - E) goes into the reciprocal, where that stays in range
-        const bool tiny = e < 40;
-        if (!tiny) r *= inv;
+        auto codes = [&](float r, auto value) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float x = raw.value(i);
-            if (tiny) x *= inv;
-            const float q = fmaf(x, r, 768.f);
-            c[i / 8] += __float_as_uint(q + (kI4Round - 768.f)) << (4 * (i & 7));
-        }
+            for (int i = 0; i < 16; ++i) {
+                const float q = fmaf(value(i), r, 768.f);
+                c[i / 8] += __float_as_uint(q + (kI4Round - 768.f)) * (1u << (4 * (i & 7)));
+            }
+        };
+        // 2^(127 - E) goes into the reciprocal, where that stays in range
+        if (!__any_sync(0xffffffffu, e < 40)) codes(r * inv, [&](int i) { return raw.value(i); });
+        else codes(r, [&](int i) { return raw.value(i) * inv; });
     }
     return bad ? make_uint2(0x88888888u, 0x88888888u) : make_uint2(c[0], c[1]);
 }
