@@ -243,3 +243,67 @@ def test_refusals():
     with pytest.raises(tq.TQError) as e:
         tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=1, inv_freq=np.full(64, np.nan))
     assert e.value.status == -1
+
+
+# ------------------------------------------------------------- many tokens
+# (from two pieces of 6 to 13 KB per SM on, rows go through shared memory)
+@pytest.mark.parametrize("n,hq,hk,d,rot,dtype,interleaved", [
+    (400, 24, 1, 128, 128, "bf16", False), (401, 23, 3, 128, 64, "bf16", True), (700, 90, 5, 128, 128, "f16", False),
+    (400, 7, 2, 256, 96, "f32", True), (1300, 25, 2, 128, 16, "f32", False), (333, 12, 12, 256, 256, "bf16", False),
+    (900, 3, 24, 128, 0, "bf16", False),
+])
+def test_many_tokens(n, hq, hk, d, rot, dtype, interleaved):
+    (q, k, v), (wq, wk), pos = _inputs(n + hq, n, hq, hk, d, dtype, "f32")
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk, rot_dim=rot, base=5e5, interleaved=interleaved)
+    f = serve.powers(5e5, rot) if rot else np.zeros(0)
+    eps, p = float(np.float32(1e-6)), _gpu(pos)
+    some = np.r_[0:9, n // 2:n // 2 + 9, n - 9:n]
+    at = _gpu(some)
+    qkv = torch.cat([q, k, v], 1)
+    a, b, c = qkv.split([hq, hk, hk], 1)
+    qo, ko = h.apply(a, b, p, wq, wk)
+    _check(qo[at], q[at], wq, pos[some], f, eps, interleaved)
+    _check(ko[at], k[at], wk, pos[some], f, eps, interleaved)
+    # few of the same rows in a call of their own, which the other kernel takes
+    part = h.apply(a[7:20], b[7:20], p[7:20], wq, wk)
+    _check(part[0], q[7:20], wq, pos[7:20], f, eps, interleaved)
+    _check(part[1], k[7:20], wk, pos[7:20], f, eps, interleaved)
+    # rows of longer buffers, some left out, some outside
+    rng = np.random.default_rng((84, n))
+    rows = rng.permutation(2 * n)[:n].astype(np.int32)
+    rows[::5], rows[3], rows[n - 2] = -1, 2 * n, -7
+    long = [torch.full((2 * n, hk, d), -7.0, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    h.apply(a, b, p, wq, wk, k_out=long[0], v=c, v_out=long[1], kv_rows=_gpu(rows))
+    assert h.device_error() == tq.TQ_DEVERR_CHUNK and h.device_error() == 0
+    good = (rows >= 0) & (rows < 2 * n)
+    want = [torch.full_like(long[0], -7.0) for _ in range(2)]
+    want[0][_gpu(rows[good]).long()], want[1][_gpu(rows[good]).long()] = ko[_gpu(good)], v[_gpu(good)]
+    assert torch.equal(long[0], want[0]) and torch.equal(long[1], want[1])
+    # in place, captured and replayed
+    keep = qkv.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        h.apply(a, b, p, wq, wk, q_out=a, k_out=b)
+    for _ in range(2):
+        qkv.copy_(keep)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, qo) and torch.equal(b, ko) and torch.equal(c, v)
+
+
+@pytest.mark.parametrize("gain,eps", [(2.0 ** 120, 1e-6), (2.0 ** -70, 0.0), (2.0 ** -120, 1e-35), (1.0, 1e-6)])
+def test_many_tokens_beyond_the_range_and_not_finite(gain, eps):
+    n, hq, hk, d = 350, 24, 2, 128
+    (q, k, _), (wq, wk), pos = _inputs(12, n, hq, hk, d, "f32", gain=gain)
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk, rot_dim=64, eps=eps)
+    clean = h.apply(q, k, _gpu(pos), wq, wk)
+    some, f = np.r_[0:4, n - 4:n], serve.powers(1e4, 64)
+    _check(clean[0][_gpu(some)], q[_gpu(some)], wq, pos[some], f, float(np.float32(eps)))
+    _check(clean[1][_gpu(some)], k[_gpu(some)], wk, pos[some], f, float(np.float32(eps)))
+    q[3, 1, 5], k[344, 0, 100] = float("nan"), float("inf")
+    got = h.apply(q, k, _gpu(pos), wq, wk)
+    assert torch.isnan(got[0][3, 1]).all() and torch.isnan(got[1][344, 0, 100])
+    for a, b, (t, hd) in ((got[0], clean[0], (3, 1)), (got[1], clean[1], (344, 0))):
+        a[t, hd], b[t, hd] = 0, 0
+        assert torch.equal(a, b)

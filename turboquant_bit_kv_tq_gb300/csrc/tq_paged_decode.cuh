@@ -1,6 +1,7 @@
 // Decode attention over the paged caches of 8 and of 4 bits.
 //
-// With k8, v8 the codes, 2^ek, 2^ev the vectors' scales and c = scale * log2(e):
+// With k8, v8 the codes (at 4 bits: code times scale), 2^ek, 2^ev the vectors' scales and
+// c = scale * log2(e):
 //   s_t = c <q, k8_t> 2^ek_t                    (log2 units)
 //   l   = sum_t 2^(s_t - r)                     r, r + x: references of the sums, moved
 //   o   = sum_t 2^((s_t - r) + (ev_t - x)) v8_t  when a weight passes 2^12
@@ -10,17 +11,16 @@
 // by its distance x from r: both sums see the same difference s_t - r, exact near r
 // however large the scores are, and ev_t - x keeps every digit beside it.
 //
-// Bound by memory (2 d + 2 bytes per token and KV head).  All pages of all
-// sequences, in the order (sequence, KV head, page), are dealt out in runs to a
-// fixed grid of resident blocks: evenly, one run per block, whose warps share its
-// segments (the pages of one (sequence, KV head) each) step by step and add up in
+// All pages of all sequences, in the order (sequence, KV head, page), are dealt out in
+// runs to a fixed grid of resident blocks: evenly, one run per block, whose warps share
+// its segments (the pages of one (sequence, KV head) each) step by step and add up in
 // shared memory at a segment's end; or, with many short sequences, whole (sequence,
-// KV head)s to warps, and no warp waits for another.  A step is 256/d pages.  Each warp
-// keeps a ring of steps in flight, across segments: one tensor copy per page,
-// whose 128-byte swizzle lays the rows out so that the operand reads below meet no
-// bank conflict, and one small copy of its scales.  (16-byte cp.async in a swizzle
-// of our own moved as much, but issuing it took a warp 1255 cycles of the 4240 of
-// a step.)  Products per 16 tokens:
+// KV head)s to warps, and no warp waits for another.  Each warp keeps a ring of steps of
+// a page or two in flight, across segments.  At 8 bits a page comes by a tensor copy, whose
+// 128-byte swizzle lays the rows out so that the operand reads below meet no bank conflict,
+// and one small copy of its scales.  (16-byte cp.async in a swizzle of our own moved as
+// much, but issuing it took a warp 1255 cycles of the 4240 of a step.)  At 4 bits it comes
+// by one plain copy.  Products per 16 tokens:
 //   S^T[tokens x heads] = K Q^T     mma.m16n8k16, A = codes as fp16 (exact)
 //   O^T[d x heads] += V^T P^T       A = pairs of value codes, B = the weights
 // so a KV head's query heads (8 or 16 columns) share every page, and tokens and
@@ -31,12 +31,16 @@
 // sums of the others go to the workspace and are joined in run order by the last
 // block to arrive, in groups first where there are many.
 //
-// Measured: 16 x 8192 tokens, 32/8 heads, d = 128: 55 us, 4.9 TB/s; 4 x up to 131072,
-// 64/8 heads: 121 us, 5.6 TB/s; 8 x up to 32768, 32/4 heads, d = 256, fp32: 58 us,
-// 5.1 TB/s (a plain copy: 6.8).  Longer caches add bytes at 6.3 to 6.7 TB/s; the rest
-// is about 15 us a call: the first pages are under way after 3 us; of 16 x 8192, blocks
-// with equal runs end between 35 and 47 us (four fifths of them between 39 and 45),
-// arriving takes 1.5 and the last join up to 5.
+// 8 bits: bound by memory (2 d + 2 bytes per token and KV head).  16 x 8192 tokens, 32/8
+// heads, d = 128: 54 us, 5.0 TB/s; 4 x up to 131072, 64/8 heads: 119 us, 5.7 TB/s; 8 x
+// up to 32768, 32/4 heads, d = 256, fp32: 57 us, 5.2 TB/s (a plain copy: 6.8).  Longer
+// caches add bytes at 6.3 to 6.7 TB/s; the rest is about 15 us a call: the first pages are
+// under way after 2 us; blocks with equal runs end up to 12 us apart, arriving takes
+// 1.5 and the last join up to 5.
+// 4 bits (1.125 d + 2 bytes): 41, 82 and 50 us, 3.7, 4.7 and 3.4 TB/s.  Bound by the
+// instructions that turn codes into operands: a page of d = 128 takes 335 a warp, 150 of
+// them masks and multiply-adds of codes, at 60% of the issue slots (a fourth block per SM
+// issues no more).  Without any of the conversions 16 x 8192 takes 35 us.
 
 #pragma once
 
@@ -188,7 +192,6 @@ struct PagedCfg {
     // two sums fit the four warps' query operands, whose place they take at a segment's end
     static_assert(2 * ITEMS * 16 <= kPagedWarps * QF, "merge buffers");
 };
-static_assert(kPagedCtas >= PagedCfg<8, 128, 1, false>::CTAS, "workspace slots");
 
 __device__ __forceinline__ int paged_clamp(const PagedArgs& a, int len) { return max(0, min(len, a.max_blocks * 16)); }
 __device__ __forceinline__ int paged_pages(const PagedArgs& a, int len) { return (paged_clamp(a, len) + 15) >> 4; }
@@ -1186,6 +1189,7 @@ static tq_status paged_page_map(CUtensorMap* m, const void* cache, int d, int64_
 template <int BITS, int D, int NT, bool PREC>
 static tq_status launch_paged_decode(const PagedArgs& a, cudaStream_t s) {
     using C = PagedCfg<BITS, D, NT, PREC>;
+    static_assert(C::CTAS <= kPagedCtas, "workspace slots");
     int sms = 0;
     tq_status st = device_sms(&sms);
     if (st != TQ_OK) return st;
