@@ -336,7 +336,7 @@ static tq_status i4_check(const tq_i4_config& c) {
     // q rows and the pages of all block-table entries, KV heads and head groups within int32
     const int nhg = paged_geom(c).nhg;
     if ((int64_t)c.max_batch * c.num_q_heads > 0x7FFFFFFF ||
-        (double)c.max_batch * (c.max_blocks_per_seq + kPagedUnitCost) * c.num_kv_heads * nhg > 2147483647.0 ||
+        (double)c.max_batch * (c.max_blocks_per_seq + paged_unit_cost(4)) * c.num_kv_heads * nhg > 2147483647.0 ||
         (double)c.num_blocks * c.num_kv_heads > 2147483647.0)
         return TQ_ERR_INVALID_ARG;
     return TQ_OK;

@@ -12,8 +12,9 @@ constexpr int kPagedSlots = 2 * kPagedCtas * kPagedMaxSms;
 // Places a unit takes beside its pages where pages are dealt out, at most: its start
 // and its sums take a block about as long as 8 (d = 128) to 16 (d = 256) pages.  With
 // 0, 4, 8, 16, 24, 32: 8 x up to 32768 tokens, d = 256: 81, 73, 68, 60, 59, 58 us;
-// 64 x up to 2000, d = 128: 56, 48, 37, 35, 34, 35 us.
-constexpr int kPagedUnitCost = 24;
+// 64 x up to 2000, d = 128: 56, 48, 37, 35, 34, 35 us.  At 4 bits, where a page takes less
+// time: 16 x 8192, d = 128, with 0, 12, 24, 32, 48: 42.9, 42.3, 40.8, 39.8, 40.2 us.
+__host__ __device__ constexpr int paged_unit_cost(int bits) { return bits == 8 ? 24 : 32; }
 
 // Query heads of one KV head that one work unit serves (nhg units per KV head
 // share its pages through L2 when G > 16), in n-tiles of 8 heads.

@@ -170,6 +170,10 @@ struct PagedCfg {
     static constexpr int ROW = BITS == 8 ? 128 : D / 2;  // bytes of a row in the ring
     static constexpr int STEP = PP * STRIDE;           // bytes of a ring stage
     static constexpr int HEADS = 8 * NT;
+    // A block whose warps share a unit makes its query operands once, together, or each warp
+    // makes its own.  Once: 16 x 8192, d = 128, 16 heads: 8 bits 56 us, 63; 8 heads: 4 bits
+    // 40.8, 43.6; but 8 bits 54.5, 53.9 (no warp waits for another)
+    static constexpr bool SHARE = BITS == 4 || NT == 2;
     static constexpr int QF = (D / 16) * NT * 32 * 8 * (PREC ? 2 : 1);  // query operands of a warp
     // blocks per SM (three where two stages per warp and the registers allow it,
     // else two), and as deep a ring as fits then
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     const bool solo = units > (int)gridDim.x && most <= max(kPagedSoloPages, 2 * share);
     // (a fixed cost, of less weight where the runs are short: the last of several runs
     // of a unit would be left with few pages)
-    const int cost = min(kPagedUnitCost, share);
+    const int cost = min(paged_unit_cost(BITS), share);
     mine += cost * some;
     int incl = mine;
 #pragma unroll
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         if (lane == 0) st.cons = cons, st.prod = prod, st.sg = s0, st.ps = ps, st.u0 = u0;
         constexpr int QW = HEADS / W;  // heads of a warp, where the block shares a unit
         uint4 qx[QW][D / 128];
-        if (!solo && more) load_heads(qx, s0, QW * warp);  // (beside the first pages' look-up)
+        if (C::SHARE && !solo && more) load_heads(qx, s0, QW * warp);  // (beside the first pages' look-up)
 
         // ---- producer: this warp's steps, segment after segment.  Lane pp of a step copies
         // its page pp; lane x of a batch of steps has looked up the batch's page x
@@ -539,8 +543,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
 
         while (more) {
             float cqr[NT][2];
-            const uint2* qu = solo ? qf : qf0;  // the unit's query operands
-            if (solo) {
+            const uint2* qu = !C::SHARE || solo ? qf : qf0;  // the unit's query operands
+            if (!C::SHARE || solo) {
                 constexpr int QB = HEADS * D <= 8 * 128 ? 8 : 4;  // heads loaded at once
 #pragma unroll
                 for (int h8 = 0; h8 < HEADS; h8 += QB) {
