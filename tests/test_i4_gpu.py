@@ -513,3 +513,75 @@ def test_refusals():
         tq.TQI4Cache(head_dim=128, num_kv_heads=2, num_q_heads=8, num_blocks=4, max_blocks_per_seq=2, cache=c.cache[:-1])
     with pytest.raises(ValueError):
         tq.tq_i4_decode_attention(c.handle, c.cfg, q, c.cache[:-1], t, n, q.clone())
+
+
+# ------------------------------------------------- other strides, shared blocks
+@pytest.mark.parametrize("d,h,dtype", [(128, 3, "bf16"), (256, 1, "f32"), (128, 2, "f16")])
+def test_rows_that_start_at_odd_multiples_of_sixteen_bytes(d, h, dtype):
+    """Stored from and loaded to rows that 32-byte accesses cannot reach."""
+    rng = _rng(73, d, h)
+    n, pad = 45, 128 // torch.finfo(DT[dtype]).bits
+    table, blocks = _table(rng, [n])
+    wide = torch.zeros((n, h * d + pad), dtype=DT[dtype], device="cuda")
+    k, v = (_gpu(rng.standard_normal((n, h, d)), DT[dtype]) for _ in range(2))
+    views = []
+    for x in (k, v):
+        w = wide.clone()
+        w[:, :h * d] = x.flatten(1)
+        views.append(w[:, :h * d].unflatten(1, (h, d)))
+    c = _cache(d, h, h, blocks, 1, table.shape[1])
+    before = c.pages().cpu().numpy()
+    slots = _slots(table, [n])
+    c.store(*views, _gpu(slots))
+    assert np.array_equal(c.pages().cpu().numpy(), i4.store(before, _np(k), _np(v), slots))
+    outs = [torch.full((n * h * d + 2 * pad,), -7.0, dtype=DT[dtype], device="cuda") for _ in range(2)]
+    ko, vo = (x[pad:-pad].view(n, h, d) for x in outs)
+    c.load(_gpu(table), _lens([n]), _lens([0]), ko, vo)
+    for got, want, whole in zip((ko, vo), i4.rows(c.pages().cpu().numpy(), table[0], n, d), outs):
+        assert np.array_equal(_np(got), want) and (whole[:pad] == -7).all() and (whole[-pad:] == -7).all()
+
+
+@pytest.mark.parametrize("d,g,qt,ot,most", [(128, 16, "bf16", "bf16", 50), (256, 4, "f32", "f32", 60),
+                                            (256, 12, "bf16", "f32", 40), (128, 4, "f32", "bf16", 35)])
+def test_many_short_sequences(d, g, qt, ot, most):
+    """More units than blocks, whole ones to warps: one and two tiles of heads, two pages a step, both precisions."""
+    rng = _rng(74, d, g)
+    lens = [int(x) for x in rng.integers(0, most, 900)]
+    lens[0], lens[1], lens[-1] = most, 0, 1
+    c, q, table = _decode_case(d, 1, g, lens, qt, 78)
+    got = c.decode(q.cuda(), _gpu(table), _lens(lens), out_dtype=DT[ot])
+    _check_decode(c, q, table, lens, got)
+    assert torch.equal(got, c.decode(q.cuda(), _gpu(table), _lens(lens), out_dtype=DT[ot])) and c.device_error() == 0
+
+
+def test_sequences_that_share_blocks():
+    """A common prefix in the same blocks, and a sequence that is another's beginning."""
+    lens = [300, 200, 64]
+    c, q, table = _decode_case(128, 2, 4, [300, 300, 300], "bf16", 79)
+    table[1, :8], table[2, :4] = table[0, :8], table[0, :4]
+    got = c.decode(q.cuda(), _gpu(table), _lens(lens))
+    _check_decode(c, q, table, lens, got)
+    alone = c.decode(q[2:].cuda(), _gpu(table[2:]), _lens(lens[2:]))
+    _check_decode(c, q[2:], table[2:], lens[2:], alone)
+
+
+def test_load_is_captured_and_replayed():
+    lens = [70, 0, 33]
+    c, q, table = _decode_case(128, 2, 2, [90, 90, 90], "bf16", 80)
+    t, ld, starts = _gpu(table), _lens(lens), _lens([0, 100, 200])
+    ko, vo = (torch.zeros((300, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.load(t, ld, starts, ko, vo)
+    pages = c.pages().cpu().numpy()
+    for lens in ([70, 0, 33], [1, 90, 16]):
+        ld.copy_(_lens(lens))
+        ko.fill_(-7)
+        vo.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = np.full((2, 300, 2, 128), -7.0)
+        for b, n in enumerate(lens):
+            want[:, 100 * b:100 * b + n] = i4.rows(pages, table[b], n, 128)
+        assert np.array_equal(_np(ko), want[0]) and np.array_equal(_np(vo), want[1])

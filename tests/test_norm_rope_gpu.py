@@ -307,3 +307,35 @@ def test_many_tokens_beyond_the_range_and_not_finite(gain, eps):
     for a, b, (t, hd) in ((got[0], clean[0], (3, 1)), (got[1], clean[1], (344, 0))):
         a[t, hd], b[t, hd] = 0, 0
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [21, 500])
+def test_rows_that_start_at_odd_multiples_of_sixteen_bytes(n):
+    (q, k, v), (wq, wk), pos = _inputs(13, n, 24, 2, 128, "bf16")
+    h = tq.TQNormRope(head_dim=128, num_q_heads=24, num_kv_heads=2)
+    want = h.apply(q, k, _gpu(pos), wq, wk, v=v)
+
+    def apart(x):
+        w = torch.zeros((n, x[0].numel() + 8), dtype=x.dtype, device="cuda")
+        w[:, :-8] = x.flatten(1)
+        return w, w[:, :-8].unflatten(1, x.shape[1:])
+
+    ins, outs = [apart(x) for x in (q, k, v)], [apart(torch.zeros_like(x)) for x in (q, k, v)]
+    h.apply(ins[0][1], ins[1][1], _gpu(pos), wq, wk, q_out=outs[0][1], k_out=outs[1][1], v=ins[2][1], v_out=outs[2][1])
+    for (whole, got), x in zip(outs, want):
+        assert torch.equal(got, x) and not whole[:, -8:].any()
+
+
+def test_one_handle_on_two_streams():
+    h = tq.TQNormRope(head_dim=128, num_q_heads=24, num_kv_heads=2)
+    made = [_inputs(14 + i, n, 24, 2, 128, "bf16") for i, n in enumerate((600, 40))]
+    args = [(q, k, _gpu(pos), wq, wk) for (q, k, _), (wq, wk), pos in made]
+    want = [h.apply(*a) for a in args]
+    outs = [[torch.zeros_like(x) for x in w] for w in want]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, o, s in zip(args, outs, streams):
+            h.apply(*a, q_out=o[0], k_out=o[1], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for o, w in zip(outs, want) for x, y in zip(o, w))
