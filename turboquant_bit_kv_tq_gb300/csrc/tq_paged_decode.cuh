@@ -37,7 +37,7 @@
 // caches add bytes at 6.3 to 6.7 TB/s; the rest is about 15 us a call: the first pages are
 // under way after 2 us; blocks with equal runs end up to 12 us apart, arriving takes
 // 1.5 and the last join up to 5.
-// 4 bits (1.125 d + 2 bytes): 41, 82 and 50 us, 3.7, 4.7 and 3.4 TB/s.  Bound by the
+// 4 bits (1.125 d + 2 bytes): 40, 82 and 50 us, 3.8, 4.7 and 3.4 TB/s.  Bound by the
 // instructions that turn codes into operands: a page of d = 128 takes 335 a warp, 150 of
 // them masks and multiply-adds of codes, at 60% of the issue slots (a fourth block per SM
 // issues no more).  Without any of the conversions 16 x 8192 takes 35 us.
