@@ -699,8 +699,8 @@ tq_status tq_norm_rope_destroy(tq_norm_rope_plan* plan);
  *              row outside [0, num_kv_rows) does, too, and sets TQ_DEVERR_CHUNK.  Rows
  *              of one call must differ
  *   q_out      [num_tokens][H_q][d]; k_out, v_out [num_kv_rows][H_kv][d], at least
- *              num_tokens rows without kv_rows.  q_out may be q with its stride and, without
- *              kv_rows, k_out may be k and v_out v; no other overlap
+ *              num_tokens rows without kv_rows.  q_out may be q with its stride (another
+ *              one is refused) and, without kv_rows, k_out k and v_out v; no other overlap
  * Bases and strides: multiples of 16 bytes.  Rows no token names are left as they
  * were.  num_tokens == 0 is a no-op.
  */

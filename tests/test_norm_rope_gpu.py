@@ -339,3 +339,26 @@ def test_one_handle_on_two_streams():
             h.apply(*a, q_out=o[0], k_out=o[1], stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for o, w in zip(outs, want) for x, y in zip(o, w))
+
+
+def test_in_place_with_another_stride_is_refused():
+    h = tq.TQNormRope(head_dim=128, num_q_heads=2, num_kv_heads=2)
+    rows = torch.zeros(6, 1024, dtype=torch.bfloat16, device="cuda")
+    apart = [rows[:, at:at + 256].view(6, 2, 128) for at in (0, 256, 512)]
+    p = torch.arange(6, dtype=torch.int32, device="cuda")
+
+    def near(x):
+        return torch.as_strided(x, (6, 2, 128), (256, 128, 1))
+
+    q, k, v = apart
+    own = torch.zeros(6, 2, 128, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(q_out=near(q), k_out=k), dict(q_out=q, k_out=near(k)), dict(q_out=q, k_out=k, v=v, v_out=near(v))):
+        with pytest.raises(tq.TQError) as e:
+            h.apply(q, k, p, **kw)
+        assert e.value.status == -1
+    # (with the same stride, a single row, or the keys somewhere else it is a call like any other)
+    h.apply(q, k, p, q_out=q, k_out=k, v=v, v_out=v)
+    h.apply(q[:1], k[:1], p[:1], q_out=near(q)[:1], k_out=near(k)[:1])
+    h.apply(q, k, p, q_out=q, k_out=own, kv_rows=p)
+    torch.cuda.synchronize()
+    assert h.device_error() == 0

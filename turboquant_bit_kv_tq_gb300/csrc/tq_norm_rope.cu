@@ -689,6 +689,10 @@ tq_status tq_norm_rope(const tq_norm_rope_plan* c, const void* q, const void* k,
     if (q_stride < qr || q_out_stride < qr || k_stride < kr || k_out_stride < kr || (v && (v_stride < kr || v_out_stride < kr)))
         return TQ_ERR_INVALID_ARG;
     if (!v) v_stride = v_out_stride = 0;
+    // in place means row by row in place
+    if (num_tokens > 1 && ((q_out == q && q_out_stride != q_stride) ||
+                           (!kv_rows && ((k_out == k && k_out_stride != k_stride) || (v && v_out == v && v_out_stride != v_stride)))))
+        return TQ_ERR_INVALID_ARG;
     const int sz = dtype == TQ_DTYPE_F32 ? 4 : 2;
     const uintptr_t bits = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out | (uintptr_t)k_out | (uintptr_t)v_out |
                            (uintptr_t)q_weight | (uintptr_t)k_weight |
