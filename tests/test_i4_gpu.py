@@ -585,3 +585,29 @@ def test_load_is_captured_and_replayed():
         for b, n in enumerate(lens):
             want[:, 100 * b:100 * b + n] = i4.rows(pages, table[b], n, 128)
         assert np.array_equal(_np(ko), want[0]) and np.array_equal(_np(vo), want[1])
+
+
+@pytest.mark.parametrize("d,hkv,g,count,shortest,longest,qt,ot", [
+    (128, 1, 4, 400, 150, 2000, "bf16", "bf16"),  # even runs: several units, and parts of them, each
+    (128, 1, 12, 270, 150, 2000, "f32", "f32"),
+    (256, 1, 4, 270, 150, 2000, "bf16", "f32"),
+    (128, 8, 4, 57, 0, 300, "bf16", "bf16"),      # about as many units as blocks: a unit a run
+    (128, 4, 2, 100, 0, 400, "f16", "f16"),       # runs of a few units' longest
+    (256, 2, 20, 30, 0, 300, "bf16", "f32"),      # two units share a head's pages
+    (128, 8, 4, 61, 0, 300, "bf16", "bf16"),      # more units than blocks: whole ones to blocks
+    (128, 1, 16, 500, 0, 700, "f32", "bf16"),
+    (256, 1, 4, 400, 0, 600, "bf16", "bf16"),
+])
+def test_how_units_are_dealt_out(d, hkv, g, count, shortest, longest, qt, ot):
+    rng = _rng(75, d, hkv, g, count)
+    lens = [int(x) for x in rng.integers(shortest, min(longest, shortest + 300), count)]
+    lens[count // 2], lens[3] = longest, 1
+    c, q, table = _decode_case(d, hkv, g, lens, qt, 81)
+    args = (q.cuda(), _gpu(table), _lens(lens))
+    got = c.decode(*args, out_dtype=DT[ot])
+    _check_decode(c, q, table, lens, got)
+    assert torch.equal(got, c.decode(*args, out_dtype=DT[ot])) and c.device_error() == 0
+    # a sequence by itself: other runs, the same bounds
+    one = slice(count // 2, count // 2 + 1)
+    got = c.decode(*(x[one] for x in args), out_dtype=DT[ot])
+    _check_decode(c, q[one], table[one], lens[one], got)

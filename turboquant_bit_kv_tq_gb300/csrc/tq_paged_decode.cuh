@@ -15,7 +15,8 @@
 // runs to a fixed grid of resident blocks: evenly, one run per block, whose warps share
 // its segments (the pages of one (sequence, KV head) each) step by step and add up in
 // shared memory at a segment's end; or, with many short sequences, whole (sequence,
-// KV head)s to warps, and no warp waits for another.  Each warp keeps a ring of steps of
+// KV head)s to warps, and no warp waits for another; at 4 bits also in runs that keep to
+// one (sequence, KV head), or whole ones to blocks.  Each warp keeps a ring of steps of
 // a page or two in flight, across segments.  At 8 bits a page comes by a tensor copy, whose
 // 128-byte swizzle lays the rows out so that the operand reads below meet no bank conflict,
 // and one small copy of its scales.  (16-byte cp.async in a swizzle of our own moved as
@@ -257,6 +258,14 @@ __device__ __forceinline__ float2 paged_norm(float X, float L) {
     return L == 0.f ? make_float2(0.f, 0.f) : make_float2(half / L, half);
 }
 
+constexpr int kPagedRun = 16;  // pages of a run, on average, at least (two steps for each warp)
+// Longest run and unit up to which runs keep to units at 4 bits.  d = 128, 8 KV heads, even
+// runs and these: 4 x up to 700 tokens 20.4 us, 10.8; 16 x up to 1000 28.3, 12.4; 1 x 8000
+// 21.8, 16.8; 4 x 16384 (77 pages) 29.1, 27.0; 8 x 8192 (83) 27.5, 27.6; 16 x 4096 (100)
+// 28.8, 29.9; 1 x 131072 (147) 43.2, 44.6.  Many units: 64 x up to 300 22.1, 13.3; 100 x up
+// to 700 28.2, 24.7; 64 x 1000 30.3, 31.1; 100 x up to 1500 (94) 35.1, 36.4; d = 256, fp32: 80 x
+// up to 700 35.2, 30.3; 160 x up to 1000 (63) 46.1, 48.2.
+constexpr int kPagedWhole = 88;
 constexpr int kPagedSoloPages = 16;  // a warp takes units of up to this many pages alone, whatever its share
 // The parts of up to kPagedJoin blocks are joined by the last of them; of more, by the
 // last of each kPagedGroup, and the groups' by the last group (one KV head, 32768 tokens
@@ -311,35 +320,63 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     const int per = (a.batch + 31) >> 5;
     const int bt0 = min(a.batch, lane * per), bt1 = min(a.batch, bt0 + per);
     int mine = 0, some = 0, most = 0;
+    bool bad = false;
+    // (as often for every lane: where some left earlier the first copies went out 5 us later.
+    // 200 x 1000 tokens, 8 KV heads: 4 bits 63.5 us, 57.6; 8 bits 76.1, 70.9)
 #pragma unroll 4
-    for (int b = bt0; b < bt1; ++b) {
-        const int len = __ldg(a.lens + b);
-        if (len < 0 || len > a.max_blocks * 16) set_error(a.err, TQ_DEVERR_SEQLEN);
+    for (int i = 0; i < per; ++i) {
+        const int len = bt0 + i < bt1 ? __ldg(a.lens + bt0 + i) : 0;
+        bad |= len < 0 || len > a.max_blocks * 16;
         const int np = paged_pages(a, len);
         mine += np;
         some += np > 0;
         most = max(most, np);
     }
+    if (bad) set_error(a.err, TQ_DEVERR_SEQLEN);
+    __syncwarp();
     const int units = (int)__reduce_add_sync(0xffffffffu, (unsigned)some) * nj;
     const int all_pages = (int)__reduce_add_sync(0xffffffffu, (unsigned)mine) * nj;
     most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
-    // One run per block, of at least 16 pages on average (two steps for each
-    // warp); or, with more units than blocks and none much longer than a warp's
-    // share, a run of whole units per warp (256 x 100 tokens, 8 KV heads: 22 us, block
-    // runs 30; 256 x up to 200: 21, 37; 512 x up to 400: 53, 69).
+    // One even run per block, of at least kPagedRun pages on average; or, with more units
+    // than blocks and none much longer than a warp's share, a run of whole units per warp
+    // (256 x 100 tokens, 8 KV heads: 22 us, block runs 30; 256 x up to 200: 21, 37; 512 x
+    // up to 400: 53, 69).
     const int warps = (int)gridDim.x * W, share = all_pages / warps;
     const bool solo = units > (int)gridDim.x && most <= max(kPagedSoloPages, 2 * share);
+    // At 4 bits, where a run has less to copy, a unit that begins within one costs more than
+    // uneven runs, up to kPagedWhole pages of a run or of a unit:
+    // whole: up to as many units as blocks, runs of a fixed length that fill a unit each;
+    // packed: more units, each of them to the block in whose even run it starts.
+    // (8 bits: even runs as ever, with the same order of the sums.)
+    bool whole = false;
+    const bool packed = BITS == 4 && !solo && units > (int)gridDim.x && most <= kPagedWhole * 128 / D;
     // (a fixed cost, of less weight where the runs are short: the last of several runs
     // of a unit would be left with few pages)
-    const int cost = min(paged_unit_cost(BITS), share);
+    int cost = packed ? paged_unit_cost(BITS) : min(paged_unit_cost(BITS), share);
+    uint32_t inv = 0;  // 2^32 / cost, rounded up: quotients of up to 2^16 are exact
+    if (BITS == 4 && !solo && units <= (int)gridDim.x) {
+        // (a run more than its even share for each unit.  The quotient may be 2^-20 of itself
+        // too low: the runs' number, a whole one, stays below the grid plus 1 / fit)
+        const float even = __fdividef((float)all_pages, (float)((int)gridDim.x - units));
+        const int fit = min(most, __float2int_ru(even * (1.f - 0x1p-20f)));
+        whole = fit <= kPagedWhole;
+        // (the length of a run, which no unit's empty places exceed)
+        if (whole) cost = max(fit, most <= 2 * kPagedRun ? 2 * kPagedRun : kPagedRun), inv = 0xFFFFFFFFu / (uint32_t)cost + 1;
+    }
+    auto places = [&](int np) { return whole ? (int)__umulhi(np + cost - 1, inv) * cost : paged_places(np, cost); };
     mine += cost * some;
+    if (whole) {
+        mine = 0;
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) mine += places(bt0 + i < bt1 ? paged_pages(a, __ldg(a.lens + bt0 + i)) : 0);
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    const int before = (incl - mine) * nj, total = all_pages + cost * units;
+    const int before = (incl - mine) * nj, total = whole ? __shfl_sync(0xffffffffu, incl, 31) * nj : all_pages + cost * units;
     // sequences without a token: their rows are zero
     if (units < a.batch * nj)
         for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
@@ -349,8 +386,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         }
     if (total == 0) return;
     PagedRuns runs;
-    runs.n = solo ? (uint32_t)min(warps, total)
-                  : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, all_pages / units / 16));
+    runs.n = solo     ? (uint32_t)min(warps, total)
+             : packed ? (uint32_t)min((int)gridDim.x, total)
+             : whole  ? __umulhi(total, inv)
+                     : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, all_pages / units / kPagedRun));
     runs.q = (uint32_t)total / runs.n;
     runs.r = (uint32_t)total - runs.q * runs.n;
     if (tid == 0) s_runs = runs;  // for the joins, behind a barrier
@@ -365,7 +404,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
             if (here)
                 for (;; ++b) {
                     len = __ldg(a.lens + b);
-                    const int n = paged_places(paged_pages(a, len), cost) * nj;
+                    const int n = places(paged_pages(a, len)) * nj;
                     if (u < at + n) break;
                     at += n;
                 }
@@ -373,7 +412,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
             PagedWalk w;
             w.b = __shfl_sync(0xffffffffu, b, src);
             w.len = paged_clamp(a, __shfl_sync(0xffffffffu, len, src));
-            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = paged_places((w.len + 15) >> 4, cost);
+            const int rel = u - __shfl_sync(0xffffffffu, at, src), np = places((w.len + 15) >> 4);
             w.j = rel / np;
             w.p = rel - w.j * np;
             w.left = total - u;
@@ -382,7 +421,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         };
         int u0 = (int)runs.start(run), u1 = (int)runs.start(run + 1);
         PagedWalk cons = locate(u0);
-        if (solo) {
+        if (solo || packed) {
             // the units that start in [u0, u1)
             if (u1 < total) {
                 const PagedWalk w = locate(u1);
