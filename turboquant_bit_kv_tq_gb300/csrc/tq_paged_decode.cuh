@@ -38,7 +38,7 @@
 // caches add bytes at 6.3 to 6.7 TB/s; the rest is about 15 us a call: the first pages are
 // under way after 2 us; blocks with equal runs end up to 12 us apart, arriving takes
 // 1.5 and the last join up to 5.
-// 4 bits (1.125 d + 2 bytes): 40, 82 and 50 us, 3.8, 4.7 and 3.4 TB/s.  Bound by the
+// 4 bits (1.125 d + 2 bytes): 40, 82 and 51 us, 3.8, 4.7 and 3.3 TB/s.  Bound by the
 // instructions that turn codes into operands: a page of d = 128 takes 335 a warp, 150 of
 // them masks and multiply-adds of codes, at 60% of the issue slots (a fourth block per SM
 // issues no more).  Without any of the conversions 16 x 8192 takes 35 us.
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
     // (a fixed cost, of less weight where the runs are short: the last of several runs
     // of a unit would be left with few pages)
     int cost = packed ? paged_unit_cost(BITS) : min(paged_unit_cost(BITS), share);
-    uint32_t inv = 0;  // 2^32 / cost, rounded up: quotients of up to 2^16 are exact
+    uint32_t inv = 0;  // 2^32 / cost, and up to 2^-19 of it more: quotients of less than 2^19 are exact
     if (BITS == 4 && !solo && units <= (int)gridDim.x) {
         // (a run more than its even share for each unit.  The quotient may be 2^-20 of itself
         // too low: the runs' number, a whole one, stays below the grid plus 1 / fit)
@@ -361,11 +361,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
         const int fit = min(most, __float2int_ru(even * (1.f - 0x1p-20f)));
         whole = fit <= kPagedWhole;
         // (the length of a run, which no unit's empty places exceed)
-        if (whole) cost = max(fit, most <= 2 * kPagedRun ? 2 * kPagedRun : kPagedRun), inv = 0xFFFFFFFFu / (uint32_t)cost + 1;
+        if (whole) cost = max(fit, most <= 2 * kPagedRun ? 2 * kPagedRun : kPagedRun);
+        inv = __float2uint_ru(__fdividef(0x1p32f * (1.f + 0x1p-20f), (float)max(cost, kPagedRun)));
     }
     auto places = [&](int np) { return whole ? (int)__umulhi(np + cost - 1, inv) * cost : paged_places(np, cost); };
-    mine += cost * some;
-    if (whole) {
+    if (!whole) {
+        mine += cost * some;
+    } else if (per == 1) {
+        mine = places(mine);
+    } else {
         mine = 0;
 #pragma unroll 1
         for (int i = 0; i < per; ++i) mine += places(bt0 + i < bt1 ? paged_pages(a, __ldg(a.lens + bt0 + i)) : 0);
@@ -390,8 +394,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedCfg<BITS, D, NT, PREC>::CT
              : packed ? (uint32_t)min((int)gridDim.x, total)
              : whole  ? __umulhi(total, inv)
                      : (uint32_t)min((long long)gridDim.x, (long long)units * max(1, all_pages / units / kPagedRun));
-    runs.q = (uint32_t)total / runs.n;
-    runs.r = (uint32_t)total - runs.q * runs.n;
+    runs.q = whole ? (uint32_t)cost : (uint32_t)total / runs.n;
+    runs.r = whole ? 0u : (uint32_t)total - runs.q * runs.n;
     if (tid == 0) s_runs = runs;  // for the joins, behind a barrier
     const uint32_t run = solo ? blockIdx.x * W + warp : blockIdx.x;
 
