@@ -611,3 +611,22 @@ def test_how_units_are_dealt_out(d, hkv, g, count, shortest, longest, qt, ot):
     one = slice(count // 2, count // 2 + 1)
     got = c.decode(*(x[one] for x in args), out_dtype=DT[ot])
     _check_decode(c, q[one], table[one], lens[one], got)
+
+
+@pytest.mark.parametrize("d,h,count,longest", [(128, 2, 33, 90), (256, 1, 100, 60), (128, 1, 70, 1500)])
+def test_load_of_many_sequences(d, h, count, longest):
+    """More sequences than are looked at together, some of them empty, with gaps between their rows."""
+    rng = _rng(76, d, count)
+    lens = [int(x) for x in rng.integers(0, longest, count)]
+    lens[0], lens[31], lens[32], lens[-1] = 0, longest, 0, 17
+    c, _, table = _decode_case(d, h, 1, lens, "bf16", 82)
+    gaps = rng.integers(0, 4, count)
+    starts = np.concatenate([[2], 2 + np.cumsum(np.array(lens) + gaps)]).astype(np.int32)
+    want = np.full((2, int(starts[-1]) + 3, h, d), -7.0)
+    ko, vo = (_gpu(x, torch.float32) for x in want)
+    c.load(_gpu(table), _lens(lens), _gpu(starts[:-1]), ko, vo)
+    pages = c.pages().cpu().numpy()
+    for b, n in enumerate(lens):
+        want[:, starts[b]:starts[b] + n] = i4.rows(pages, table[b], n, d)
+    assert np.array_equal(_np(ko), want[0]) and np.array_equal(_np(vo), want[1])
+    assert c.device_error() == 0

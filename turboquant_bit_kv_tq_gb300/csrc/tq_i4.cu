@@ -204,8 +204,9 @@ static tq_status launch_i4_store(const I4StoreArgs& a, cudaStream_t s) {
 // The pages of all sequences, in the order (sequence, page, KV head), are dealt out to
 // the warps of a fixed grid; a warp reads one page and writes its 16 rows of keys and
 // of values, a lane 16 elements (one scale) at a time.  Bound by memory, four fifths of it
-// writes: 16 sequences of up to 16384 tokens, 8 heads, d = 128, to bf16: 113 us, 6290 GB/s
-// (93% of a plain copy); with 16-byte stores, half a sector each, 129.
+// writes: 16 sequences of up to 16384 tokens, 8 heads, d = 128, to bf16: 109 us, 6510 GB/s
+// (96% of a plain copy); with 16-byte stores, half a sector each, 129.  (Sequence by sequence
+// the walk alone took every warp a quarter of a microsecond each: 100 x up to 700 53 us, now 33.)
 struct I4LoadArgs {
     const uint8_t* cache;
     const int32_t *table, *lens, *cu;
@@ -254,14 +255,14 @@ __global__ void __launch_bounds__(kI4LoadThreads) i4_load_kernel(I4LoadArgs a) {
     constexpr int PAGE = i4_page_bytes(D);
     constexpr int CPR = D / 16;  // pieces of a row
     const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kI4LoadThreads / 32);
-    const int64_t w0 = (int64_t)blockIdx.x * (kI4LoadThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t warps = gridDim.x * (kI4LoadThreads / 32);
+    const uint32_t w0 = blockIdx.x * (kI4LoadThreads / 32) + (threadIdx.x >> 5);
     const int cap = a.max_blocks * 16;
     pdl_wait();  // (the launch overlaps the previous kernel's end)
-    // the walk over the sequences is the same for every warp: warp w takes the
-    // units w, w + warps, ... of the running count
-    int64_t done = 0;  // units before sequence b
-    int64_t next = w0;
+    // the walk over the sequences, 32 at a time, is the same for every warp: warp w takes
+    // the units w, w + warps, ... of the running count (which the configuration keeps in 32 bits)
+    uint32_t done = 0;  // units before sequence b0
+    uint32_t next = w0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int bl = b0 + lane;
         int len = bl < a.batch ? __ldg(a.lens + bl) : 0;
@@ -270,46 +271,52 @@ __global__ void __launch_bounds__(kI4LoadThreads) i4_load_kernel(I4LoadArgs a) {
             len = len < 0 ? 0 : cap;
         }
         const int start = bl < a.batch ? __ldg(a.cu + bl) : 0;
-        const int nb = min(32, a.batch - b0);
-        for (int i = 0; i < nb; ++i) {
+        const uint32_t mine = (uint32_t)((len + 15) >> 4) * (uint32_t)a.heads;
+        uint32_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+        while (next - done < all) {
+            const uint32_t at = next - done;
+            next += warps;
+            const int i = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;  // its sequence
             const int n = __shfl_sync(0xffffffffu, len, i);
             const int row0 = __shfl_sync(0xffffffffu, start, i);
-            const int64_t units = (int64_t)((n + 15) >> 4) * a.heads;
-            while (next < done + units) {
-                const int64_t u = next - done;
-                next += warps;
-                const int p = (int)(u / a.heads), h = (int)(u - (int64_t)p * a.heads);
-                const int blk = __ldg(a.table + (int64_t)(b0 + i) * a.max_blocks + p);
-                if (blk < 0 || blk >= a.num_blocks) {
-                    if (lane == 0) set_error(a.err, TQ_DEVERR_BLOCK);
+            const uint32_t u = at - __shfl_sync(0xffffffffu, incl - mine, i);
+            const int p = (int)(u / (uint32_t)a.heads), h = (int)(u - (uint32_t)p * (uint32_t)a.heads);
+            const int blk = __ldg(a.table + (int64_t)(b0 + i) * a.max_blocks + p);
+            if (blk < 0 || blk >= a.num_blocks) {
+                if (lane == 0) set_error(a.err, TQ_DEVERR_BLOCK);
+                continue;
+            }
+            const uint8_t* page = a.cache + ((int64_t)blk * a.heads + h) * PAGE;
+            const int rows = min(16, n - 16 * p);
+            const uint32_t eb = __ldg(page + i4_exps_at(D) + lane);  // lanes 0-15: keys, 16-31: values
+            uint2 c[CPR];
+            uint32_t sb[CPR];
+#pragma unroll
+            for (int j = 0; j < CPR; ++j) {
+                c[j] = __ldg(reinterpret_cast<const uint2*>(page) + lane + 32 * j);
+                sb[j] = __ldg(page + i4_scales_at(D) + lane + 32 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < CPR; ++j) {
+                const int idx = lane + 32 * j, r = idx / CPR, ch = idx % CPR;  // r: 0-15 keys, 16-31 values
+                const float scale = f8_scale(__shfl_sync(0xffffffffu, eb, r));
+                const int64_t row = (int64_t)row0 + 16 * p + (r & 15);
+                if ((r & 15) >= rows) continue;
+                if (row < 0 || row >= a.n_rows) {
+                    set_error(a.err, TQ_DEVERR_CHUNK);
                     continue;
                 }
-                const uint8_t* page = a.cache + ((int64_t)blk * a.heads + h) * PAGE;
-                const int rows = min(16, n - 16 * p);
-                const uint32_t eb = __ldg(page + i4_exps_at(D) + lane);  // lanes 0-15: keys, 16-31: values
-                uint2 c[CPR];
-                uint32_t sb[CPR];
-#pragma unroll
-                for (int j = 0; j < CPR; ++j) {
-                    c[j] = __ldg(reinterpret_cast<const uint2*>(page) + lane + 32 * j);
-                    sb[j] = __ldg(page + i4_scales_at(D) + lane + 32 * j);
-                }
-#pragma unroll
-                for (int j = 0; j < CPR; ++j) {
-                    const int idx = lane + 32 * j, r = idx / CPR, ch = idx % CPR;  // r: 0-15 keys, 16-31 values
-                    const float scale = f8_scale(__shfl_sync(0xffffffffu, eb, r));
-                    const int64_t row = (int64_t)row0 + 16 * p + (r & 15);
-                    if ((r & 15) >= rows) continue;
-                    if (row < 0 || row >= a.n_rows) {
-                        set_error(a.err, TQ_DEVERR_CHUNK);
-                        continue;
-                    }
-                    // (exact: multiples of 2^-144, at most 2^127)
-                    i4_put16<OT>(r < 16 ? a.k : a.v, (row * a.heads + h) * D + 16 * ch, c[j], i4_scale(sb[j]) * scale, a.wide);
-                }
+                // (exact: multiples of 2^-144, at most 2^127)
+                i4_put16<OT>(r < 16 ? a.k : a.v, (row * a.heads + h) * D + 16 * ch, c[j], i4_scale(sb[j]) * scale, a.wide);
             }
-            done += units;
         }
+        done += all;
     }
 }
 
@@ -318,8 +325,13 @@ static tq_status launch_i4_load(const I4LoadArgs& a, cudaStream_t s) {
     int sms = 0;
     const tq_status st = device_sms(&sms);
     if (st != TQ_OK) return st;
-    const int64_t most = (int64_t)a.batch * a.max_blocks * a.heads;
-    const int64_t blocks = std::min<int64_t>((most + 7) / 8, (int64_t)sms * 8);
+    // pages there may be: those of the table, and of the rows to be written.  Two of them a warp,
+    // from 8 to 32 blocks per SM: blocks that follow one another keep to fewer places in memory
+    // (16 x up to 16384: 8 per SM 115.8 us, 16 112, 24 110, 32 108.4; 100 x up to 700: 8 to 16 33,
+    // 32 35)
+    const int64_t most = std::min((int64_t)a.batch * a.max_blocks, (a.n_rows >> 4) + a.batch) * a.heads;
+    constexpr int W = kI4LoadThreads / 32;
+    const int64_t blocks = std::min((most + W - 1) / W, std::max((int64_t)sms * 8, std::min((int64_t)sms * 32, most / (2 * W))));
     return cuda_status(launch_pdl(true, i4_load_kernel<D, OT>, dim3((unsigned)blocks), dim3(kI4LoadThreads), 0, s, a));
 }
 
