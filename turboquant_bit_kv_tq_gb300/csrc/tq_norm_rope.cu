@@ -10,7 +10,7 @@
 //
 // Few tokens: a warp takes a token, or some of its heads, 4 (d = 128) or 2 at a time, and
 // computes the token's sines once, each lane some of those that the lanes beside it with
-// the same pieces need, too.  16 rows of 32/8 heads: 2.5 us, the chain of position, sine,
+// the same pieces need, too.  16 rows of 32/8 heads: 2.4 us, the chain of position, sine,
 // product.  (The 8192 rows took 48 us so: too little under way.)
 //
 // A pair turns by F 2^-64 of a full turn a position, F = its frequency / 2 pi in
@@ -112,13 +112,12 @@ __device__ __forceinline__ void rope_weights(const void* g, int at, int dtype, f
     }
 }
 
-// sums over the d/16 lanes of a head of U heads' values, the exchanges side by side
-template <int LPV, int U>
-__device__ __forceinline__ void rope_sums(float (&v)[U]) {
+// a value's sum over the d/16 lanes of a head
+template <int LPV>
+__device__ __forceinline__ float rope_sum(float v) {
 #pragma unroll
-    for (int o = LPV / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+    for (int o = LPV / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 __device__ __forceinline__ float rope_squares(const float (&x)[16]) {
     float s[2] = {0.f, 0.f};
@@ -145,9 +144,8 @@ __device__ __forceinline__ float rope_far(float (&x)[16], float mean, float eps,
         for (int j = 0; j < 16; ++j) x[j] *= f;
         eps = eps * f * f;
     }
-    float ss[1] = {rope_squares(x)};
-    rope_sums<LPV>(ss);
-    return far ? fmaf(ss[0], 1.f / D, eps) : mean;
+    const float ss = rope_sum<LPV>(rope_squares(x));
+    return far ? fmaf(ss, 1.f / D, eps) : mean;
 }
 
 // sine and cosine of position p for one pair
@@ -161,7 +159,6 @@ __device__ __forceinline__ float2 rope_turn(uint64_t p, uint64_t turns) {
 template <int D, int DT>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     constexpr int LPV = D / 16, VPW = 32 / LPV;  // lanes per head, heads at a time
-    constexpr int U = 2;  // steps whose loads are under way together
     const int lane = threadIdx.x & 31, sub = lane % LPV, slot = lane / LPV;
     const int64_t item = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int64_t t = item / a.parts;
@@ -240,78 +237,57 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
                 fs[j] = f * sn[j], gs[j] = g2 * sn[j];
             }
         }
+        // (one step at a time: the registers of a second one's loads cost more warps than they
+        // gain, 9000 rows of 8/1 heads 26.2 us, 20.7)
 #pragma unroll 1
-        for (int i = lo; i < hi; i += U) {
-            RopeRaw<DT> raw[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i + u < hi && h + u * VPW < heads) {
-                    raw[u][0].load(src, (int64_t)u * VPW * D * SZ);
-                    raw[u][1].load(src + second, (int64_t)u * VPW * D * SZ);
-                } else {
-                    raw[u][0].clear();
-                    raw[u][1].clear();
-                }
+        for (int i = lo; i < hi; ++i) {
+            const bool here = h < heads;
+            RopeRaw<DT> raw[2];
+            if (here) {
+                raw[0].load(src, 0);
+                raw[1].load(src + second, 0);
+            } else {
+                raw[0].clear();
+                raw[1].clear();
             }
-            float mean[U];  // with eps
-            bool far = false;
-            if (kind < 2 && a.norm) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float x[16];
-                    raw[u][0].values(x);
-                    raw[u][1].values(x + 8);
-                    mean[u] = rope_squares(x);
+            if (kind < 2) {
+                float x[16], r = 1.f;
+                raw[0].values(x);
+                raw[1].values(x + 8);
+                if (a.norm) {
+                    const float sum = rope_sum<LPV>(rope_squares(x));
+                    float mean = fmaf(sum, 1.f / D, a.eps);  // with eps
+                    const bool far = !(sum < INFINITY) || mean < 0x1p-100f;
+                    if (__any_sync(0xffffffffu, far)) mean = rope_far<D>(x, mean, a.eps, far);
+                    r = rsqrtf(mean);
                 }
-                rope_sums<LPV>(mean);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool inf = !(mean[u] < INFINITY);
-                    mean[u] = fmaf(mean[u], 1.f / D, a.eps);
-                    far |= inf || mean[u] < 0x1p-100f;
-                }
-                far = __any_sync(0xffffffffu, far);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i + u >= hi) break;  // (the same for the whole warp)
-                const bool here = h + u * VPW < heads;
-                if (kind < 2) {
-                    float x[16], r = 1.f;
-                    raw[u][0].values(x);
-                    raw[u][1].values(x + 8);
-                    if (a.norm) {
-                        if (far) mean[u] = rope_far<D>(x, mean[u], a.eps, !(mean[u] < INFINITY) || mean[u] < 0x1p-100f);
-                        r = rsqrtf(mean[u]);
-                    }
-                    auto turn = [&](int j, float& y, float& z) {
-                        const float yy = y * r, zz = z * r;  // (first: small elements may be subnormal)
-                        if (turned) {
-                            y = fmaf(yy, fc[j], -zz * gs[j]);
-                            z = fmaf(zz, gc[j], yy * fs[j]);
-                        } else {
-                            y = yy * fc[j];
-                            z = zz * gc[j];
-                        }
-                    };
-                    if (a.interleaved) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) turn(j, x[2 * j], x[2 * j + 1]);
+                auto turn = [&](int j, float& y, float& z) {
+                    const float yy = y * r, zz = z * r;  // (first: small elements may be subnormal)
+                    if (turned) {
+                        y = fmaf(yy, fc[j], -zz * gs[j]);
+                        z = fmaf(zz, gc[j], yy * fs[j]);
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) turn(j, x[j], x[8 + j]);
+                        y = yy * fc[j];
+                        z = zz * gc[j];
                     }
-                    raw[u][0].set(x);
-                    raw[u][1].set(x + 8);
+                };
+                if (a.interleaved) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) turn(j, x[2 * j], x[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) turn(j, x[j], x[8 + j]);
                 }
-                if (here) {
-                    raw[u][0].store(dst, (int64_t)u * VPW * D * SZ);
-                    raw[u][1].store(dst + second, (int64_t)u * VPW * D * SZ);
-                }
+                raw[0].set(x);
+                raw[1].set(x + 8);
             }
-            src += (int64_t)U * VPW * D * SZ;
-            dst += (int64_t)U * VPW * D * SZ;
-            h += U * VPW;
+            if (here) {
+                raw[0].store(dst, 0);
+                raw[1].store(dst + second, 0);
+            }
+            src += VPW * D * SZ;
+            dst += VPW * D * SZ;
+            h += VPW;
         }
     }
 }
@@ -326,7 +302,7 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
 constexpr int kRopeStages = 3, kRopeBulkWarps = 4, kRopeBulkCtas = 5;
 constexpr int kRopePieceBytes = 13312;  // of a stage: 5 blocks of 3 stages share an SM
 // This kernel is taken from so many pieces per SM and bytes of a piece on.  32/8 heads,
-// d = 128, bf16 (12 KB): 152 tokens 3.3 us here, 3.0 by the other one; 304 3.6, 3.9; 1216
+// d = 128, bf16 (12 KB): 152 tokens 3.3 us here, 3.0 by the other one; 304 3.6, 3.6; 1216
 // 6.6, 7.6; 4864 22.0, 27.1.  64/8 heads (2 x 10 KB): 152 3.4, 3.5; 4864 33.8, 41.2.
 // 8/1 heads (2.5 KB): 1216 4.4, 3.8; 2432 6.6, 5.5; 4864 10.9, 11.3.
 constexpr int kRopeBulkFrom = 2, kRopeBulkLeast = 6144;
@@ -485,13 +461,11 @@ __global__ void __launch_bounds__(32 * kRopeBulkWarps, kRopeBulkCtas) norm_rope_
                     q[j & 1] = rope_fma2(z, z, q[j & 1]);
                 }
                 const float2 q0 = rope_unpack(q[0]), q1 = rope_unpack(q[1]);
-                float mean[1] = {(q0.x + q0.y) + (q1.x + q1.y)};
-                rope_sums<LPV>(mean);
-                const bool inf = !(mean[0] < INFINITY);
-                mean[0] = fmaf(mean[0], 1.f / D, a.eps);
-                const bool far = inf || mean[0] < 0x1p-100f;
-                if (__any_sync(0xffffffffu, far)) mean[0] = rope_far<D>(x, mean[0], a.eps, far);
-                const float r = rsqrtf(mean[0]);
+                const float sum = rope_sum<LPV>((q0.x + q0.y) + (q1.x + q1.y));
+                float mean = fmaf(sum, 1.f / D, a.eps);
+                const bool far = !(sum < INFINITY) || mean < 0x1p-100f;
+                if (__any_sync(0xffffffffu, far)) mean = rope_far<D>(x, mean, a.eps, far);
+                const float r = rsqrtf(mean);
                 const uint64_t rr = rope_pack(r, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
