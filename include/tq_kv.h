@@ -747,8 +747,8 @@ tq_status tq_plan_destroy(tq_plan* plan);
  *            position L + i, slot table[b][(L + i) / 16] * 16 + (L + i) % 16, and row
  *            cu_k[b] + L + i of packed keys (tq_f8_load's and tq_norm_rope's rows,
  *            tq_prompt_attention's cu_k)
- *   lengths  seq_lens[b] = L + n; cu_q, cu_k [batch + 1]: sums of n and of seq_lens;
- *            *next_free_out = *next_free + the blocks taken
+ *   lengths  seq_lens[b] = L + n; cu_q, cu_k [batch + 1]: sums of n and of L + n (cut
+ *            off at 2^31 - 1); *next_free_out = *next_free + the blocks taken
  * lens, new_lens   device int32 [batch]
  * free_blocks      device int32 [num_free]; ids are passed on unchecked, but a
  *                  token whose block id is negative gets slot -1
@@ -760,9 +760,12 @@ tq_status tq_plan_destroy(tq_plan* plan);
  * replayed.  No other overlap.
  * What does not fit is left out, and a request's length grows by its tokens with a
  * slot only: beyond its row of the table (TQ_DEVERR_SEQLEN), beyond the list
- * (TQ_DEVERR_POOL), beyond num_tokens (TQ_DEVERR_CHUNK, cu_q cut off there).  Such
- * tokens get slot -1 and row -1.  lens outside [0, 16 max_blocks_per_seq] and negative
- * new_lens are clamped (TQ_DEVERR_SEQLEN), *next_free to [0, num_free] (TQ_DEVERR_POOL).
+ * (TQ_DEVERR_POOL), beyond num_tokens (TQ_DEVERR_CHUNK, cu_q and cu_k cut off
+ * there).  Such tokens get slot -1 and row -1.  Those within num_tokens keep their
+ * places in cu_q and cu_k, so that causal prompt attention lines the request's other
+ * tokens up with the keys before them; the rows of keys that are left free lie behind
+ * all that those see.  lens outside [0, 16 max_blocks_per_seq] and negative new_lens
+ * are clamped (TQ_DEVERR_SEQLEN), *next_free to [0, num_free] (TQ_DEVERR_POOL).
  * 1 <= batch <= max_batch; 0 <= num_tokens, num_free < 2^31.  One launch.
  */
 tq_status tq_plan_step(const tq_plan* plan, const int32_t* lens, const int32_t* new_lens, int batch,

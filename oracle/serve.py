@@ -63,7 +63,8 @@ def norm_rope(x, weight, positions, inv_freq, eps, interleaved=False, norm=True)
 
 
 def plan(lens, new, table, free, next_free, n_tokens):
-    """One step's plan, token by token: (table, slots, positions, kv_rows, seq_lens, cu_q, cu_k, next)."""
+    """One step's plan, token by token: (table, slots, positions, kv_rows, seq_lens, cu_q, cu_k, next).  Packed
+    keys keep a row for every new token of a request, served or not."""
     table = table.copy()
     cap = table.shape[1] * BLOCK
     slots, pos, rows = (np.full(n_tokens, x, np.int64) for x in (-1, 0, -1))
@@ -90,5 +91,5 @@ def plan(lens, new, table, free, next_free, n_tokens):
             served += 1
         seq.append(have + served)
         cu_q.append(t0 + n)
-        cu_k.append(cu_k[-1] + have + served)
+        cu_k.append(cu_k[-1] + have + n)
     return table, slots, pos, rows, np.array(seq), np.array(cu_q), np.array(cu_k), at

@@ -272,3 +272,84 @@ def test_serving_steps(d, g, kind):
     ids = np.concatenate([used[b, :(int(at[b]) + 15) // 16] for b in range(B)])
     assert len(set(ids)) == len(ids) == int(out.next_free.item())  # no block twice
     assert cache.device_error() == 0 and plan.device_error() == 0 and rope.device_error() == 0
+
+
+@pytest.mark.parametrize("d,kind,columns,spare,cut,served", [
+    (128, "i4", 20, 3, 0, (30, 22, 2, 5)),   # the list runs out inside request 1; 2 and 3 have room in their blocks
+    (128, "f8", 20, 0, 0, (0, 6, 2, 5)),     # it is empty
+    (256, "i4", 4, 99, 0, (30, 38, 14, 5)),  # requests 1 and 2 outgrow their rows of the table
+    (128, "i4", 4, 4, 7, (30, 38, 14, 0)),   # they do, and fewer rows than tokens
+])
+def test_a_chunk_of_which_only_a_part_fits(d, kind, columns, spare, cut, served):
+    """The tokens of a chunk that got a slot attend to what lies before them, whatever of it was left out; the rest
+    comes with the next step."""
+    rng = np.random.default_rng((94, d, columns, spare))
+    h, hq, dt, blocks = 2, 8, torch.bfloat16, 64
+    make, oracle = (tq.TQI4Cache, i4) if kind == "i4" else (tq.TQF8Cache, f8)
+    cache = make(head_dim=d, num_kv_heads=h, num_q_heads=hq, num_blocks=blocks, max_batch=4, max_blocks_per_seq=20)
+    rope = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=h)
+    prompt = tq.TQPrompt(head_dim=d, num_kv_heads=h, num_q_heads=hq, max_batch=4, max_tokens=256)
+    lens, chunk = np.array([16, 26, 46 if columns > 4 else 50, 11]), np.array([30, 50, 20, 5])
+    free, table = rng.permutation(blocks), np.full((4, 20), -1)
+    at = 0
+    for b, n in enumerate((lens + 15) // 16):
+        table[b, :n] = free[at:at + n]
+        at += n
+    old = [rng.standard_normal((int(lens.sum()), h, d)) for _ in range(2)]
+    slots = np.concatenate([table[b, np.arange(n) // 16] * 16 + np.arange(n) % 16 for b, n in enumerate(lens)])
+    cache.store(*(_gpu(x, np.float32).to(dt) for x in old), _gpu(slots, np.int64))
+    wide = _gpu(table)
+    for step in range(2):
+        # (the second step has all the room it needs)
+        cols = columns if step == 0 else 20
+        plan = tq.TQPlan(max_batch=4, max_blocks_per_seq=cols)
+        n = int(chunk.sum()) - (cut if step == 0 else 0)
+        out, t = plan.outputs(4, n), wide[:, :cols].contiguous()
+        plan.step(_gpu(lens), _gpu(chunk), t, _gpu(free[at:at + spare] if step == 0 else free[at:]), _gpu([0]), out)
+        wide[:, :cols] = t
+        assert bool(plan.device_error()) == (step == 0)
+        got = _gpu(served) if step == 0 else _gpu(chunk)
+        assert torch.equal(out.seq_lens, _gpu(lens) + got)
+        q, k, v = _gpu(rng.standard_normal((n, hq + 2 * h, d)), np.float32).to(dt).split([hq, h, h], 1)
+        cq, ck = out.cu_q.cpu().numpy(), out.cu_k.cpu().numpy()
+        kr = torch.full((int(ck[-1]), h, d), float("nan"), dtype=dt, device="cuda")
+        vr = kr.clone()
+        cache.load(wide, _gpu(lens), out.cu_k, kr, vr)
+        qo, _, _ = rope.apply(q, k, out.positions, k_out=kr, v=v, v_out=vr, kv_rows=out.kv_rows)
+        att = prompt.attention(qo, kr, vr, out.cu_q, out.cu_k)
+        for b, m in enumerate(got.tolist()):
+            if m == 0:
+                continue
+            kb, vb = (x[ck[b]:ck[b] + lens[b] + m].double().cpu().numpy() for x in (kr, vr))
+            assert np.isfinite(kb).all() and np.isfinite(vb).all()
+            rows = qo[cq[b]:cq[b] + m].double().cpu().numpy()
+            ref, _, mag = f8.attention(rows, kb, vb, 1 / np.sqrt(d), np.arange(m) + int(lens[b]) + 1)
+            # (weights and outputs rounded to bf16: half a step is 2^-8 at most of either)
+            err = np.abs(att[cq[b]:cq[b] + m].double().cpu().numpy() - ref)
+            assert (err <= 2.0 ** -7 * mag + 2.0 ** -8 * np.abs(ref)).all(), (step, b, err.max())
+        fits = out.slot_mapping >= 0
+        assert int(fits.sum()) == int(got.sum())
+        cache.store(kr[out.kv_rows.clamp(min=0).long()], v, out.slot_mapping)
+        pages, tn = cache.pages().cpu().numpy(), wide.cpu().numpy()
+        for b, m in enumerate(got.tolist()):  # what the prompt saw is what is stored
+            if m == 0:
+                continue
+            x = oracle.rows(pages, tn[b], int(lens[b]) + m, d)[0]
+            new = kr[ck[b] + lens[b]:ck[b] + lens[b] + m].double().cpu().numpy()
+            assert np.array_equal(x[lens[b]:], oracle.values(*oracle.quantise(new)))
+        lens, chunk, at = out.seq_lens.cpu().numpy(), chunk - got.cpu().numpy(), at + int(out.next_free)
+    assert rope.device_error() == 0 and cache.device_error() == 0 and prompt.device_error() == 0
+
+
+def test_sums_of_lengths_beyond_an_int_are_cut_off():
+    """Two requests that fill their rows of the widest table; rows and positions behind 2^31 - 1 do not wrap."""
+    columns = 2 ** 26 - 1
+    table = torch.zeros((2, columns), dtype=torch.int32, device="cuda")
+    plan = tq.TQPlan(max_batch=2, max_blocks_per_seq=columns)
+    out, full = plan.outputs(2, 80), 16 * columns
+    plan.step(_gpu([full, full - 1]), _gpu([40, 40]), table, _gpu([]), _gpu([0]), out)
+    assert plan.device_error() == tq.TQ_DEVERR_SEQLEN
+    assert out.cu_q.tolist() == [0, 40, 80] and out.seq_lens.tolist() == [full, full]
+    assert out.cu_k.tolist() == [0, full + 40, 2 ** 31 - 1]
+    assert out.slot_mapping.tolist() == [-1] * 40 + [15] + [-1] * 39
+    assert out.kv_rows.tolist() == [-1] * 40 + [2 ** 31 - 1] + [-1] * 39

@@ -105,3 +105,13 @@ def test_bindings_check_before_any_call():
     with pytest.raises(ValueError):
         tq.tq_plan_step(None, tq.tq_plan_config(**PLAN), n, None, t, one, one, torch.zeros(2, dtype=torch.int64), n, n, n,
                         pos, pos, one)
+
+
+def test_oracle_plan_of_which_only_a_part_fits():
+    """Packed keys keep rows for tokens that got no slot: the last key stays that of the last token."""
+    table = np.array([[7, -1, -1], [3, -1, -1]])
+    t, s, p, r, n, cq, ck, at = serve.plan([14, 2], [9, 3], table, [], 0, 12)
+    assert np.array_equal(t, table) and at == 0
+    assert list(s) == [126, 127] + [-1] * 7 + [50, 51, 52] and list(p) == list(range(14, 23)) + [2, 3, 4]
+    assert list(r) == [14, 15] + [-1] * 7 + [25, 26, 27]
+    assert list(n) == [16, 5] and list(cq) == [0, 9, 12] and list(ck) == [0, 23, 28]

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     extern __shared__ int32_t sm[];
     // per request: first row, stored tokens, tokens served, its blocks' place in the list
     int32_t *s_cu = sm, *s_len = s_cu + a.batch + 1, *s_served = s_len + a.batch, *s_off = s_served + a.batch;
-    int32_t* s_row = s_off + a.batch;  // first row of packed keys
+    int32_t* s_row = s_off + a.batch;  // first row of packed keys (all new tokens have one, served or not)
     __shared__ int64_t s_scan[kPlanWarps][3];
     __shared__ bool s_last;
     const int tid = threadIdx.x;
@@ -87,15 +87,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         n = max((int64_t)0, n);
     };
     // Requests in chunks of one per thread.  First as if all rows and blocks sufficed: one
-    // sum of rows, blocks and lengths.  If they do not, again, one after the other: a
-    // request's rows depend on the rows before it, its blocks on its rows, and so on.
+    // sum of rows, blocks and keys.  If they do not, again, one after the other: a
+    // request's rows depend on the rows before it, its blocks on its rows.
     int64_t rows0 = 0, blocks0 = 0, keys0 = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int64_t len, n;
         request(b, len, n);
         const int64_t served = min(n, cap - len), want = ((len + served + 15) >> 4) - ((len + 15) >> 4);
-        int64_t x[3] = {n, want, len + served}, tot[3];
+        int64_t x[3] = {n, want, len + n}, tot[3];
         plan_scan(x, tot, s_scan);
         if (b < a.batch) {
             if (served < n) bad |= TQ_DEVERR_SEQLEN;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             s_len[b] = (int)len;
             s_served[b] = (int)served;
             s_off[b] = (int)min((int64_t)0x7FFFFFFF, blocks0 + x[1] - want);
-            s_row[b] = (int)(keys0 + x[2] - len - served);
+            s_row[b] = (int)min((int64_t)0x7FFFFFFF, keys0 + x[2] - len - n);
         }
         rows0 += tot[0], blocks0 += tot[1], keys0 += tot[2];
     }
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             const int b = b0 + tid;
             int64_t len, n;
             request(b, len, n);
-            int64_t x[1] = {n}, tot[1];
+            int64_t x[1] = {n}, tot[1], both[2];
             plan_scan(x, tot, s_scan);
             const int64_t first = min((int64_t)a.n_tokens, rows0 + x[0] - n);
             if (rows0 + x[0] > a.n_tokens) bad |= TQ_DEVERR_CHUNK;
@@ -124,24 +124,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             int64_t served = min(n, cap - len);
             const int64_t have = (len + 15) >> 4;
             const int64_t want = ((len + served + 15) >> 4) - have;
-            int64_t y[1] = {want};
-            plan_scan(y, tot, s_scan);
+            int64_t y[2] = {want, len + n};
+            plan_scan(y, both, s_scan);
             const int64_t off = blocks0 + y[0] - want;
-            blocks0 += tot[0];
+            blocks0 += both[0];
             if (off + want > avail) {
                 bad |= TQ_DEVERR_POOL;
                 served = min(served, 16 * (have + max((int64_t)0, avail - off)) - len);
             }
-            int64_t z[1] = {b < a.batch ? len + served : 0};
-            plan_scan(z, tot, s_scan);
             if (b < a.batch) {
                 s_cu[b] = (int)first;
                 s_len[b] = (int)len;
                 s_served[b] = (int)served;
                 s_off[b] = (int)min(off, (int64_t)0x7FFFFFFF);
-                s_row[b] = (int)(keys0 + z[0] - len - served);
+                s_row[b] = (int)min((int64_t)0x7FFFFFFF, keys0 + y[1] - len - n);
             }
-            keys0 += tot[0];
+            keys0 += both[1];
         }
     }
     const int rows = (int)min(rows0, (int64_t)a.n_tokens);
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             const int i = (int)t - s_cu[lo], len = s_len[lo];
             pos = len + i;
             if (i < s_served[lo]) {
-                row = s_row[lo] + pos;
+                row = (int)min((uint32_t)s_row[lo] + (uint32_t)pos, 0x7FFFFFFFu);
                 const int col = pos >> 4, have = (len + 15) >> 4;
                 int32_t* entry = a.table + (int64_t)lo * a.columns + col;
                 int id;
@@ -201,7 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     if (tid == 0) {
         a.cu_q[a.batch] = rows;
-        a.cu_k[a.batch] = (int)keys0;
+        a.cu_k[a.batch] = (int)min((int64_t)0x7FFFFFFF, keys0);
         *a.next_out = next + (int)min(blocks0, avail);
     }
 }
