@@ -362,3 +362,27 @@ def test_in_place_with_another_stride_is_refused():
     h.apply(q, k, p, q_out=q, k_out=own, kv_rows=p)
     torch.cuda.synchronize()
     assert h.device_error() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_frequencies_below_zero_are_as_exact_as_the_others(interleaved):
+    """The bound: less than 2^-32 of a turn is cut off, and half a unit of 2^-64 of a turn a position (2^-34 at the
+    farthest): 2^-29 together; fp32 rounds the reduced angle t by 2^-24 of itself, and a sine or cosine errs by two
+    units at most, 2^-22 of itself.  So small sines show the angle itself, which a frequency of 53 bits behind the
+    point would miss by up to 2^-20 at the farthest positions."""
+    rng = np.random.default_rng(85)
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 77, 1234567890, -2000000011], np.int32)
+    f = np.r_[0.3, 1e-3, 1e-6, 1e-9, 1e-12, 7e-16, 3e-16, 1e-17, 1e-30, 2.0 ** -54, 2.0 ** -60 * 6.28, 5.0,
+              np.exp(rng.uniform(-35, 2, 52))]
+    # (a pair's first element 1, its second 0: the outputs are cosines and sines)
+    pair = torch.tensor([1.0, 0.0], device="cuda")
+    q = (pair.repeat(64) if interleaved else pair.repeat_interleave(64)).expand(8, 1, 128).contiguous()
+    for sign in (1.0, -1.0):
+        h = tq.TQNormRope(head_dim=128, num_q_heads=1, num_kv_heads=1, inv_freq=sign * f, interleaved=interleaved, norm=0)
+        y = _np(h.apply(q, q, _gpu(pos))[0]).reshape(8, *((64, 2) if interleaved else (2, 64)))
+        c, s = (y[..., 0], y[..., 1]) if interleaved else (y[:, 0], y[:, 1])
+        t = serve.angles(pos, sign * f)
+        angle = 2.0 ** -29 + 2.0 ** -24 * np.abs(t)
+        assert (np.abs(c - np.cos(t)) <= angle + 2.0 ** -22).all(), sign
+        err = np.abs(s - np.sin(t)) / (angle + 2.0 ** -22 * np.abs(np.sin(t)))
+        assert (err <= 1).all(), (sign, f[err.max(0).argmax()], err.max())

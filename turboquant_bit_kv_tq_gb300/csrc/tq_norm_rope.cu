@@ -586,15 +586,17 @@ static tq_status norm_rope_check(const tq_norm_rope_config& c) {
 
 constexpr size_t kRopeTurnsAt = 16;
 
-// 2^64 f / (2 pi) modulo 2^64: the quotient in two doubles, 1 / 2 pi = hi + lo
+// 2^64 f / (2 pi) modulo 2^64, to the nearest: the quotient in two doubles, 1 / 2 pi = hi +
+// lo.  Of the magnitude, negated at the end: of a small negative quotient the part
+// above its floor would be rounded to 53 bits, or to 1.
 static uint64_t turns_of(double f) {
     constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
-    const double q = f * hi, rest = fma(f, hi, -q) + f * lo;
-    const double part = q - floor(q);  // exact, in [0, 1)
-    const uint64_t a = (uint64_t)(ldexp(part, 64));
-    const double r = ldexp(rest, 64);
-    if (!(fabs(r) < 0x1p62)) return a;  // (a frequency beyond 2^50: nothing left to keep)
-    return a + (uint64_t)(int64_t)nearbyint(r);
+    const double m = fabs(f), q = m * hi, rest = fma(m, hi, -q) + m * lo;
+    const double units = ldexp(q - floor(q), 64), whole = floor(units);  // exact, in [0, 2^64)
+    const double below = (units - whole) + ldexp(rest, 64);
+    uint64_t a = (uint64_t)whole;
+    if (fabs(below) < 0x1p62) a += (uint64_t)(int64_t)nearbyint(below);  // (a frequency beyond 2^50: nothing left to keep)
+    return f < 0.0 ? 0 - a : a;
 }
 
 }  // namespace tq
