@@ -1,6 +1,10 @@
 """The plan of a step on the GPU against its oracle (oracle/serve.py), entry by
 entry, and the plan in use: chunked prompts and a captured decode loop."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -10,6 +14,7 @@ from oracle import f8, i4, serve
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 NAMES = ("slot_mapping", "positions", "kv_rows", "seq_lens", "cu_q", "cu_k", "next_free")
 
 
@@ -353,3 +358,23 @@ def test_sums_of_lengths_beyond_an_int_are_cut_off():
     assert out.cu_k.tolist() == [0, full + 40, 2 ** 31 - 1]
     assert out.slot_mapping.tolist() == [-1] * 40 + [15] + [-1] * 39
     assert out.kv_rows.tolist() == [-1] * 40 + [2 ** 31 - 1] + [-1] * 39
+
+
+def test_batches_around_the_launch_limit_of_shared_memory():
+    """Sums of 2448 .. 2457 requests take up to 48 KB with what the kernel has beside them, and more with it; each size
+    in a process that has asked for no larger one."""
+    call = ("import numpy as np, torch, turboquant_bit_kv_tq_gb300 as tq\n"
+            "b = {}\n"
+            "plan = tq.TQPlan(max_batch=b, max_blocks_per_seq=2)\n"
+            "out = plan.outputs(b, b)\n"
+            "table = torch.arange(2 * b, dtype=torch.int32, device='cuda').view(b, 2)\n"
+            "lens = torch.arange(b, dtype=torch.int32, device='cuda') % 16 + 1\n"
+            "zero = torch.zeros(1, dtype=torch.int32, device='cuda')\n"
+            "plan.step(lens, None, table, torch.arange(2 * b, dtype=torch.int32, device='cuda'), zero, out)\n"
+            "n = int((lens == 16).sum())\n"
+            "assert plan.device_error() == 0 and int(out.next_free) == n\n"
+            "assert torch.equal(out.seq_lens, lens + 1) and torch.equal(out.positions, lens)\n"
+            "assert out.cu_k[-1] == (lens + 1).sum() and out.cu_q[-1] == b\n")
+    for b in (2436, 2447, 2448, 2457, 2458):
+        done = subprocess.run([sys.executable, "-c", call.format(b)], cwd=ROOT, capture_output=True, text=True)
+        assert done.returncode == 0, (b, done.stderr[-2000:])

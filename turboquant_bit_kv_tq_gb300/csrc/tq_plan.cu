@@ -31,6 +31,15 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32, kPlanMaxBatch = 8192, kPlanTokens = 256;
 
+// what a block keeps beside its sums
+struct PlanShared {
+    int64_t scan[kPlanWarps][3];
+    bool last;
+};
+// The launch limit without an opt-in is 48 KB of both together
+constexpr int kPlanOptIn = 47 * 1024;
+static_assert(sizeof(PlanShared) <= 1024 - 64, "shared memory beside the sums");
+
 // inclusive sums over the block's threads of N values; tot: those of all
 template <int N>
 __device__ __forceinline__ void plan_scan(int64_t (&x)[N], int64_t (&tot)[N], int64_t (*s)[3]) {
@@ -66,8 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     // per request: first row, stored tokens, tokens served, its blocks' place in the list
     int32_t *s_cu = sm, *s_len = s_cu + a.batch + 1, *s_served = s_len + a.batch, *s_off = s_served + a.batch;
     int32_t* s_row = s_off + a.batch;  // first row of packed keys (all new tokens have one, served or not)
-    __shared__ int64_t s_scan[kPlanWarps][3];
-    __shared__ bool s_last;
+    __shared__ PlanShared sh;
     const int tid = threadIdx.x;
     const int64_t cap = (int64_t)a.columns * 16;
     pdl_wait();  // (the launch overlaps the previous kernel's end)
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         request(b, len, n);
         const int64_t served = min(n, cap - len), want = ((len + served + 15) >> 4) - ((len + 15) >> 4);
         int64_t x[3] = {n, want, len + n}, tot[3];
-        plan_scan(x, tot, s_scan);
+        plan_scan(x, tot, sh.scan);
         if (b < a.batch) {
             if (served < n) bad |= TQ_DEVERR_SEQLEN;
             s_cu[b] = (int)min((int64_t)0x7FFFFFFF, rows0 + x[0] - n);
@@ -115,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             int64_t len, n;
             request(b, len, n);
             int64_t x[1] = {n}, tot[1], both[2];
-            plan_scan(x, tot, s_scan);
+            plan_scan(x, tot, sh.scan);
             const int64_t first = min((int64_t)a.n_tokens, rows0 + x[0] - n);
             if (rows0 + x[0] > a.n_tokens) bad |= TQ_DEVERR_CHUNK;
             rows0 += tot[0];
@@ -125,7 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             const int64_t have = (len + 15) >> 4;
             const int64_t want = ((len + served + 15) >> 4) - have;
             int64_t y[2] = {want, len + n};
-            plan_scan(y, both, s_scan);
+            plan_scan(y, both, sh.scan);
             const int64_t off = blocks0 + y[0] - want;
             blocks0 += both[0];
             if (off + want > avail) {
@@ -184,11 +192,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (a.in_place && gridDim.x > 1) {
         if (tid == 0) {
             __threadfence();
-            s_last = atomicAdd(a.cnt, 1u) == gridDim.x - 1;
-            if (s_last) *a.cnt = 0;
+            sh.last = atomicAdd(a.cnt, 1u) == gridDim.x - 1;
+            if (sh.last) *a.cnt = 0;
         }
         __syncthreads();
-        if (!s_last) return;
+        if (!sh.last) return;
     } else if (blockIdx.x > 0) {
         return;
     }
@@ -287,7 +295,7 @@ tq_status tq_plan_step(const tq_plan* p, const int32_t* lens, const int32_t* new
     tq_status st = device_sms(&sms);
     if (st != TQ_OK) return st;
     const int smem = (5 * batch + 1) * 4;
-    if (smem > 48 * 1024) {
+    if (smem > kPlanOptIn) {
         st = ensure_dynamic_smem((const void*)plan_kernel, (5 * kPlanMaxBatch + 1) * 4, "plan_kernel");
         if (st != TQ_OK) return st;
     }
