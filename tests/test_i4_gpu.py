@@ -630,3 +630,33 @@ def test_load_of_many_sequences(d, h, count, longest):
         want[:, starts[b]:starts[b] + n] = i4.rows(pages, table[b], n, d)
     assert np.array_equal(_np(ko), want[0]) and np.array_equal(_np(vo), want[1])
     assert c.device_error() == 0
+
+
+def test_pages_whose_memory_is_exchanged():
+    """The calls go by the cache tensor as it is now, not by the memory that it had when the handle was made."""
+    c, cfg = _cache(128, 2, 4, 8, 2, 4, fill=0), dict(dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(97)
+    k, v, q = (_gpu(rng.standard_normal((20, h, 128)), torch.bfloat16) for h in (2, 2, 4))
+    slots, table, lens = _gpu(np.arange(20)), _gpu(np.arange(8, dtype=np.int32).reshape(2, 4)), _gpu(np.int32([20, 0]))
+    old = c.cache.data  # (the same memory, which stays allocated)
+    c.cache.data = torch.zeros_like(old)
+    c.store(k, v, slots)
+    assert not old.any()
+    want = i4.store(np.zeros((8, 2, c.page_bytes), np.uint8), _np(k), _np(v), np.arange(20))
+    assert np.array_equal(c.pages().cpu().numpy(), want)
+    out = [torch.zeros((20, 2, 128), **cfg) for _ in range(2)]
+    c.load(table, lens, _gpu(np.int32([0, 20])), *out)
+    for x, y in zip(out, i4.rows(want, np.arange(4), 20, 128)):
+        assert np.array_equal(_np(x), torch.from_numpy(y).to(torch.bfloat16).double().numpy())
+    got = c.decode(q[:2], table, lens)
+    c.cache.data = old
+    old.copy_(torch.from_numpy(want.reshape(-1)))
+    assert torch.equal(c.decode(q[:2], table, lens), got) and bool(got[0].any())
+    for bad in (old[:-1], old.cpu(), torch.cat([old, old])[::2]):
+        c.cache.data = bad
+        for call in (lambda: c.store(k, v, slots), lambda: c.load(table, lens, lens, *out),
+                     lambda: c.decode(q[:2], table, lens)):
+            with pytest.raises(ValueError):
+                call()
+    c.cache.data = old
+    assert torch.equal(c.decode(q[:2], table, lens), got) and c.device_error() == 0

@@ -994,8 +994,8 @@ class TQI4Cache:
         elif (cache.dtype != torch.uint8 or cache.numel() != self.sizes["cache_bytes"] or not cache.is_contiguous()
               or cache.device != self.device):
             raise ValueError(f"cache must be {self.sizes['cache_bytes']} contiguous uint8 bytes on {self.device}")
-        # (the owner's own memory and sizes, looked at once, here)
-        self._cache, self._at, self._dev = cache, cache.data_ptr(), cache.get_device()
+        # (the owner's own sizes, looked at once, here)
+        self._cache, self._bytes, self._dev = cache, cache.numel(), cache.get_device()
         self._kv, self._q, self._d = self.cfg.num_kv_heads, self.cfg.num_q_heads, self.cfg.head_dim
         self._columns = self.cfg.max_blocks_per_seq
         self.workspace = torch.empty(self.sizes["workspace_bytes"], dtype=torch.uint8, device=self.device)
@@ -1014,19 +1014,26 @@ class TQI4Cache:
         """The cache as [num_blocks, H_kv, page_bytes]."""
         return self.cache.view(self.cfg.num_blocks, self.cfg.num_kv_heads, self.page_bytes)
 
+    def _pages(self):
+        """Pointer of the pages as they are now: the tensor may have been given other memory."""
+        c = self._cache
+        if c.get_device() != self._dev or c.numel() < self._bytes or not c.is_contiguous():
+            raise ValueError(f"cache must be {self._bytes} contiguous bytes on {self.device}")
+        return c.data_ptr()
+
     def store(self, k, v, slot_mapping, stream=None):
-        _i4_store(self.handle, self._kv, self._d, k, v, slot_mapping, self._at, self._dev, stream)
+        _i4_store(self.handle, self._kv, self._d, k, v, slot_mapping, self._pages(), self._dev, stream)
 
     def load(self, block_table, seq_lens, cu_out, k_out, v_out, stream=None):
-        _i4_load(self.handle, self._kv, self._d, self._columns, block_table, seq_lens, cu_out, k_out, v_out, self._at,
-                 self._dev, stream)
+        _i4_load(self.handle, self._kv, self._d, self._columns, block_table, seq_lens, cu_out, k_out, v_out,
+                 self._pages(), self._dev, stream)
         return k_out, v_out
 
     def decode(self, q, block_table, seq_lens, out=None, scale=0.0, stream=None, out_dtype=None):
         if out is None:
             out = _output(q, out_dtype or q.dtype, stream)
-        _i4_decode(self.handle, self._q, self._d, self._columns, q, self._at, self._dev, block_table, seq_lens, out,
-                   scale, stream)
+        _i4_decode(self.handle, self._q, self._d, self._columns, q, self._pages(), self._dev, block_table, seq_lens,
+                   out, scale, stream)
         return out
 
     def device_error(self, stream=None):
