@@ -378,3 +378,28 @@ def test_batches_around_the_launch_limit_of_shared_memory():
     for b in (2436, 2447, 2448, 2457, 2458):
         done = subprocess.run([sys.executable, "-c", call.format(b)], cwd=ROOT, capture_output=True, text=True)
         assert done.returncode == 0, (b, done.stderr[-2000:])
+
+
+def test_outputs_whose_memory_is_exchanged():
+    """A step writes its outputs where they are now, and refuses what they no longer can be."""
+    lens, new, table, free, nxt, tokens = _case(9, 30, 100, 20)
+    plan = tq.TQPlan(max_batch=30, max_blocks_per_seq=table.shape[1])
+    out = plan.outputs(30, tokens)
+    args = (_gpu(lens), _gpu(new), _gpu(table), _gpu(free), _gpu([nxt]))
+    want = serve.plan(lens, new, table, free, nxt, tokens)
+    old = [getattr(out, n).data for n in NAMES]  # (the same memory, which stays allocated)
+    for x, n in zip(old, NAMES):
+        x.fill_(-99)
+        getattr(out, n).data = torch.full((x.shape[0] + 3,), -98, dtype=x.dtype, device="cuda")[:x.shape[0]]
+    plan.step(*args, out)
+    assert plan.device_error() == 0 and all(bool((x == -99).all()) for x in old)
+    _same((0, args[2].cpu().numpy(), [getattr(out, n).cpu().numpy() for n in NAMES]), want)
+    for x, n in zip(old, NAMES):
+        good, other = getattr(out, n).data, torch.float32 if x.dtype != torch.int64 else torch.int32
+        for bad in [x[1:], x.cpu(), x.to(other)] + [torch.cat([x, x])[::2]] * (x.shape[0] > 1):
+            getattr(out, n).data = bad
+            with pytest.raises((ValueError, TypeError)):
+                plan.step(*args, out)
+        getattr(out, n).data = good
+    plan.step(_gpu(lens), *args[1:], out)
+    _same((0, args[2].cpu().numpy(), [getattr(out, n).cpu().numpy() for n in NAMES]), want)

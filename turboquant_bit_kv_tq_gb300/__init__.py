@@ -1229,7 +1229,7 @@ def tq_plan_get_device_error(handle, stream=None):
 class TQPlanStep:
     """The tensors that a plan's step writes, for ``batch`` requests and ``tokens``
     rows: slot_mapping, positions, kv_rows, seq_lens, cu_q, cu_k, next_free.  They are
-    its own, so that a step need not look at them again."""
+    its own, so that a step looks at them again only where their memory is another."""
 
     _NAMES = ("slot_mapping", "positions", "kv_rows", "seq_lens", "cu_q", "cu_k", "next_free")
 
@@ -1240,9 +1240,18 @@ class TQPlanStep:
         with torch.cuda.stream(stream):
             made = [torch.empty(n, dtype=torch.int32 if i else torch.int64, device=device)
                     for i, n in enumerate(sizes)]
-        self._made = dict(zip(self._NAMES, made))
-        self._at = (tokens,) + tuple(t.data_ptr() for t in made)
+        self._made, self._tensors, self._sizes = dict(zip(self._NAMES, made)), made, sizes
+        self._at = [tokens] + [t.data_ptr() for t in made]
         self._of = (batch, made[0].get_device())
+
+    def _memory(self):
+        """The number of rows, then the tensors' pointers as they are now."""
+        at = [self._sizes[0]] + [t.data_ptr() for t in self._tensors]
+        if at != self._at:
+            for name, t, n in zip(self._NAMES, self._tensors, self._sizes):
+                _index(t, name, _TORCH.int64 if name == "slot_mapping" else _TORCH.int32, n, self._of[1])
+            self._at = at
+        return at
 
     slot_mapping = property(lambda self: self._made["slot_mapping"])
     positions = property(lambda self: self._made["positions"])
@@ -1283,7 +1292,7 @@ class TQPlan:
             None if new_lens is None else _index(new_lens, "new_lens", i32, b, dev), b,
             _index(free_blocks, "free_blocks", i32, 0, dev), free_blocks.numel(),
             _index(next_free, "next_free", i32, 1, dev), _table(block_table, b, self._columns, dev),
-            *out._at, _launch_stream(stream, dev))
+            *out._memory(), _launch_stream(stream, dev))
         if st:
             raise TQError(st, "tq_plan_step")
         return out
