@@ -746,7 +746,7 @@ tq_status tq_plan_destroy(tq_plan* plan);
  *   tokens   packed, request by request: token i of request b is row cu_q[b] + i, with
  *            position L + i, slot table[b][(L + i) / 16] * 16 + (L + i) % 16, and row
  *            cu_k[b] + L + i of packed keys (tq_f8_load's and tq_norm_rope's rows,
- *            tq_prompt_attention's cu_k)
+ *            tq_prompt_attention's cu_k); positions and rows cut off at 2^31 - 1
  *   lengths  seq_lens[b] = L + n; cu_q, cu_k [batch + 1]: sums of n and of L + n (cut
  *            off at 2^31 - 1); *next_free_out = *next_free + the blocks taken
  * lens, new_lens   device int32 [batch]

@@ -403,3 +403,16 @@ def test_outputs_whose_memory_is_exchanged():
         getattr(out, n).data = good
     plan.step(_gpu(lens), *args[1:], out)
     _same((0, args[2].cpu().numpy(), [getattr(out, n).cpu().numpy() for n in NAMES]), want)
+
+
+def test_positions_beyond_an_int_are_cut_off():
+    """Tokens behind the end of the widest row of a table, which get no slot."""
+    columns = 2 ** 27 - 1
+    table = torch.zeros((1, columns), dtype=torch.int32, device="cuda")
+    plan = tq.TQPlan(max_batch=1, max_blocks_per_seq=columns)
+    out, full = plan.outputs(1, 40), 16 * columns
+    plan.step(_gpu([full - 8]), _gpu([40]), table, _gpu([]), _gpu([0]), out)
+    assert plan.device_error() == tq.TQ_DEVERR_SEQLEN and out.seq_lens.tolist() == [full]
+    assert out.positions.tolist() == [min(full - 8 + i, 2 ** 31 - 1) for i in range(40)]
+    assert out.slot_mapping.tolist() == [8 + i for i in range(8)] + [-1] * 32
+    assert out.kv_rows.tolist() == [full - 8 + i for i in range(8)] + [-1] * 32

@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 else hi = mid;
             }
             const int i = (int)t - s_cu[lo], len = s_len[lo];
-            pos = len + i;
+            pos = (int)min((uint32_t)len + (uint32_t)i, 0x7FFFFFFFu);  // (far behind the widest row's end)
             if (i < s_served[lo]) {
                 row = (int)min((uint32_t)s_row[lo] + (uint32_t)pos, 0x7FFFFFFFu);
                 const int col = pos >> 4, have = (len + 15) >> 4;
