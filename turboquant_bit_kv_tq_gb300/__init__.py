@@ -1277,7 +1277,8 @@ class TQPlan:
             self.handle = tq_plan_create(self.cfg, self.workspace)
 
     def outputs(self, batch, tokens, stream=None):
-        """Tensors for ``step``; they can be used again from step to step."""
+        """Tensors for ``step``; they can be used again from step to step.  Nothing is in them yet: where a
+        step is to read its lengths and list entry from them, they are set first."""
         return TQPlanStep(batch, tokens, self.device, stream)
 
     def step(self, lens, new_lens, block_table, free_blocks, next_free, out, stream=None):
