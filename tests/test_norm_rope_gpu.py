@@ -386,3 +386,35 @@ def test_frequencies_below_zero_are_as_exact_as_the_others(interleaved):
         assert (np.abs(c - np.cos(t)) <= angle + 2.0 ** -22).all(), sign
         err = np.abs(s - np.sin(t)) / (angle + 2.0 ** -22 * np.abs(np.sin(t)))
         assert (err <= 1).all(), (sign, f[err.max(0).argmax()], err.max())
+
+
+def test_rows_behind_two_to_the_31_elements():
+    """Rows that differ, with positions of their own, at the ends and where an element's offset passes 2^31 (and 2^32
+    bytes); outputs in memory of their own, the others' too."""
+    n, hq, hk, d = 70000, 250, 1, 128
+    row = hq * d
+    q, out = (torch.zeros((n, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, k_out = (torch.zeros((n, hk, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    edge = 2 ** 31 // row
+    some = np.concatenate([np.arange(x - 2, x + 3) for x in (2, n - 3 - edge, edge // 2, edge, n - 3)])
+    rng = np.random.default_rng(86)
+    at, pos = _gpu(some), torch.zeros(n, dtype=torch.int32, device="cuda")
+    q[at] = _gpu(rng.standard_normal((len(some), hq, d)), torch.bfloat16)
+    k[at] = _gpu(rng.standard_normal((len(some), hk, d)), torch.bfloat16)
+    p = rng.integers(1, 1 << 20, len(some)).astype(np.int32)
+    pos[at] = _gpu(p)
+    h = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=hk)
+    out.fill_(7)
+    h.apply(q, k, pos, q_out=out, k_out=k_out)
+    f, eps = serve.powers(1e4, 128), float(np.float32(1e-6))
+    _check(out[at], q[at], None, p, f, eps)
+    _check(k_out[at], k[at], None, p, f, eps)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert not bool((out.amax((1, 2)) != 0)[rest].any()) and not bool((out.amin((1, 2)) != 0)[rest].any())
+    # keys from the last row to the first and back: every row goes where it is sent
+    rows = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    back = torch.zeros_like(k_out)
+    h.apply(q, k, pos, q_out=q, k_out=back, kv_rows=rows)
+    assert torch.equal(back.flip(0), k_out) and torch.equal(q, out)
+    assert h.device_error() == 0
