@@ -10,6 +10,7 @@ import pytest
 
 import turboquant_bit_kv_tq_gb300 as tq
 from oracle import f8, i4, serve
+from turboquant_bit_kv_tq_gb300 import workloads as wl
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -416,3 +417,50 @@ def test_positions_beyond_an_int_are_cut_off():
     assert out.positions.tolist() == [min(full - 8 + i, 2 ** 31 - 1) for i in range(40)]
     assert out.slot_mapping.tolist() == [8 + i for i in range(8)] + [-1] * 32
     assert out.kv_rows.tolist() == [full - 8 + i for i in range(8)] + [-1] * 32
+
+
+def test_decode_steps_over_the_rotated_codebooks_pages():
+    """Plan, norm with rotation, store and decode of TurboQuant's own pages, which take contiguous rows: norm with
+    rotation's outputs, the values' among them, out of a fused projection.  A captured step, bit for bit the calls on
+    plain copies of the same rows with the oracle's slots."""
+    w = wl.scaled(wl.config("llama8b_gqa4_b16_8k"), q_heads=8, kv_heads=2, batch=3)
+    rng = np.random.default_rng(95)
+    B, cap, hq, h, d, dt = 3, 6, 8, 2, 128, torch.bfloat16
+    caches = [tq.TQCache(**wl.cache_config_kwargs(w, num_blocks=20, max_blocks=cap, max_batch=B, split_blocks=2))
+              for _ in range(2)]
+    rope = tq.TQNormRope(head_dim=d, num_q_heads=hq, num_kv_heads=h)
+    plan = tq.TQPlan(max_batch=B, max_blocks_per_seq=cap)
+    out = plan.outputs(B, B + 2)  # a padded batch: the rows behind the last token are stored nowhere
+    out.seq_lens.copy_(_gpu([0, 0, 0]))
+    out.next_free.zero_()
+    host, free = np.full((B, cap), -1), rng.permutation(20)
+    table, list_ = _gpu(np.zeros((B, cap))), _gpu(free)
+    qkv = torch.zeros((B + 2, hq + 2 * h, d), dtype=dt, device="cuda")
+    q, k, v = qkv.split([hq, h, h], 1)
+    to = [torch.zeros((B + 2, n, d), dtype=dt, device="cuda") for n in (hq, h, h)]
+    att = torch.zeros((B, hq, d), device="cuda")
+
+    def step():
+        plan.step(out.seq_lens, None, table, list_, out.next_free, out)
+        rope.apply(q, k, out.positions, q_out=to[0], k_out=to[1], v=v, v_out=to[2])
+        caches[0].store(to[1], to[2], out.slot_mapping)
+        caches[0].decode(to[0][:B], table, out.seq_lens, out=att)
+
+    step()  # (loads and sets up; its tokens, zeros, are written over)
+    out.seq_lens.zero_()
+    out.next_free.zero_()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    lens, nxt = [0] * B, 0
+    for _ in range(40):
+        qkv.copy_(_gpu(rng.standard_normal(qkv.shape), np.float32))
+        graph.replay()
+        host, slots, pos, _, lens, _, _, nxt = serve.plan(lens, [1] * B, host, free, nxt, B + 2)
+        qo, ko = rope.apply(q.contiguous(), k.contiguous(), _gpu(pos))
+        caches[1].store(ko[:B].contiguous(), v[:B].contiguous(), _gpu(slots[:B], np.int64))
+        want = caches[1].decode(qo[:B].contiguous(), _gpu(np.maximum(host, 0)), _gpu(lens))
+        assert torch.equal(att, want) and bool(torch.isfinite(att).all())
+    assert torch.equal(caches[0].cache, caches[1].cache)
+    assert all(c.device_error() == 0 for c in caches) and plan.device_error() == 0 and rope.device_error() == 0
