@@ -506,8 +506,9 @@ tq_status tq_f8_load(const tq_f8_cache* cache, const void* cache_buf, const int3
  * half of one counts as 0.
  * A query with an infinity or a NaN gets NaN.  1 <= batch <= max_batch.  One
  * launch of a fixed grid: the caches' pages are dealt out evenly whatever the
- * lengths, and the last block to finish a (sequence, KV head) joins its parts
- * in a fixed order, so results do not change from run to run.
+ * lengths (many short sequences by whole (sequence, KV head)s), and the last
+ * block to finish a (sequence, KV head) joins its parts in a fixed order, so
+ * results do not change from run to run.
  */
 tq_status tq_f8_decode_attention(const tq_f8_cache* cache, const void* q, int q_dtype, int64_t q_stride,
                                  const void* cache_buf, const int32_t* block_table, const int32_t* seq_lens,
@@ -641,8 +642,14 @@ tq_status tq_i4_load(const tq_i4_cache* cache, const void* cache_buf, const int3
 
 /*
  * Decode attention over the 4-bit cache, one new query per sequence: arguments,
- * definition, limits and order of the sums as for tq_f8_decode_attention.  The
- * products run on 16-bit operands that hold code times scale exactly.
+ * definition and limits as for tq_f8_decode_attention, and its rule for the
+ * operands: these hold code times scale exactly; with 16-bit q and out the
+ * probabilities (times their values' exponents) are one fp16 number each, rounded
+ * once, and where q or out is F32 two.  Pages are dealt out by all lengths of the
+ * batch: where runs are short they keep to a (sequence, KV head), or such go whole
+ * to a block or a warp; longer ones are even.  So a sequence's sums, joined in a
+ * fixed order, come out the same from run to run, but their last bits may differ
+ * with the lengths beside it.
  */
 tq_status tq_i4_decode_attention(const tq_i4_cache* cache, const void* q, int q_dtype, int64_t q_stride,
                                  const void* cache_buf, const int32_t* block_table, const int32_t* seq_lens,
@@ -675,8 +682,9 @@ tq_status tq_norm_rope_sizes(const tq_norm_rope_config* cfg, size_t* workspace_b
 /*
  * Make a handle that records workspace_dev (>= workspace_bytes, 16-byte aligned)
  * and writes the turns per position of its pairs there.  inv_freq: host double
- * [rot_dim / 2], radians per position (scaled variants), or NULL for the powers
- * of cfg->base.  Synchronises `stream` (set-up only).  Calls of one handle may
+ * [rot_dim / 2], radians per position (scaled variants), of either sign, or NULL
+ * for the powers of cfg->base; up to 2^44 of them are kept to half of 2^-64 of a
+ * turn.  Synchronises `stream` (set-up only).  Calls of one handle may
  * overlap on the GPU: nothing but the error word is written.
  */
 tq_status tq_norm_rope_create(const tq_norm_rope_config* cfg, const double* inv_freq, void* workspace_dev,
@@ -751,7 +759,8 @@ tq_status tq_plan_destroy(tq_plan* plan);
  *            off at 2^31 - 1); *next_free_out = *next_free + the blocks taken
  * lens, new_lens   device int32 [batch]
  * free_blocks      device int32 [num_free]; ids are passed on unchecked, but a
- *                  token whose block id is negative gets slot -1
+ *                  token whose block id is negative gets slot -1 (and counts as
+ *                  stored: the block has been taken)
  * block_table      device int32 [batch][max_blocks_per_seq], other entries left as they were
  * slot_mapping     device int64 [num_tokens]; positions, kv_rows device int32
  *                  [num_tokens].  Rows behind the last token (a padded batch) get slot

@@ -204,8 +204,8 @@ static tq_status launch_i4_store(const I4StoreArgs& a, cudaStream_t s) {
 // The pages of all sequences, in the order (sequence, page, KV head), are dealt out to
 // the warps of a fixed grid; a warp reads one page and writes its 16 rows of keys and
 // of values, a lane 16 elements (one scale) at a time.  Bound by memory, four fifths of it
-// writes: 16 sequences of up to 16384 tokens, 8 heads, d = 128, to bf16: 109 us, 6510 GB/s
-// (96% of a plain copy); with 16-byte stores, half a sector each, 129.  (Sequence by sequence
+// writes: 16 sequences of up to 16384 tokens, 8 heads, d = 128, to bf16: 110 us, 6430 GB/s
+// (95% of a plain copy); with 16-byte stores, half a sector each, 129.  (Sequence by sequence
 // the walk alone took every warp a quarter of a microsecond each: 100 x up to 700 53 us, now 33.)
 struct I4LoadArgs {
     const uint8_t* cache;

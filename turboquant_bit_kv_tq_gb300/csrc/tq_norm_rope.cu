@@ -304,7 +304,10 @@ constexpr int kRopePieceBytes = 13312;  // of a stage: 5 blocks of 3 stages shar
 // This kernel is taken from so many pieces per SM and bytes of a piece on.  32/8 heads,
 // d = 128, bf16 (12 KB): 152 tokens 3.3 us here, 3.0 by the other one; 304 3.6, 3.6; 1216
 // 6.6, 7.6; 4864 22.0, 27.1.  64/8 heads (2 x 10 KB): 152 3.4, 3.5; 4864 33.8, 41.2.
-// 8/1 heads (2.5 KB): 1216 4.4, 3.8; 2432 6.6, 5.5; 4864 10.9, 11.3.
+// Few heads: the other one wins up to about 9000 tokens of 8/1 heads (2.5 KB: 1216 4.6, 3.5;
+// 4864 11.2, 10 to 11.5; 9000 21.0, 21.0; 65536 130, 137), at d = 256 (5 KB) up to about 4000
+// (2432 8.5, 7.3; 4864 16.3, 18.6; 9000 26.9, 29.0; 65536 166, 190).  The rule goes by bytes
+// alone: many tokens of few heads are 5 to 14% slower so.
 constexpr int kRopeBulkFrom = 2, kRopeBulkLeast = 6144;
 
 __device__ __forceinline__ uint64_t rope_pack(float x, float y) {

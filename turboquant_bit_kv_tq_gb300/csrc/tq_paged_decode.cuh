@@ -38,10 +38,13 @@
 // caches add bytes at 6.3 to 6.7 TB/s; the rest is about 15 us a call: the first pages are
 // under way after 2 us; blocks with equal runs end up to 12 us apart, arriving takes
 // 1.5 and the last join up to 5.
-// 4 bits (1.125 d + 2 bytes): 40, 82 and 51 us, 3.8, 4.7 and 3.3 TB/s.  Bound by the
-// instructions that turn codes into operands: a page of d = 128 takes 335 a warp, 150 of
-// them masks and multiply-adds of codes, at 60% of the issue slots (a fourth block per SM
-// issues no more).  Without any of the conversions 16 x 8192 takes 35 us.
+// 4 bits (1.125 d + 2 bytes): 40, 82 and 51 us, 3.8, 4.7 and 3.3 TB/s; a copy's time
+// would be 23, 56 and 25.  The conversion of codes is a part of it: a page of d = 128 takes
+// 335 instructions a warp, 150 of them masks and multiply-adds of codes, but without any
+// 16 x 8192 still takes 35 us.  The rest is latency: start, equal runs that end 8 us apart
+// (not known why) and joins, some 12 us; and within a warp's step scores, exchange,
+// exponentials, transposes and value products follow one another, so that 56 to 60% of the
+// issue slots are busy whether 8, 12 or 16 warps share an SM.
 
 #pragma once
 
@@ -264,7 +267,10 @@ constexpr int kPagedRun = 16;  // pages of a run, on average, at least (two step
 // 21.8, 16.8; 4 x 16384 (77 pages) 29.1, 27.0; 8 x 8192 (83) 27.5, 27.6; 16 x 4096 (100)
 // 28.8, 29.9; 1 x 131072 (147) 43.2, 44.6.  Many units: 64 x up to 300 22.1, 13.3; 100 x up
 // to 700 28.2, 24.7; 64 x 1000 30.3, 31.1; 100 x up to 1500 (94) 35.1, 36.4; d = 256, fp32: 80 x
-// up to 700 35.2, 30.3; 160 x up to 1000 (63) 46.1, 48.2.
+// up to 700 35.2, 30.3; 160 x up to 1000 (63) 46.1, 48.2.  The first of the two rules with
+// 16 heads a unit, d = 128, bf16 (128/8 heads): 4 x up to 700 26.2, 12.2; 4 x up to 8000 24.8,
+// 20.2; 8 x 8192 36.4, 36.2; 4 x 16384 35.6, 35.9; d = 256 (32/4): bf16 8 x 8192 29.4, 26.9; 4 x
+// 16384 32.1, 28.0; fp32 33.0, 31.4; 36.4, 32.2; d = 256, 16 heads (64/4), bf16: 43.8, 39.6; 49.1, 41.3.
 constexpr int kPagedWhole = 88;
 constexpr int kPagedSoloPages = 16;  // a warp takes units of up to this many pages alone, whatever its share
 // The parts of up to kPagedJoin blocks are joined by the last of them; of more, by the
